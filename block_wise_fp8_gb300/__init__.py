@@ -29,6 +29,7 @@ __all__ = [
     "fp8bq_ue8m0_gemm", "fp8bq_ue8m0_linear",
     "OP_GROUPED_GEMM", "fp8bq_grouped_gemm", "fp8bq_grouped_gemm_masked",
     "fp8bq_check_scales",
+    "OP_LORA_ADD", "fp8bq_qk_norm_rope", "fp8bq_lora_group", "fp8bq_lora_add",
     "library_path",
     "fp8bq_version", "fp8bq_status_string", "fp8bq_last_cuda_error",
     "fp8bq_workspace_bytes", "fp8bq_workspace_init", "fp8bq_poll_status",
@@ -44,7 +45,7 @@ __all__ = [
 SCALE_ROW_MAJOR, SCALE_COL_MAJOR = 0, 1
 (OP_GEMM, OP_LINEAR, OP_MX_GEMM, OP_MX_LINEAR, OP_STATIC_GEMM,
  OP_STATIC_LINEAR, OP_CHANNEL_GEMM, OP_CHANNEL_LINEAR, OP_UE8M0_GEMM,
- OP_UE8M0_LINEAR, OP_GROUPED_GEMM) = range(11)
+ OP_UE8M0_LINEAR, OP_GROUPED_GEMM, OP_LORA_ADD) = range(12)
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024      # FP8BQ_NOALLOC_SCRATCH_BYTES
 
 STATUS_NAMES = {0: "FP8BQ_OK", 1: "FP8BQ_ERR_NULL", 2: "FP8BQ_ERR_SHAPE",
@@ -116,6 +117,11 @@ def _load():
                                       P]),
         "fp8bq_quant_weight_block": (I32, [P, I64, I64, I64, P, P, P]),
         "fp8bq_absmax_scale": (I32, [P, I64, I64, I64, P, P]),
+        "fp8bq_qk_norm_rope": (I32, [P, I64, I64, I64, P, I64, I64, I64, P, P, F32, P, I64, I64,
+                                     P, I32, I32, P, I64, I64, P, I64, I64, I64, I64, P]),
+        "fp8bq_lora_group": (I32, [P, I64, I64, P, P, P]),
+        "fp8bq_lora_add": (I32, [P, I64, P, P, P, P, P, P, P, I64, P, I64, I64, I64, I64, I64,
+                                 I64, P, SZ, P]),
         "fp8bq_e4m3_from_bits": (I32, [ctypes.c_uint32, I64, P, P]),
     }
     for name, (res, args) in sigs.items():
@@ -193,7 +199,8 @@ class _Spec:
 
     kind "contig": contiguous with exactly `shape` (or `numel` elements when
     shape is None); kind "rows": 2-D [shape] with unit stride in the last
-    dimension and any row pitch (the C call takes the pitch)."""
+    dimension and any row pitch (the C call takes the pitch); kind "heads": 3-D
+    [shape] with unit stride in the last dimension and any other strides."""
     __slots__ = ("name", "t", "dtypes", "shape", "numel", "kind", "optional")
 
     def __init__(self, name, t, dtypes, shape=None, numel=None, kind="contig", optional=False):
@@ -224,6 +231,12 @@ def _validate(what: str, specs, stream=None):
             if t.numel() and (t.stride(1) != 1 or t.stride(0) < t.shape[1]):
                 raise ValueError(f"{what}: {sp.name} needs unit stride in its last dimension "
                                  f"and a row pitch of at least {t.shape[1]}")
+        elif sp.kind == "heads":
+            if tuple(t.shape) != sp.shape:
+                raise ValueError(f"{what}: {sp.name} must have shape {sp.shape}, "
+                                 f"not {tuple(t.shape)}")
+            if t.numel() and (t.stride(2) != 1 or min(t.stride()) < 0):
+                raise ValueError(f"{what}: {sp.name} needs unit stride in its last dimension")
         else:
             if sp.shape is not None and tuple(t.shape) != sp.shape:
                 raise ValueError(f"{what}: {sp.name} must have shape {sp.shape}, "
@@ -579,6 +592,87 @@ def fp8bq_grouped_gemm_masked(q, s_x, w, s_w, masked_m, y, ws, s_layout: int = S
                                           _ptr(masked_m), E, max_m, _ptr(y), N, K, _ptr(ws),
                                           _nbytes(ws), _stream(stream)),
            "fp8bq_grouped_gemm_masked")
+
+
+# ---------------------------------------------------------------- beside the linears
+
+def _heads(t, name):
+    """(tokens, heads, head size) of a 3-D argument whose shape sets the call's sizes."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D tensor [tokens, heads, head size]")
+    return (int(v) for v in t.shape)
+
+
+def _strides(t):
+    return (0, 0) if t is None else (t.stride(0), t.stride(1))
+
+
+def fp8bq_qk_norm_rope(q, k, q_gamma, k_gamma, table, positions, q_out, k_out, eps: float = 1e-6,
+                       interleaved: bool = False, stream=None):
+    """RMSNorm of each head of q [T, HQ, D] and k [T, HK, D] (any token and head
+    strides: slices of the packed QKV rows) and the rotary embedding, into
+    q_out and k_out (which may be q and k).  A gamma of None leaves out the
+    norm; k (and k_out) may be None.  table: FP32 [P, rot], a position's
+    cosines, then its sines; positions: int32 or int64 [T]."""
+    T, HQ, D = _heads(q, "q")
+    HK = 0
+    if k is not None:
+        _, HK, _ = _heads(k, "k")
+    P, rot = _mat(table, "table")
+    _validate("fp8bq_qk_norm_rope", [
+        _Spec("q", q, _BF16, (T, HQ, D), kind="heads"),
+        _Spec("k", k, _BF16, (T, HK, D), kind="heads", optional=True),
+        _Spec("q_gamma", q_gamma, _BF16, numel=D, optional=True),
+        _Spec("k_gamma", k_gamma, _BF16, numel=D, optional=True),
+        _Spec("table", table, _F32, (P, rot)),
+        _Spec("positions", positions, (torch.int32, torch.int64), (T,)),
+        _Spec("q_out", q_out, _BF16, (T, HQ, D), kind="heads"),
+        _Spec("k_out", k_out, _BF16, (T, HK, D), kind="heads", optional=k is None)], stream)
+    if k is None and k_out is not None:
+        raise ValueError("fp8bq_qk_norm_rope: k_out without k")
+    _check(_lib.fp8bq_qk_norm_rope(
+        _ptr(q), *_strides(q), HQ, _ptr(k), *_strides(k), HK, _ptr(q_gamma), _ptr(k_gamma),
+        float(eps), _ptr(table), P, rot, _ptr(positions),
+        32 if positions.dtype == torch.int32 else 64, int(interleaved), _ptr(q_out),
+        *_strides(q_out), _ptr(k_out), *_strides(k_out), T, D, _stream(stream)),
+        "fp8bq_qk_norm_rope")
+
+
+def fp8bq_lora_group(ids, order, offsets, stream=None):
+    """Token indices sorted by adapter (stable) into order [M], and each
+    adapter's places in it into offsets [L+1]; ids outside [0, L) come last."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise ValueError("ids must be a 1-D tensor")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a 1-D tensor of L + 1 elements")
+    M, L = ids.numel(), offsets.numel() - 1
+    _validate("fp8bq_lora_group", [
+        _Spec("ids", ids, _I32, (M,)), _Spec("order", order, _I32, (M,)),
+        _Spec("offsets", offsets, _I32, (L + 1,))], stream)
+    _check(_lib.fp8bq_lora_group(_ptr(ids), M, L, _ptr(order), _ptr(offsets), _stream(stream)),
+           "fp8bq_lora_group")
+
+
+def fp8bq_lora_add(x, a, b, scales, order, offsets, base, y, ws, ranks=None, stream=None):
+    """y = base + scales[i] * b[i] @ (a[i] @ x[t]) with each token's adapter i
+    (a [L, R, K], b [L, N, R]; order and offsets from fp8bq_lora_group); y may
+    be base.  Workspace: new_workspace(OP_LORA_ADD, M, R, K)."""
+    M, K = _mat(x, "x")
+    N = _mat(y, "y")[1]
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError("a must be a 3-D tensor [L, R, K]")
+    L, R = int(a.shape[0]), int(a.shape[1])
+    _validate("fp8bq_lora_add", [
+        _Spec("x", x, _BF16, (M, K), kind="rows"),
+        _Spec("a", a, _BF16, (L, R, K)), _Spec("b", b, _BF16, (L, N, R)),
+        _Spec("scales", scales, _F32, (L,)), _Spec("ranks", ranks, _I32, (L,), optional=True),
+        _Spec("order", order, _I32, (M,)), _Spec("offsets", offsets, _I32, (L + 1,)),
+        _Spec("base", base, _BF16, (M, N), kind="rows"),
+        _Spec("y", y, _BF16, (M, N), kind="rows"), _ws(ws)], stream)
+    _check(_lib.fp8bq_lora_add(
+        _ptr(x), _ld(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(ranks), _ptr(order), _ptr(offsets),
+        _ptr(base), _ld(base), _ptr(y), _ld(y), M, N, K, L, R, _ptr(ws), _nbytes(ws),
+        _stream(stream)), "fp8bq_lora_add")
 
 
 # ---------------------------------------------------------------- residual add + RMSNorm

@@ -80,6 +80,47 @@ void launch_check_scales(const float *s, int64_t n, unsigned long long *out, int
 // (i < n); `codes` 8-byte aligned.
 void launch_e4m3_bits(uint32_t first, int64_t n, uint8_t *codes, int num_sms, cudaStream_t st);
 
+// ---------------------------------------------------------------- beside the linears
+
+// RMSNorm of query and key heads and the rotary embedding (strides in elements)
+struct RopeArgs {
+  const uint16_t *q, *k;
+  uint16_t *qo, *ko;
+  int64_t q_ts, q_hs, k_ts, k_hs;      // token and head strides of the inputs
+  int64_t qo_ts, qo_hs, ko_ts, ko_hs;  // and of the outputs
+  const uint16_t *gq, *gk;             // gains [D], or nullptr: no norm
+  const float *table;                  // [P][rot]: rot/2 cosines, rot/2 sines
+  const void *pos;                     // [T] int32 or int64
+  int64_t T, P;
+  int HQ, HK, D, rot, pos_is64, interleaved;
+  float eps;
+  int chunks, chunk_heads;  // set by the launcher: heads of a token a warp walks
+};
+cudaError_t launch_qk_norm_rope(RopeArgs a, int num_sms, cudaStream_t st);
+
+// Low-rank adapters (lora.cu)
+constexpr int kMaxAdapters = 512;
+constexpr int kMaxLoraRank = 128;
+struct LoraArgs {
+  const uint16_t *x, *a, *b, *base;
+  uint16_t *y;
+  int64_t ldx, ldbase, ldy;
+  const float *scales;
+  const int *order, *offsets, *ranks;  // ranks may be nullptr: every rank is R
+  float *part;                         // [splits][M][R]
+  int64_t M;
+  int L, R, K, N;
+  int splits, kb_split;  // K blocks of 64: split s takes kb_split of them
+  int ngroups;           // 32-column groups an expand CTA walks
+  int copy_rest;         // y is not base: rows without an adapter are copied
+};
+// K splits of the first product (a pure function, so that the workspace's size
+// and the launch agree)
+int lora_splits(int64_t M, int64_t K, int *kb_split);
+cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st);
+cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int *offsets,
+                              cudaStream_t st);
+
 // ---------------------------------------------------------------- GEMM
 
 // kModeChannel: one FP32 scale per token (activation row) and per output

@@ -253,6 +253,14 @@ int check_grouped(const void *q, const float *s_x, int s_layout, const void *w, 
   return FP8BQ_OK;
 }
 
+// Adapters: a status word (never set: these kernels have no waits), then the
+// first product's FP32 sums, one [M, R] plane per K split.
+size_t lora_workspace(int64_t M, int64_t R, int64_t K) {
+  int per;
+  const size_t planes = static_cast<size_t>(lora_splits(M, K, &per));
+  return 256 + (planes * static_cast<size_t>(M) * static_cast<size_t>(R) * 4 + 255) / 256 * 256;
+}
+
 int empty_batch(int64_t K, int64_t N) { return (K >= 1 && N >= 1) ? FP8BQ_OK : FP8BQ_ERR_SHAPE; }
 
 int check_parts(const int64_t *parts, int n_parts, int64_t N) {
@@ -324,7 +332,8 @@ const char *fp8bq_status_string(int s) {
 int fp8bq_last_cuda_error(void) { return g_last_cuda_error; }
 
 size_t fp8bq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
-  if (op < FP8BQ_OP_GEMM || op > FP8BQ_OP_GROUPED_GEMM || M < 0 || N < 1 || K < 1) return 256;
+  if (op < FP8BQ_OP_GEMM || op > FP8BQ_OP_LORA_ADD || M < 0 || N < 1 || K < 1) return 256;
+  if (op == FP8BQ_OP_LORA_ADD) return lora_workspace(M, N, K);
   return workspace_layout(op, M, N, K).total;
 }
 
@@ -881,6 +890,85 @@ int fp8bq_grouped_gemm_masked(const void *q, const float *s_x, int s_layout, con
   RETURN_IF(device_info(&dev));
   return gemm_grouped_impl(q, s_x, s_layout, w, s_w, nullptr, masked_m, E, max_m, y, M, N, K,
                            ws, static_cast<cudaStream_t>(stream), dev);
+}
+
+// ------------------------------------------------------------------ beside the linears
+
+int fp8bq_qk_norm_rope(const void *q, int64_t q_ts, int64_t q_hs, int64_t HQ, const void *k,
+                       int64_t k_ts, int64_t k_hs, int64_t HK, const void *q_gamma,
+                       const void *k_gamma, float eps, const float *table, int64_t P, int64_t rot,
+                       const void *pos, int pos_bits, int interleaved, void *q_out,
+                       int64_t qo_ts, int64_t qo_hs, void *k_out, int64_t ko_ts, int64_t ko_hs,
+                       int64_t T, int64_t D, void *stream) {
+  constexpr int64_t kMax = (int64_t(1) << 31) - 1;
+  if (T < 0 || T > kMax || HQ < 0 || HK < 0 || HQ + HK < 1 || HQ + HK > 65536 || D < 16 ||
+      D > 512 || rot < 0 || rot > D || P < 1 || !(eps >= 0.0f) || eps > 3.0e38f)
+    return FP8BQ_ERR_SHAPE;
+  if (D % 16 || rot % 16) return FP8BQ_ERR_ALIGN;
+  if (pos_bits != 32 && pos_bits != 64) return FP8BQ_ERR_UNSUPPORTED;
+  if (T == 0) return FP8BQ_OK;
+  if (!pos || (rot > 0 && !table) || (HQ > 0 && (!q || !q_out)) || (HK > 0 && (!k || !k_out)))
+    return FP8BQ_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(q_gamma, 16) || !aligned(k_gamma, 16) || !aligned(table, 16) ||
+      !aligned(pos, pos_bits / 8))
+    return FP8BQ_ERR_ALIGN;
+  if ((q_ts | q_hs | k_ts | k_hs | qo_ts | qo_hs | ko_ts | ko_hs) & 7) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  RopeArgs a = {};
+  a.q = static_cast<const uint16_t *>(q), a.k = static_cast<const uint16_t *>(k);
+  a.qo = static_cast<uint16_t *>(q_out), a.ko = static_cast<uint16_t *>(k_out);
+  a.q_ts = q_ts, a.q_hs = q_hs, a.k_ts = k_ts, a.k_hs = k_hs;
+  a.qo_ts = qo_ts, a.qo_hs = qo_hs, a.ko_ts = ko_ts, a.ko_hs = ko_hs;
+  a.gq = static_cast<const uint16_t *>(q_gamma), a.gk = static_cast<const uint16_t *>(k_gamma);
+  a.table = table, a.pos = pos, a.T = T, a.P = P;
+  a.HQ = static_cast<int>(HQ), a.HK = static_cast<int>(HK), a.D = static_cast<int>(D);
+  a.rot = static_cast<int>(rot), a.pos_is64 = pos_bits == 64, a.interleaved = interleaved != 0;
+  a.eps = eps;
+  return finish_launch(0, launch_qk_norm_rope(a, dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_lora_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order, int32_t *offsets,
+                     void *stream) {
+  if (M < 0 || M > (int64_t(1) << 31) - 1025 || L < 1 || L > kMaxAdapters) return FP8BQ_ERR_SHAPE;
+  if (!offsets || (M > 0 && (!ids || !order))) return FP8BQ_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(offsets, 4)) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  return finish_launch(0, launch_lora_group(ids, M, static_cast<int>(L), order, offsets,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, const float *scales,
+                   const int32_t *ranks, const int32_t *order, const int32_t *offsets,
+                   const void *base, int64_t ld_base, void *y, int64_t ldy, int64_t M, int64_t N,
+                   int64_t K, int64_t L, int64_t R, void *ws, size_t ws_bytes, void *stream) {
+  if (L < 1 || L > kMaxAdapters || R < 1 || R > kMaxLoraRank) return FP8BQ_ERR_SHAPE;
+  if (R % 8) return FP8BQ_ERR_ALIGN;
+  if (M == 0) return empty_batch(K, N);
+  if (!a || !b || !scales || !order || !offsets || !base || !y) return FP8BQ_ERR_NULL;
+  RETURN_IF(check_act(x, M, K, ldx, 16));
+  RETURN_IF(check_gemm_shape(M, N, K, 16));
+  if (ld_base < N || ldy < N || N > (int64_t(1) << 24)) return FP8BQ_ERR_SHAPE;
+  if (N % 8 || ld_base % 8 || ldy % 8 || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) ||
+      !aligned(y, 16) || !aligned(scales, 4) || !aligned(ranks, 4) || !aligned(order, 4) ||
+      !aligned(offsets, 4))
+    return FP8BQ_ERR_ALIGN;
+  if (!ws || ws_bytes < lora_workspace(M, R, K)) return FP8BQ_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  LoraArgs p = {};
+  p.x = static_cast<const uint16_t *>(x), p.ldx = ldx;
+  p.a = static_cast<const uint16_t *>(a), p.b = static_cast<const uint16_t *>(b);
+  p.base = static_cast<const uint16_t *>(base), p.ldbase = ld_base;
+  p.y = static_cast<uint16_t *>(y), p.ldy = ldy;
+  p.scales = scales, p.ranks = ranks, p.order = order, p.offsets = offsets;
+  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+  p.M = M, p.N = static_cast<int>(N), p.K = static_cast<int>(K);
+  p.L = static_cast<int>(L), p.R = static_cast<int>(R);
+  return finish_launch(0, launch_lora_add(p, dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

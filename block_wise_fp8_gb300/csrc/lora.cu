@@ -1,0 +1,534 @@
+// lora.cu -- low-rank adapters of many requests beside a shared projection:
+// the grouping of tokens by adapter, and
+//   y[t] = BF16(base[t] + s_a * B_a (A_a x[t])),   a the adapter of token t,
+// with A_a [R, K], B_a [N, R] in BF16 and only the first ranks[a] rows of A_a
+// and columns of B_a in use.
+//
+// Two products, two launches.  The first (shrink) leaves t = A_a x in FP32,
+// split over K so that few tokens still fill the GPU; the second (expand) adds
+// the splits in a fixed order, multiplies by B_a and adds the base row.  The
+// rank is so small that both are bound by their long operands (x once, base
+// and y once, the adapters once a tile): the tensor instruction takes its
+// operands straight from global memory in registers.  That needs no shared
+// memory because the K index of a product may be permuted at will if both
+// operands agree: a lane takes 16 contiguous values of a 64-wide K block and
+// feeds them to four MMAs, so every load is 16 bytes and a quad of lanes reads
+// 128 contiguous bytes of a row.  In the same way the columns of the second
+// product are dealt out so that a lane ends with 8 neighbouring outputs.
+//
+// t enters the second product as the sum of two BF16 values (hi + lo, 16
+// significant bits; the rounding left is 2^-17 of t, below the FP32 sums' own
+// noise at these lengths and far below the output's 2^-9), so that y carries
+// one BF16 rounding, its own.
+#include "common.cuh"
+#include "ptx.cuh"
+#include "quant_math.cuh"
+
+namespace fp8bq {
+namespace {
+
+constexpr int kTile = 128;      // tokens of one adapter that a CTA takes
+constexpr int kWarpTokens = 32; // two 16-row MMA tiles
+constexpr int kLoraThreads = 128;
+
+// D (16x8, FP32) += A (16x16, BF16) B (16x8, BF16)
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+struct Tile {
+  int a, start, count;  // adapter (L: no adapter), first sorted row, rows
+};
+
+// The idx-th tile of the segments (rows offsets[a] .. offsets[a+1]-1 of
+// adapter a, cut into tiles of kTile rows; with `rest`, the rows after the
+// last segment as adapter L).  One warp; count 0 when there is no such tile.
+// Bounds outside [0, M] are clamped.
+__device__ Tile find_tile(const int *offsets, int L, int M, int idx, bool rest) {
+  const int lane = threadIdx.x & 31;
+  const int segs = L + (rest ? 1 : 0);
+  const int per = (segs + 31) / 32;
+  auto bound = [&](int k) { return k > L ? M : min(max(__ldg(offsets + k), 0), M); };
+  int n = 0;
+  for (int i = 0; i < per; ++i) {
+    const int k = lane * per + i;
+    if (k < segs) n += (max(bound(k + 1) - bound(k), 0) + kTile - 1) / kTile;
+  }
+  int upto = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > idx);
+  Tile t = {L, 0, 0};
+  if (past == 0) return t;
+  const int owner = __ffs(past) - 1;
+  if (lane == owner) {
+    int left = idx - (upto - n);
+    for (int i = 0; i < per; ++i) {
+      const int k = lane * per + i;
+      if (k >= segs) break;
+      const int s = bound(k), len = max(bound(k + 1) - s, 0);
+      const int tiles = (len + kTile - 1) / kTile;
+      if (left < tiles) {
+        t = {k, s + left * kTile, min(kTile, len - left * kTile)};
+        break;
+      }
+      left -= tiles;
+    }
+  }
+  t.a = __shfl_sync(0xFFFFFFFFu, t.a, owner);
+  t.start = __shfl_sync(0xFFFFFFFFu, t.start, owner);
+  t.count = __shfl_sync(0xFFFFFFFFu, t.count, owner);
+  return t;
+}
+
+__device__ __forceinline__ int rank_of(const LoraArgs &p, int a) {
+  if (a >= p.L) return 0;
+  return p.ranks ? min(max(__ldg(p.ranks + a), 0), p.R) : p.R;
+}
+
+// t = A_a x over one K split, 64 ranks at most (a higher rank takes a second
+// plane of CTAs, which finds x in L2).  A tile of at most 32 tokens has its K blocks
+// dealt to the four warps, whose sums are joined in a fixed order; a longer
+// one has its tokens dealt to them.
+template <int NT>  // 8-row groups of A: min(R, 64) <= 8 NT
+__global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArgs p) {
+  __shared__ float red[3][NT * 8][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int M = static_cast<int>(p.M);
+  const Tile t = find_tile(p.offsets, p.L, M, blockIdx.x, false);
+  const int r0 = blockIdx.z * (NT * 8);  // first rank of this plane
+  const int rank = rank_of(p, t.a) - r0;
+  if (t.count == 0 || rank <= 0) return;
+  const bool by_k = t.count <= kWarpTokens;
+  const int tok0 = by_k ? 0 : w * kWarpTokens;
+  const int here = min(t.count - tok0, kWarpTokens);  // tokens of this warp
+  if (!by_k && here <= 0) return;                      // no barrier follows in that form
+  const bool two = here > 16;
+
+  const uint16_t *xr[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = m * 16 + r * 8 + g;
+      xr[m][r] = nullptr;
+      if (row < here) {
+        const int tok = __ldg(p.order + t.start + tok0 + row);
+        if (tok >= 0 && tok < M) xr[m][r] = p.x + tok * p.ldx + 16 * q;
+      }
+    }
+  const uint16_t *ar[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    ar[n] = n * 8 + g < rank ? p.a + (static_cast<int64_t>(t.a) * p.R + r0 + n * 8 + g) * p.K + 16 * q
+                             : nullptr;
+
+  float acc[2][NT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+
+  const int kb0 = blockIdx.y * p.kb_split;
+  const int kb1 = min((p.K + 63) / 64, kb0 + p.kb_split);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  constexpr int kUnroll = NT <= 2 ? 2 : 1;
+#pragma unroll kUnroll
+  for (int kb = kb0 + (by_k ? w : 0); kb < kb1; kb += by_k ? 4 : 1) {
+    const int k = kb * 64;
+    const bool in = k + 16 * q < p.K;
+    uint4 xv[2][2][2], av[NT][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool on = in && xr[m][r] != nullptr;
+        const uint4 *src = reinterpret_cast<const uint4 *>(xr[m][r] + k);
+        xv[m][r][0] = on ? __ldg(src) : zero;
+        xv[m][r][1] = on ? __ldg(src + 1) : zero;
+      }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const bool on = in && ar[n] != nullptr;
+      const uint4 *src = reinterpret_cast<const uint4 *>(ar[n] + k);
+      av[n][0] = on ? __ldg(src) : zero;
+      av[n][1] = on ? __ldg(src + 1) : zero;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (m == 1 && !two) break;
+      const uint32_t x0[8] = {xv[m][0][0].x, xv[m][0][0].y, xv[m][0][0].z, xv[m][0][0].w,
+                              xv[m][0][1].x, xv[m][0][1].y, xv[m][0][1].z, xv[m][0][1].w};
+      const uint32_t x1[8] = {xv[m][1][0].x, xv[m][1][0].y, xv[m][1][0].z, xv[m][1][0].w,
+                              xv[m][1][1].x, xv[m][1][1].y, xv[m][1][1].z, xv[m][1][1].w};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n * 8 >= rank) break;
+        const uint32_t b[8] = {av[n][0].x, av[n][0].y, av[n][0].z, av[n][0].w,
+                               av[n][1].x, av[n][1].y, av[n][1].z, av[n][1].w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(acc[m][n], x0[2 * s], x1[2 * s], x0[2 * s + 1], x1[2 * s + 1], b[2 * s],
+                   b[2 * s + 1]);
+      }
+    }
+  }
+
+  if (by_k) {
+    if (w > 0) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) red[w - 1][(m * NT + n) * 4 + i][lane] = acc[m][n][i];
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int o = 0; o < 3; ++o)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] += red[o][(m * NT + n) * 4 + i][lane];
+  }
+  float *out = p.part + (static_cast<int64_t>(blockIdx.y) * p.M + t.start + tok0) * p.R;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = m * 16 + r * 8 + g;
+      if (row >= here) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int c = r0 + n * 8 + 2 * q;
+        if (c < p.R)
+          *reinterpret_cast<float2 *>(out + static_cast<int64_t>(row) * p.R + c) =
+              make_float2(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
+      }
+    }
+}
+
+// y = base + s_a * B_a t.  A warp holds up to 32 tokens' t as MMA operands in
+// its own part of shared memory and walks groups of 32 columns; in a tile of
+// at most 32 tokens the four warps take different groups, else different
+// tokens.  Rows without an adapter come as a tile of rank 0 and are copied.
+template <int KS>  // 16-wide steps of the rank: R <= 16 KS
+__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArgs p) {
+  extern __shared__ uint4 sm[];
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int M = static_cast<int>(p.M);
+  // the first product's launch waited for everything before it, so what it
+  // read (offsets, order, weights) and the base rows are visible here already
+  const Tile t = find_tile(p.offsets, p.L, M, blockIdx.x, p.copy_rest != 0);
+  const bool by_n = t.count <= kWarpTokens;
+  const int tok0 = by_n ? 0 : w * kWarpTokens;
+  const int here = min(t.count - tok0, kWarpTokens);
+  if (here <= 0) {  // nothing to do, but this grid must not end before the first product's
+    griddep_wait();
+    return;
+  }
+  const bool two = here > 16;
+  const int rank = rank_of(p, t.a);
+  const int ks_n = (rank + 15) / 16;
+  uint4 *my = sm + w * (KS * 2 * 2 * 32) + lane;  // [ks][m][hi, lo][lane]
+
+  int tok[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = m * 16 + r * 8 + g;
+      const int v = row < here ? __ldg(p.order + t.start + tok0 + row) : -1;
+      tok[m][r] = v < M ? v : -1;
+    }
+
+  griddep_wait();
+  if (rank > 0) {
+    const float scale = __ldg(p.scales + t.a);
+    const float *src = p.part + (static_cast<int64_t>(t.start) + tok0) * p.R;
+    for (int ks = 0; ks < ks_n; ++ks) {
+      const int k = ks * 16 + 4 * q;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m == 1 && !two) break;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = m * 16 + r * 8 + g;
+          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (row < here && k < p.R) {
+            const float *at = src + static_cast<int64_t>(row) * p.R + k;
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s) {
+              const float4 f = __ldcg(reinterpret_cast<const float4 *>(at + s * p.M * p.R));
+              v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+            }
+          }
+          float l[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = k + i < rank ? v[i] * scale : 0.0f;
+            l[i] = v[i] - __uint_as_float(pack_bf16(0.0f, v[i]) & 0xFFFF0000u);
+          }
+          hi[r] = pack_bf16(v[0], v[1]), hi[2 + r] = pack_bf16(v[2], v[3]);
+          lo[r] = pack_bf16(l[0], l[1]), lo[2 + r] = pack_bf16(l[2], l[3]);
+        }
+        my[((ks * 2 + m) * 2 + 0) * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        my[((ks * 2 + m) * 2 + 1) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+  }
+  // each lane reads back only what it wrote: no barrier
+
+  const int groups = (p.N + 31) / 32;
+  const int g0 = blockIdx.y * p.ngroups;
+  const int g1 = min(groups, g0 + p.ngroups);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint16_t *bw = p.b + static_cast<int64_t>(t.a) * p.N * p.R + 4 * q;
+  for (int cg = g0 + (by_n ? w : 0); cg < g1; cg += by_n ? 4 : 1) {
+    const int n0 = cg * 32;
+    const int nc = n0 + 8 * q;  // this lane's 8 output columns
+    uint4 bs[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        bs[m][r] = tok[m][r] >= 0 && nc < p.N
+                       ? *reinterpret_cast<const uint4 *>(p.base + tok[m][r] * p.ldbase + nc)
+                       : zero;
+    uint2 bv[KS][4];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+        const int k = ks * 16 + 4 * q;
+        bv[ks][j] = make_uint2(0, 0);
+        if (col < p.N && k < rank)
+          bv[ks][j] = __ldg(reinterpret_cast<const uint2 *>(
+              bw + static_cast<int64_t>(col) * p.R + ks * 16));
+        if (k + 4 > rank) {  // columns past the rank are not read as numbers
+          if (k + 3 >= rank) bv[ks][j].y &= 0xFFFFu;
+          if (k + 2 >= rank) bv[ks][j].y = 0;
+          if (k + 1 >= rank) bv[ks][j].x &= 0xFFFFu;
+        }
+      }
+    float acc[2][4][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks >= ks_n) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m == 1 && !two) break;
+        const uint4 hi = my[((ks * 2 + m) * 2 + 0) * 32];
+        const uint4 lo = my[((ks * 2 + m) * 2 + 1) * 32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma_bf16(acc[m][j], hi.x, hi.y, hi.z, hi.w, bv[ks][j].x, bv[ks][j].y);
+          mma_bf16(acc[m][j], lo.x, lo.y, lo.z, lo.w, bv[ks][j].x, bv[ks][j].y);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (tok[m][r] < 0 || nc >= p.N) continue;
+        const uint32_t bb[4] = {bs[m][r].x, bs[m][r].y, bs[m][r].z, bs[m][r].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = pack_bf16(bf16_lo(bb[j]) + acc[m][j][2 * r],
+                           bf16_hi(bb[j]) + acc[m][j][2 * r + 1]);
+        *reinterpret_cast<uint4 *>(p.y + tok[m][r] * p.ldy + nc) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+  }
+}
+
+// Stable counting sort of tokens by adapter in one CTA: each warp counts its
+// own stretch of tokens in its own row of counters (equal keys of 32 tokens
+// found with a match, added by one lane: no atomics, so the order is fixed),
+// the counters are scanned key by key, and each warp writes its stretch.
+constexpr int kGroupThreads = 1024;
+__global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const int *ids, int M, int L,
+                                                                   int *order, int *offsets) {
+  extern __shared__ int cnt[];  // [warps][L + 1]
+  __shared__ int wsum[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int keys = L + 1;
+  const int each = ((M + 31) / 32 + 31) / 32 * 32;  // tokens of a warp
+  const int warps = each ? (M + each - 1) / each : 0;
+  for (int i = threadIdx.x; i < warps * keys; i += kGroupThreads) cnt[i] = 0;
+  __syncthreads();
+  const int64_t from = static_cast<int64_t>(w) * each;
+  const int begin = static_cast<int>(from < M ? from : M);
+  const int end = static_cast<int>(from + each < M ? from + each : M);
+  int *mine = cnt + w * keys;
+  auto walk = [&](auto &&at) {
+    for (int i0 = begin; i0 < end; i0 += 32 * 4) {
+      int id[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * 32 + lane;
+        id[u] = i < end ? __ldg(ids + i) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * 32 + lane;
+        const uint32_t act = __ballot_sync(0xFFFFFFFFu, i < end);
+        if (i < end) {
+          const int key = id[u] >= 0 && id[u] < L ? id[u] : L;
+          const uint32_t same = __match_any_sync(act, key);
+          at(i, key, same);
+        }
+        __syncwarp();
+      }
+    }
+  };
+  walk([&](int, int key, uint32_t same) {
+    if ((same & ((1u << lane) - 1u)) == 0) mine[key] += __popc(same);
+  });
+  __syncthreads();
+  // exclusive positions: keys in order, a key's warps in order
+  const int key = threadIdx.x;
+  int total = 0;
+  if (key < keys)
+    for (int i = 0; i < warps; ++i) {
+      const int c = cnt[i * keys + key];
+      cnt[i * keys + key] = total;
+      total += c;
+    }
+  int upto = total;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) wsum[w] = upto;
+  __syncthreads();
+  if (w == 0) {
+    int v = wsum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+      if (lane >= d) v += o;
+    }
+    wsum[lane] = v;
+  }
+  __syncthreads();
+  const int base = upto - total + (w ? wsum[w - 1] : 0);
+  if (key < keys) {
+    offsets[key] = base;
+    for (int i = 0; i < warps; ++i) cnt[i * keys + key] += base;
+  }
+  __syncthreads();
+  walk([&](int i, int key_i, uint32_t same) {
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int at = mine[key_i] + rank;
+    __syncwarp(same);  // every lane of this key has read its counter
+    order[at] = i;
+    if (rank == 0) mine[key_i] += __popc(same);
+  });
+}
+
+}  // namespace
+
+// Enough splits that few tokens still fill the GPU (four K blocks a split at
+// least, one for each warp), and four from 512 tokens on, where the token
+// tiles do.
+int lora_splits(int64_t M, int64_t K, int *kb_split) {
+  const int kbs = static_cast<int>((K + 63) / 64);
+  int splits = M >= 512 ? 4 : (kbs + 3) / 4;
+  if (splits > 24) splits = 24;
+  if (splits > kbs) splits = kbs;
+  const int per = (kbs + splits - 1) / splits;
+  *kb_split = per;
+  return (kbs + per - 1) / per;
+}
+
+cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
+  a.splits = lora_splits(a.M, a.K, &a.kb_split);
+  a.copy_rest = a.y != a.base;
+  // each segment adds at most one partly filled tile; none is empty
+  const int64_t full = (a.M + kTile - 1) / kTile;
+  const int64_t shrink_tiles = full + a.L < a.M ? full + a.L : a.M;
+  const int64_t expand_tiles = full + a.L + 1 < a.M ? full + a.L + 1 : a.M;
+  {
+    const dim3 grid(static_cast<unsigned>(shrink_tiles), a.splits), block(kLoraThreads);
+    cudaError_t e;
+    if (a.R <= 16) e = launch_pdl(lora_shrink_kernel<2>, grid, block, 0, st, a);
+    else if (a.R <= 32) e = launch_pdl(lora_shrink_kernel<4>, grid, block, 0, st, a);
+    else e = launch_pdl(lora_shrink_kernel<8>, dim3(grid.x, grid.y, (a.R + 63) / 64), block, 0, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  const int groups = (a.N + 31) / 32;
+  int64_t ng = (groups * expand_tiles + num_sms * 8 - 1) / (num_sms * 8);
+  ng = (ng + 3) / 4 * 4;
+  a.ngroups = static_cast<int>(ng < groups ? ng : groups);
+  const dim3 grid(static_cast<unsigned>(expand_tiles), (groups + a.ngroups - 1) / a.ngroups),
+      block(kLoraThreads);
+  const int ks = (a.R + 15) / 16;
+  auto run = [&](auto kern, int KS) {
+    const size_t smem = static_cast<size_t>(KS) * 2 * 2 * 32 * 16 * 4;
+    if (smem > 48 * 1024) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, grid, block, smem, st, a);
+  };
+  if (ks <= 1) return run(lora_expand_kernel<1>, 1);
+  if (ks <= 2) return run(lora_expand_kernel<2>, 2);
+  if (ks <= 4) return run(lora_expand_kernel<4>, 4);
+  return run(lora_expand_kernel<8>, 8);
+}
+
+cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int *offsets,
+                              cudaStream_t st) {
+  const int each = static_cast<int>(((M + 31) / 32 + 31) / 32 * 32);
+  const int warps = each ? static_cast<int>((M + each - 1) / each) : 0;
+  const size_t smem = static_cast<size_t>(warps) * (L + 1) * sizeof(int);
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(lora_group_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(lora_group_kernel, dim3(1), dim3(kGroupThreads), smem, st, ids,
+                    static_cast<int>(M), L, order, offsets);
+}
+
+}  // namespace fp8bq

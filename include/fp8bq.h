@@ -106,7 +106,8 @@ enum {
   FP8BQ_OP_CHANNEL_LINEAR = 7,
   FP8BQ_OP_UE8M0_GEMM = 8,
   FP8BQ_OP_UE8M0_LINEAR = 9,
-  FP8BQ_OP_GROUPED_GEMM = 10 /* both grouped forms; M = rows of A and Y in all */
+  FP8BQ_OP_GROUPED_GEMM = 10, /* both grouped forms; M = rows of A and Y in all */
+  FP8BQ_OP_LORA_ADD = 11      /* fp8bq_lora_add; N = the adapters' rank R */
 };
 
 /* ---------------------------------------------------------------- utility
@@ -430,6 +431,64 @@ FP8BQ_API int fp8bq_grouped_gemm_masked(const void *q, const float *s_x,
                                         int64_t max_m, void *y, int64_t N,
                                         int64_t K, void *ws, size_t ws_bytes,
                                         void *stream);
+
+/* ------------------------------------------------ beside the linears
+ * What stands next to the block-FP8 linears in a served decoder layer.  The
+ * pages name these steps around the linear without giving their kernels. */
+
+/* RMSNorm of every query and key head and the rotary embedding, in one pass
+ * over the QKV projection's output.  Per head v of D values, in FP32 with one
+ * rounding to BF16 at the end:
+ *   n = v / sqrt(mean(v^2) + eps) * gamma        (gamma NULL: n = v)
+ *   a' = a cos - b sin, b' = b cos + a sin       for the pairs (a, b) of n
+ * where the pairs are (n_i, n_{i + rot/2}), i < rot/2, or (n_2i, n_{2i+1}) when
+ * `interleaved` is not 0, and values from `rot` on are not rotated.
+ * q: BF16, value d of head h of token t at q[t * q_ts + h * q_hs + d] (a slice
+ * of the packed QKV rows, for example); k, q_out, k_out likewise.  An output may
+ * be its own input (same pointer and strides); no other overlap.  HQ or HK may
+ * be 0 (its pointers NULL).  q_gamma, k_gamma: BF16 [D] or NULL.  table: FP32
+ * [P][rot], the cosines of a position's rot/2 angles, then the sines.  pos:
+ * DEVICE int32 or int64 [T] (pos_bits 32 or 64); a token whose position lies
+ * outside [0, P) counts as padding and its outputs are zeros.
+ * 16 <= D <= 512; D % 16 == 0, rot % 16 == 0 (rot == 0: the norm alone, table
+ * NULL), strides multiples of 8, data pointers 16-byte aligned (ERR_ALIGN).
+ * T == 0: nothing is launched.  eps finite, >= 0 (ERR_SHAPE). */
+FP8BQ_API int fp8bq_qk_norm_rope(const void *q, int64_t q_ts, int64_t q_hs, int64_t HQ,
+                                 const void *k, int64_t k_ts, int64_t k_hs, int64_t HK,
+                                 const void *q_gamma, const void *k_gamma, float eps,
+                                 const float *table, int64_t P, int64_t rot, const void *pos,
+                                 int pos_bits, int interleaved, void *q_out, int64_t qo_ts,
+                                 int64_t qo_hs, void *k_out, int64_t ko_ts, int64_t ko_hs,
+                                 int64_t T, int64_t D, void *stream);
+
+/* Groups tokens by adapter, for fp8bq_lora_add: order receives the token
+ * indices 0 .. M-1 sorted by adapter (stable), offsets[a] .. offsets[a+1]-1
+ * the places of adapter a's tokens in it.  ids: DEVICE int32 [M]; a token whose
+ * id lies outside [0, L) has no adapter and comes after offsets[L].  order:
+ * int32 [M]; offsets: int32 [L+1].  1 <= L <= 512.  M == 0 writes zero offsets.
+ * One call serves every projection of a forward step. */
+FP8BQ_API int fp8bq_lora_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order,
+                               int32_t *offsets, void *stream);
+
+/* Low-rank adapters of many requests beside a shared projection (fp8bq_linear's
+ * y as `base`):
+ *   y[t] = BF16(base[t] + scales[a] * sum_{r < ranks[a]} b[a][:, r] (a[a][r] . x[t]))
+ * with a the adapter that order and offsets (fp8bq_lora_group's) give token t;
+ * a token without an adapter gets y[t] = base[t].  FP32 sums; t_r = a[a][r] . x[t]
+ * enters the second product with 16 significant bits, y is rounded once.
+ * x: BF16 [M, K] pitch ldx; a: BF16 [L, R, K]; b: BF16 [L, N, R]; scales: FP32
+ * [L]; ranks: DEVICE int32 [L], clamped to [0, R], or NULL (every rank is R) --
+ * rows and columns past a rank are never used, whatever they hold; base: BF16
+ * [M, N] pitch ld_base; y: BF16 [M, N] pitch ldy, which may be base itself.
+ * Offsets outside [0, M] are clamped and order entries outside [0, M) skipped.
+ * K % 16 == 0, N % 8 == 0, R % 8 == 0, pitches multiples of 8, pointers 16-byte
+ * aligned (ERR_ALIGN); 1 <= R <= 128, 1 <= L <= 512 (ERR_SHAPE).  Workspace:
+ * fp8bq_workspace_bytes(FP8BQ_OP_LORA_ADD, M, R, K); two launches. */
+FP8BQ_API int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b,
+                             const float *scales, const int32_t *ranks, const int32_t *order,
+                             const int32_t *offsets, const void *base, int64_t ld_base, void *y,
+                             int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
+                             void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------ weight / calibration set-up */
 

@@ -1,0 +1,184 @@
+"""Adapter grouping and the adapters' products against plain forms in 64 bits.
+
+Bound of y: half a BF16 step of the result (2^-8), t = A x held with 16
+significant bits (2^-17 of each term b t), and binary32 sums of K and of R + 1
+terms: (K + R + 64) * 2^-23 of the sums of magnitudes (one step, not half, a
+term: the tensor instruction may truncate)."""
+import pytest
+import torch
+
+import block_wise_fp8_gb300 as fb
+
+pytestmark = pytest.mark.gpu
+BF16, I32 = torch.bfloat16, torch.int32
+
+
+def group_ref(ids, L):
+    key = torch.where((ids >= 0) & (ids < L), ids, L).long().cpu()
+    order = torch.sort(key, stable=True).indices
+    counts = torch.bincount(key, minlength=L + 1)[:L]
+    return order.to(I32), torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).to(I32)
+
+
+def group(ids, L):
+    order = torch.full((ids.numel(),), -7, device="cuda", dtype=I32)
+    offsets = torch.full((L + 1,), -7, device="cuda", dtype=I32)
+    fb.fp8bq_lora_group(ids, order, offsets)
+    return order, offsets
+
+
+@pytest.mark.parametrize("M,L", [(0, 3), (1, 1), (31, 5), (32, 512), (33, 2), (1000, 7),
+                                 (1025, 512), (16384, 128), (100003, 33)])
+def test_group_sorts_stably(M, L):
+    g = torch.Generator("cuda").manual_seed(M + L)
+    ids = torch.randint(-2, L + 2, (M,), generator=g, device="cuda", dtype=I32)
+    order, offsets = group(ids, L)
+    ro, rf = group_ref(ids, L)
+    assert torch.equal(offsets.cpu(), rf)
+    assert torch.equal(order.cpu(), ro)
+
+
+@pytest.mark.parametrize("value", [0, 4, -1])
+def test_group_of_one_key(value):
+    ids = torch.full((777,), value, device="cuda", dtype=I32)
+    order, offsets = group(ids, 5)
+    ro, rf = group_ref(ids, 5)
+    assert torch.equal(offsets.cpu(), rf) and torch.equal(order.cpu(), ro)
+
+
+def reference(x, a, b, scales, ids, base, ranks):
+    L, R, K = a.shape
+    y = base.double().clone()
+    tol = torch.zeros_like(y)
+    for i in range(L):
+        tok = (ids == i).nonzero(as_tuple=True)[0]
+        r = R if ranks is None else int(ranks[i].clamp(0, R))
+        if not tok.numel() or r == 0:
+            continue
+        xa, aa, ba, s = x[tok].double(), a[i, :r].double(), b[i, :, :r].double(), scales[i].double()
+        t = xa @ aa.t()
+        y[tok] += s * (t @ ba.t())
+        tol[tok] = s.abs() * (t.abs() @ ba.abs().t() * 2.0 ** -17 +
+                              xa.abs() @ aa.abs().t() @ ba.abs().t() * (K + R + 64) * 2.0 ** -23)
+    return y, tol + (y.abs() + tol) * 2.0 ** -8 + base.double().abs() * 2.0 ** -22
+
+
+def inputs(M, L, R, K, N, seed, low=-1):
+    g = torch.Generator("cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    return dict(x=rn(M, K).to(BF16), a=(rn(L, R, K) * K ** -0.5).to(BF16),
+                b=rn(L, N, R).to(BF16), scales=rn(L), base=(2 * rn(M, N)).to(BF16),
+                ids=torch.randint(low, L, (M,), generator=g, device="cuda", dtype=I32))
+
+
+def run(d, ranks=None, y=None, base=None):
+    M, K = d["x"].shape
+    L, R, _ = d["a"].shape
+    order, offsets = group(d["ids"], L)
+    base = d["base"] if base is None else base
+    y = torch.full(base.shape, 5.0, device="cuda", dtype=BF16) if y is None else y
+    ws = fb.new_workspace(fb.OP_LORA_ADD, M, R, K)
+    fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, base, y, ws, ranks=ranks)
+    return y
+
+
+def check(y, ref, bound):
+    err = (y.double() - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound.clamp(min=1e-30)).max())
+
+
+@pytest.mark.parametrize("M,L,R,K,N", [
+    (1, 1, 8, 16, 8), (1, 4, 16, 6144, 6144), (2, 3, 24, 272, 40), (17, 2, 32, 1040, 136),
+    (33, 1, 64, 528, 104), (64, 32, 16, 512, 1000), (129, 2, 40, 256, 264),
+    (300, 3, 128, 400, 72), (517, 5, 72, 320, 328), (1500, 4, 64, 640, 512),
+    (700, 200, 16, 128, 64)])
+def test_products(M, L, R, K, N):
+    d = inputs(M, L, R, K, N, seed=M + R)
+    y = run(d)
+    check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
+
+
+@pytest.mark.parametrize("M", [5, 200])
+def test_ranks_hide_what_lies_past_them(M):
+    L, R, K, N = 6, 64, 256, 128
+    d = inputs(M, L, R, K, N, seed=M, low=0)
+    ranks = torch.tensor([0, 1, 7, 21, 64, 1000], device="cuda", dtype=I32)
+    for i in range(L):
+        r = min(int(ranks[i]), R)
+        d["a"][i, r:] = float("nan")
+        d["b"][i, :, r:] = float("inf")
+    y = run(d, ranks=ranks)
+    check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], ranks))
+    assert torch.equal(y[d["ids"] == 0], d["base"][d["ids"] == 0])
+
+
+@pytest.mark.parametrize("M", [3, 190])
+def test_in_place_and_pitched(M):
+    L, R, K, N = 3, 16, 144, 80
+    d = inputs(M, L, R, K, N, seed=9)
+    d["x"] = torch.cat([d["x"], torch.full((M, 24), float("nan"), device="cuda", dtype=BF16)], 1)[:, :K]
+    wide = torch.cat([d["base"], torch.full((M, 16), 3.0, device="cuda", dtype=BF16)], 1)
+    view = wide[:, :N]
+    ref = reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None)
+    run(d, y=view, base=view)
+    check(view, *ref)
+    assert bool((wide[:, N:] == 3.0).all())
+
+
+def test_no_token_has_an_adapter():
+    d = inputs(70, 4, 16, 128, 96, seed=1)
+    d["ids"].fill_(-1)
+    assert torch.equal(run(d), d["base"])
+    keep = d["base"].clone()
+    assert torch.equal(run(d, y=keep, base=keep), d["base"])
+
+
+def test_bounds_and_indices_outside_the_tokens_touch_nothing():
+    d = inputs(40, 2, 16, 128, 64, seed=2, low=0)
+    order = torch.arange(40, device="cuda", dtype=I32)
+    order[3], order[5] = -4, 4000
+    offsets = torch.tensor([-9, 20, 900], device="cuda", dtype=I32)
+    ids = torch.where(torch.arange(40, device="cuda") < 20, 0, 1).to(I32)
+    ref, bound = reference(d["x"], d["a"], d["b"], d["scales"], ids, d["base"], None)
+    y = torch.full_like(d["base"], 5.0)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, 40, 16, 128)
+    fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
+    left = torch.ones(40, dtype=torch.bool, device="cuda")
+    left[[3, 5]] = False
+    check(y[left], ref[left], bound[left])
+    assert bool((y[~left] == 5.0).all())
+
+
+def test_repeats_are_identical_and_capture_replays():
+    d = inputs(130, 3, 32, 512, 256, seed=5)
+    first = run(d)
+    assert torch.equal(first, run(d))
+    order, offsets = group(d["ids"], 3)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, 130, 32, 512)
+    y = torch.empty_like(first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fb.fp8bq_lora_group(d["ids"], order, offsets)
+        fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
+    d["ids"].copy_((d["ids"] + 2) % 3)
+    graph.replay()
+    check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
+
+
+def test_a_stream_of_its_own():
+    d = inputs(50, 2, 16, 256, 128, seed=6)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        y = run(d)
+    st.synchronize()
+    check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
+
+
+def test_no_tokens():
+    d = inputs(1, 2, 16, 64, 64, seed=7)
+    e = torch.empty(0, 64, device="cuda", dtype=BF16)
+    none = torch.empty(0, device="cuda", dtype=I32)
+    fb.fp8bq_lora_add(e, d["a"], d["b"], d["scales"], none, torch.zeros(3, device="cuda", dtype=I32),
+                      e, e, fb.new_workspace(fb.OP_LORA_ADD, 0, 16, 64))
