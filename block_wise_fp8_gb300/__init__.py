@@ -30,6 +30,8 @@ __all__ = [
     "OP_GROUPED_GEMM", "fp8bq_grouped_gemm", "fp8bq_grouped_gemm_masked",
     "fp8bq_check_scales",
     "OP_LORA_ADD", "fp8bq_qk_norm_rope", "fp8bq_lora_group", "fp8bq_lora_add",
+    "MOE_SOFTMAX", "MOE_SIGMOID", "MOE_MAX_TOKENS", "fp8bq_moe_layer", "fp8bq_moe_experts",
+    "fp8bq_moe_workspace_bytes", "new_moe_workspace",
     "library_path",
     "fp8bq_version", "fp8bq_status_string", "fp8bq_last_cuda_error",
     "fp8bq_workspace_bytes", "fp8bq_workspace_init", "fp8bq_poll_status",
@@ -46,6 +48,8 @@ SCALE_ROW_MAJOR, SCALE_COL_MAJOR = 0, 1
 (OP_GEMM, OP_LINEAR, OP_MX_GEMM, OP_MX_LINEAR, OP_STATIC_GEMM,
  OP_STATIC_LINEAR, OP_CHANNEL_GEMM, OP_CHANNEL_LINEAR, OP_UE8M0_GEMM,
  OP_UE8M0_LINEAR, OP_GROUPED_GEMM, OP_LORA_ADD) = range(12)
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1               # router scores of fp8bq_moe_layer
+MOE_MAX_TOKENS = 64
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024      # FP8BQ_NOALLOC_SCRATCH_BYTES
 
 STATUS_NAMES = {0: "FP8BQ_OK", 1: "FP8BQ_ERR_NULL", 2: "FP8BQ_ERR_SHAPE",
@@ -122,6 +126,11 @@ def _load():
         "fp8bq_lora_group": (I32, [P, I64, I64, P, P, P]),
         "fp8bq_lora_add": (I32, [P, I64, P, P, P, P, P, P, P, I64, P, I64, I64, I64, I64, I64,
                                  I64, P, SZ, P]),
+        "fp8bq_moe_workspace_bytes": (SZ, [I64, I64, I64, I64, I64]),
+        "fp8bq_moe_layer": (I32, [P, I64, P, P, I32, I32, F32, I64, P, P, P, P, P, P, P, I64, I64,
+                                  I64, I64, P, SZ, P]),
+        "fp8bq_moe_experts": (I32, [P, I64, P, P, I64, P, P, P, P, P, I64, I64, I64, I64, P, SZ,
+                                    P]),
         "fp8bq_e4m3_from_bits": (I32, [ctypes.c_uint32, I64, P, P]),
     }
     for name, (res, args) in sigs.items():
@@ -673,6 +682,63 @@ def fp8bq_lora_add(x, a, b, scales, order, offsets, base, y, ws, ranks=None, str
         _ptr(x), _ld(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(ranks), _ptr(order), _ptr(offsets),
         _ptr(base), _ld(base), _ptr(y), _ld(y), M, N, K, L, R, _ptr(ws), _nbytes(ws),
         _stream(stream)), "fp8bq_lora_add")
+
+
+def fp8bq_moe_workspace_bytes(M: int, E: int, H: int, I: int, topk: int) -> int:
+    return _lib.fp8bq_moe_workspace_bytes(M, E, H, I, topk)
+
+
+def new_moe_workspace(M: int, E: int, H: int, I: int, topk: int, device="cuda", stream=None):
+    """A zero-initialised workspace for fp8bq_moe_layer and fp8bq_moe_experts at these sizes."""
+    ws = torch.empty(fp8bq_moe_workspace_bytes(M, E, H, I, topk), dtype=torch.uint8, device=device)
+    fp8bq_workspace_init(ws, stream)
+    return ws
+
+
+def _moe_specs(x, w13, s13, w2, s2, y, ws):
+    M, H = _mat(x, "x")
+    E, I2, _ = _experts_w(w13)
+    I = I2 // 2
+    return M, E, H, I, [
+        _Spec("x", x, _BF16, (M, H), kind="rows"),
+        _Spec("w13", w13, _E4M3, (E, 2 * I, H)),
+        _Spec("s13", s13, _F32, (E, _kb(2 * I), _kb(H))),
+        _Spec("w2", w2, _E4M3, (E, H, I)),
+        _Spec("s2", s2, _F32, (E, _kb(H), _kb(I))),
+        _Spec("y", y, _BF16, (M, H)), _ws(ws)]
+
+
+def fp8bq_moe_layer(x, logits, w13, s13, w2, s2, y, ws, topk: int, score: int = MOE_SOFTMAX,
+                    renormalize: bool = True, routed_scale: float = 1.0, bias=None, ids_out=None,
+                    weights_out=None, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens x [M, H] from the
+    router's logits [M, E]: top-k routing, w13 [E, 2I, H], SiLU(gate) * up,
+    w2 [E, H, I], weighted sum into y.  bias [E] (MOE_SIGMOID): added to the
+    score for the choice only.  ids_out / weights_out [M, topk] receive the
+    routing.  Workspace: new_moe_workspace(M, E, H, I, topk)."""
+    M, E, H, I, specs = _moe_specs(x, w13, s13, w2, s2, y, ws)
+    _validate("fp8bq_moe_layer", specs + [
+        _Spec("logits", logits, _F32, (M, E)),
+        _Spec("bias", bias, _F32, (E,), optional=True),
+        _Spec("ids_out", ids_out, _I32, (M, topk), optional=True),
+        _Spec("weights_out", weights_out, _F32, (M, topk), optional=True)], stream)
+    _check(_lib.fp8bq_moe_layer(
+        _ptr(x), _ld(x), _ptr(logits), _ptr(bias), score, int(renormalize), float(routed_scale),
+        topk, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(y), _ptr(ids_out),
+        _ptr(weights_out), M, E, H, I, _ptr(ws), _nbytes(ws), _stream(stream)),
+        "fp8bq_moe_layer")
+
+
+def fp8bq_moe_experts(x, ids, weights, w13, s13, w2, s2, y, ws, stream=None):
+    """The layer for tokens already routed: ids int32 [M, topk] (values outside
+    [0, E) are left out) and weights FP32 [M, topk]."""
+    M, E, H, I, specs = _moe_specs(x, w13, s13, w2, s2, y, ws)
+    topk = _mat(ids, "ids")[1]
+    _validate("fp8bq_moe_experts", specs + [
+        _Spec("ids", ids, _I32, (M, topk)), _Spec("weights", weights, _F32, (M, topk))], stream)
+    _check(_lib.fp8bq_moe_experts(
+        _ptr(x), _ld(x), _ptr(ids), _ptr(weights), topk, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
+        _ptr(y), M, E, H, I, _ptr(ws), _nbytes(ws), _stream(stream)), "fp8bq_moe_experts")
 
 
 # ---------------------------------------------------------------- residual add + RMSNorm

@@ -121,6 +121,38 @@ cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st);
 cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int *offsets,
                               cudaStream_t st);
 
+// A whole mixture-of-experts layer for a few tokens (moe.cu)
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMaxMoeExperts = 512;
+constexpr int kMoeMaxTopk = 16;
+constexpr int kMoeMaxCtas = 160;  // more than the SMs of a GB300
+struct MoeArgs {
+  const uint16_t *x;
+  int64_t ldx;
+  const float *logits, *bias;  // logits nullptr: the caller's ids and weights
+  const int *ids_in;
+  const float *w_in;
+  int *ids_out;                // optional copies of the routing
+  float *w_out;
+  const float *s13, *s2;
+  uint16_t *y;
+  int M, E, H, I, topk;
+  int score;                   // 0 softmax, 1 sigmoid
+  int renorm;
+  float scale;
+  uint64_t wait_limit_ns;
+  int fault;                   // fault injection, as GemmArgs::fault_skip_first_load
+  // set by the launcher: the workspace's parts and the ring's stages
+  uint32_t *status, *sync;
+  uint8_t *xq, *hq;
+  float *xs, *hs, *part1, *part2;
+  int max_entries, sync_words, stages;
+};
+struct DeviceInfo;
+size_t moe_workspace(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk);
+cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *ws,
+                             const DeviceInfo &dev, cudaStream_t st);
+
 // ---------------------------------------------------------------- GEMM
 
 // kModeChannel: one FP32 scale per token (activation row) and per output

@@ -261,6 +261,39 @@ size_t lora_workspace(int64_t M, int64_t R, int64_t K) {
   return 256 + (planes * static_cast<size_t>(M) * static_cast<size_t>(R) * 4 + 255) / 256 * 256;
 }
 
+int check_moe_shape(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
+  constexpr int64_t kMax = (int64_t(1) << 31) - 1;
+  if (M < 0 || E < 1 || E > kMaxMoeExperts || H < 1 || H > 65536 || I < 1 || I > 65536 ||
+      topk < 1 || topk > kMoeMaxTopk || E * H > kMax || E * 2 * I > kMax)
+    return FP8BQ_ERR_SHAPE;
+  if (M > kMoeMaxTokens) return FP8BQ_ERR_UNSUPPORTED;
+  if (H % 16 || I % 128) return FP8BQ_ERR_ALIGN;
+  return FP8BQ_OK;
+}
+
+// Checks and the launch shared by both forms of the MoE layer (the routing's
+// own arguments are already in `a`, and checked).
+int moe_impl(MoeArgs a, const void *x, int64_t ldx, const void *w13, const float *s13,
+             const void *w2, const float *s2, void *y, int64_t M, int64_t E, int64_t H, int64_t I,
+             int64_t topk, void *ws, size_t ws_bytes, cudaStream_t st) {
+  if (!w13 || !s13 || !w2 || !s2 || !y) return FP8BQ_ERR_NULL;
+  RETURN_IF(check_act(x, M, H, ldx, 16));
+  if (!aligned(w13, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(s13, 4) ||
+      !aligned(s2, 4))
+    return FP8BQ_ERR_ALIGN;
+  if (!ws || ws_bytes < moe_workspace(M, E, H, I, topk)) return FP8BQ_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  a.x = static_cast<const uint16_t *>(x), a.ldx = ldx;
+  a.s13 = s13, a.s2 = s2, a.y = static_cast<uint16_t *>(y);
+  a.M = static_cast<int>(M), a.E = static_cast<int>(E), a.H = static_cast<int>(H);
+  a.I = static_cast<int>(I), a.topk = static_cast<int>(topk);
+  a.wait_limit_ns = wait_limit_ns();
+  a.fault = fault_skip_first_load();
+  return finish_launch(0, launch_moe_layer(a, w13, w2, ws, dev, st));
+}
+
 int empty_batch(int64_t K, int64_t N) { return (K >= 1 && N >= 1) ? FP8BQ_OK : FP8BQ_ERR_SHAPE; }
 
 int check_parts(const int64_t *parts, int n_parts, int64_t N) {
@@ -969,6 +1002,46 @@ int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, con
   p.M = M, p.N = static_cast<int>(N), p.K = static_cast<int>(K);
   p.L = static_cast<int>(L), p.R = static_cast<int>(R);
   return finish_launch(0, launch_lora_add(p, dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8bq_moe_workspace_bytes(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
+  if (check_moe_shape(M, E, H, I, topk) != FP8BQ_OK) return 256;
+  return moe_workspace(M, E, H, I, topk);
+}
+
+int fp8bq_moe_layer(const void *x, int64_t ldx, const float *logits, const float *bias, int score,
+                    int renormalize, float routed_scale, int64_t topk, const void *w13,
+                    const float *s13, const void *w2, const float *s2, void *y,
+                    int32_t *ids_out, float *weights_out, int64_t M, int64_t E, int64_t H,
+                    int64_t I, void *ws, size_t ws_bytes, void *stream) {
+  RETURN_IF(check_moe_shape(M, E, H, I, topk));
+  if (topk > E) return FP8BQ_ERR_SHAPE;
+  if ((score != FP8BQ_MOE_SOFTMAX && score != FP8BQ_MOE_SIGMOID) ||
+      (bias && score != FP8BQ_MOE_SIGMOID))
+    return FP8BQ_ERR_UNSUPPORTED;
+  if (M == 0) return FP8BQ_OK;
+  if (!logits) return FP8BQ_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids_out, 4) || !aligned(weights_out, 4))
+    return FP8BQ_ERR_ALIGN;
+  MoeArgs a = {};
+  a.logits = logits, a.bias = bias, a.score = score, a.renorm = renormalize != 0;
+  a.scale = routed_scale, a.ids_out = ids_out, a.w_out = weights_out;
+  return moe_impl(a, x, ldx, w13, s13, w2, s2, y, M, E, H, I, topk, ws, ws_bytes,
+                  static_cast<cudaStream_t>(stream));
+}
+
+int fp8bq_moe_experts(const void *x, int64_t ldx, const int32_t *ids, const float *weights,
+                      int64_t topk, const void *w13, const float *s13, const void *w2,
+                      const float *s2, void *y, int64_t M, int64_t E, int64_t H, int64_t I,
+                      void *ws, size_t ws_bytes, void *stream) {
+  RETURN_IF(check_moe_shape(M, E, H, I, topk));
+  if (M == 0) return FP8BQ_OK;
+  if (!ids || !weights) return FP8BQ_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(weights, 4)) return FP8BQ_ERR_ALIGN;
+  MoeArgs a = {};
+  a.ids_in = ids, a.w_in = weights;
+  return moe_impl(a, x, ldx, w13, s13, w2, s2, y, M, E, H, I, topk, ws, ws_bytes,
+                  static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

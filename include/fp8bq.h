@@ -490,6 +490,55 @@ FP8BQ_API int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const vo
                              int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
                              void *ws, size_t ws_bytes, void *stream);
 
+/* Router scores of fp8bq_moe_layer. */
+enum { FP8BQ_MOE_SOFTMAX = 0, FP8BQ_MOE_SIGMOID = 1 };
+
+/* A whole mixture-of-experts layer for at most 64 tokens in one launch, over
+ * the expert weights of fp8bq_grouped_gemm (w13 [E, 2I, H], w2 [E, H, I]).
+ * Per token i:
+ *   route   the topk experts with the largest logits (a tie goes to the lower
+ *           index; with `bias`, the largest sigmoid(logit) + bias), weight
+ *           w = softmax over all E logits, or sigmoid(logit), of the expert;
+ *           renormalize != 0 divides by the sum over the chosen; times
+ *           routed_scale.  NaN and -inf logits are never chosen: a token with
+ *           fewer usable experts than topk takes those (id -1 and weight 0 in the
+ *           places left), one with none gets y = 0.
+ *   x       group-128 codes q = RNE_sat(x / s), s = max(max|x|, 1e-10) * RN(1/448)
+ *           in binary32 (fp8bq_quant_act's rule with a product for its division;
+ *           the codes stay inside the layer)
+ *   g, u    rows 0 .. I-1 and I .. 2I-1 of w13[e] times x, as fp8bq_grouped_gemm
+ *           up to its BF16 rounding, which is left out
+ *   h       = g / (1 + exp(-g)) * u in FP32, quantised by the same rule
+ *   y       = BF16(sum_k w_k (w2[e_k] h_k))
+ * x: BF16 [M, H] pitch ldx; logits: FP32 [M, E]; bias: FP32 [E] or NULL
+ * (FP8BQ_MOE_SIGMOID only); w13: E4M3 [E, 2I, H], s13: FP32
+ * [E][2I/128][ceil(H/128)]; w2: E4M3 [E, H, I], s2: FP32
+ * [E][ceil(H/128)][I/128]; y: BF16 [M, H]; ids_out: int32 [M, topk] and
+ * weights_out: FP32 [M, topk], or NULL.  Results do not vary between calls.
+ * M <= 64 (ERR_UNSUPPORTED; for more tokens, fp8bq_grouped_gemm), E <= 512,
+ * topk <= min(E, 16), H and I <= 65536 (ERR_SHAPE), H % 16 == 0, I % 128 == 0
+ * (ERR_ALIGN).  Workspace: fp8bq_moe_workspace_bytes(M, E, H, I, topk), zeroed
+ * once with fp8bq_workspace_init.  The launch is cooperative (one CTA an SM;
+ * ERR_CUDA where the device cannot hold it). */
+FP8BQ_API int fp8bq_moe_layer(const void *x, int64_t ldx, const float *logits, const float *bias,
+                              int score, int renormalize, float routed_scale, int64_t topk,
+                              const void *w13, const float *s13, const void *w2, const float *s2,
+                              void *y, int32_t *ids_out, float *weights_out, int64_t M, int64_t E,
+                              int64_t H, int64_t I, void *ws, size_t ws_bytes, void *stream);
+
+/* The same layer for tokens that are routed already: ids int32 [M, topk]
+ * (an id outside [0, E), such as an expert of another rank, is left out) and
+ * weights FP32 [M, topk]; one expert may stand twice in a row. */
+FP8BQ_API int fp8bq_moe_experts(const void *x, int64_t ldx, const int32_t *ids,
+                                const float *weights, int64_t topk, const void *w13,
+                                const float *s13, const void *w2, const float *s2, void *y,
+                                int64_t M, int64_t E, int64_t H, int64_t I, void *ws,
+                                size_t ws_bytes, void *stream);
+
+/* Workspace bytes of both forms (256 for sizes that they refuse). */
+FP8BQ_API size_t fp8bq_moe_workspace_bytes(int64_t M, int64_t E, int64_t H, int64_t I,
+                                           int64_t topk);
+
 /* ------------------------------------------------ weight / calibration set-up */
 
 /* 128x128 block quantisation of a BF16 weight [N, K] (pitch ldw) into E4M3
