@@ -145,7 +145,7 @@ struct MoeArgs {
   // set by the launcher: the workspace's parts and the ring's stages
   uint32_t *status, *sync;
   uint8_t *xq, *hq;
-  float *xs, *hs, *part1, *part2;
+  float *xs, *hs, *sums, *out, *part1, *part2;
   int max_entries, sync_words, stages;
 };
 struct DeviceInfo;
