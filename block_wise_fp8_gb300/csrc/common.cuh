@@ -145,8 +145,8 @@ struct MoeArgs {
   // set by the launcher: the workspace's parts and the ring's stages
   uint32_t *status, *sync;
   uint8_t *xq, *hq;
-  float *xs, *hs, *sums, *out, *part1, *part2;
-  int max_entries, sync_words, stages;
+  float *xs, *hs, *sums, *out;
+  int max_entries, sync_words, stages, planes;
 };
 struct DeviceInfo;
 size_t moe_workspace(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk);

@@ -20,19 +20,20 @@
 // produce them have published them.  Across each dependency (quantised x, the
 // experts' h) the ring fills with weights instead of draining.
 //
-// Both products are cut into steps of two 128 x 128 weight tiles that share an
-// activation tile (gate and up rows of 128 hidden columns; two tiles of 128
-// output rows), and the steps into runs that a CTA takes whole: one long run
-// each, and short ones that whoever is done first takes (dealt equally in
-// advance, the slowest SMs finished up to a third later than the rest: 276
-// against 240 us for 16 tokens of 32 experts of 7168 x 2048).  The epilogue
-// warps leave each sum, or their part of one that a run's end cuts, in the
-// workspace and go on; they wait for nobody but the tensor core.  Two warps of
-// a CTA that the unit names join the parts of the first product, in run order,
-// and make h of them; the parts of the second are joined when all is done, each
-// CTA taking its share of the outputs.  The runs' bounds and every order of
-// addition follow from the sizes and the routing alone, so results repeat bit
-// for bit whoever took which run.
+// Both products are cut into units -- 128 hidden columns of an expert (its gate
+// and up rows), or two 128-row tiles of its output -- and a unit's sum over K
+// into runs of a few steps; a step is two 128 x 128 weight tiles that share an
+// activation tile.  CTAs take the runs in turn: all of the first product, expert
+// by expert, then the second's in the same order, so that the first experts' h
+// is long finished when the second product begins.  (Dealt equally in advance,
+// the slowest SMs finished up to a third later than the rest: 276 against 240 us
+// for 16 tokens of 32 experts of 7168 x 2048.)  The epilogue warps leave a run's
+// sums in the workspace and go on; they wait for nobody but the tensor core.
+// Two warps of a CTA that the unit names add the runs' sums of the first product
+// and make h of them; those of the second are added when all is done, each CTA
+// taking its share of the outputs.  The runs' bounds and every order of addition
+// follow from the sizes and the routing alone, so results repeat bit for bit
+// whoever took which run.
 //
 // The tensor core sees the weights as the 128 rows of A and up to NT tokens as
 // the columns of B (tcgen05.mma, M = 128).  In the first product the columns
@@ -51,12 +52,13 @@
 namespace fp8bq {
 namespace {
 
-// Warps: 0 weight copies, 2 activation copies, 1, 3 and 12 MMA issuers, 4 to 11
-// the epilogue, 13 idle, 14 and 15 finish h.  One MMA instruction of so few
-// columns takes its issuer about 0.06 us: a single issuer set the pace (0.75 us
-// for a step's eight, HBM half idle), so three take the stages in turn.
+// Warps: 0 weight copies, 2 activation copies, 1 and 3 MMA issuers, 4 to 11 the
+// epilogue, 12 signals, 13 scales, 14 and 15 finish h.  One MMA instruction of so
+// few columns takes its issuer about 0.06 us: a single issuer set the pace (0.75
+// us for a step's eight, HBM half idle), so two take the stages in turn.
 constexpr int kMoeThreads = 512;
-constexpr int kIssuers = 3;
+constexpr int kIssuers = 2;
+constexpr int kSignals = 4;
 constexpr int kEpi = 256;
 constexpr int kEpiWarps = 8;
 constexpr int kTileBytes = 128 * 128;
@@ -135,40 +137,26 @@ struct Entry {
   int e, row, n;
 };
 
-// How `steps` steps are cut into runs.  Run c < parts is CTA c's own; together
-// they hold `fixed` steps, all of them where a CTA's share is small, else three
-// fifths.  The runs after them, of q steps, are taken in turn.
-struct Deal {
-  uint32_t steps, parts, fixed, q, runs;
-  __device__ __forceinline__ Deal(int steps_, int ctas, int q_min) {
-    steps = steps_, parts = min(steps_, ctas);
-    const bool small = steps_ < 12 * ctas;
-    fixed = small ? steps : steps / 5 * 3;
-    q = max(q_min, (steps_ + 12 * ctas - 1) / (12 * ctas));
-    runs = parts + (steps - fixed + q - 1) / q;
-  }
-  // Products below stay below 2^32: no GPU's memory holds 2^24 steps' weights.
-  __device__ __forceinline__ int begin(uint32_t c) const {  // also the end of run c - 1
-    if (c >= runs) return steps;
-    return c <= parts ? (parts ? c * fixed / parts : 0)
-                      : fixed + (c - parts) * q;
-  }
-  __device__ __forceinline__ int owner(uint32_t s) const {  // the run that has step s
-    return s < fixed ? ((s + 1) * parts - 1) / fixed : parts + (s - fixed) / q;
-  }
-};
-constexpr int kMaxRuns = 960;  // 160 + 0.4 * 12 * 160, rounded up
+// Runs a unit of KB steps is cut into: runs of about 12 steps, or shorter ones
+// where all units together give a CTA less than 12 steps; `most` bounds the
+// workspace.
+__device__ __forceinline__ int runs_of(int KB, int units, int ctas, int most) {
+  const int each = (units * KB + ctas - 1) / ctas;
+  return min(most, (KB + (each < 12 ? max(each, 1) : 12) - 1) / (each < 12 ? max(each, 1) : 12));
+}
 
-// What the weight warp hands to the others: a run of one of the products.
+// What the weight warp hands to the others: a run of one of the products
+// (0: no more), K blocks kb .. kb + steps - 1 of entry ei's unit `sub`, whose
+// sums go to plane `plane`.
 struct Run {
-  int product;  // 1, 2; 0: no more
-  int id, begin, end;
+  int product, ei, sub, plane, kb, steps;
 };
 
 struct MoeBars {
   uint64_t full_w[kMaxRing], full_b[kMaxRing], empty[kMaxRing];
   uint64_t tfull[kMaxRing], tempty[kMaxRing];
   uint64_t run_full[kRunQueue], run_empty[kRunQueue];
+  uint64_t sig[kSignals], sig_free[kSignals];
   uint64_t drain;
   Run run[kRunQueue];
   uint32_t tmem;
@@ -299,19 +287,6 @@ __device__ void route_tokens(const MoeArgs &a, int t0, int step, short *id, floa
 
 // ---------------------------------------------------------------- the kernel
 
-// A part of a cut sum, [rows][256]: a run is cut at most in its first unit (slot
-// 0) and in its last.
-__device__ __forceinline__ int64_t part_at(int run, int slot, int rows) {
-  return (static_cast<int64_t>(run) * 2 + slot) * rows * 256;
-}
-// The runs that hold unit u's sum, and the slot of the first one's part (the
-// others begin inside the unit: slot 0).
-struct Parts {
-  int c0, c1, slot0;
-  __device__ __forceinline__ Parts(const Deal &d, int u, int KB)
-      : c0(d.owner(u * KB)), c1(d.owner(u * KB + KB - 1)), slot0(d.begin(c0) / KB == u ? 0 : 1) {}
-};
-
 // One hidden row's 128 columns of group g by a warp: h = silu(gate) * up, codes
 // and scale.
 __device__ void hidden_row(const MoeArgs &a, float4 gate, float4 up, int row, int g, int pairs) {
@@ -349,10 +324,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   volatile uint32_t *never = &bars.never;
   const int pairs = a.M * a.topk;
   const int KB1 = (a.H + 127) / 128, G1 = a.I / 128, KB2 = G1;
-  const int J = (a.H + 255) / 256, rows = min(a.M, NT);
+  const int J = (a.H + 255) / 256;
 
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float *wgt = reinterpret_cast<float *>(ring + a.stages * kStage);  // [M][16]: weight by choice
+  float *scl = reinterpret_cast<float *>(ring + a.stages * kStage);  // [stages][2][NT] scales
+  float *wgt = scl + a.stages * 2 * NT;                     // [M][16]: weight by choice
   float *wrow = wgt + a.M * kMoeMaxTopk;                    // [pairs]: by hidden row
   Entry *ent = reinterpret_cast<Entry *>(wrow + pairs);     // [max_entries]
   uint32_t *mask = reinterpret_cast<uint32_t *>(ent + a.max_entries);  // [E][2]: tokens' bits
@@ -360,16 +336,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   short *ids = reinterpret_cast<short *>(first + a.E);      // [M][16], -1: none
   short *row_of = ids + a.M * kMoeMaxTopk;                  // [M][16]: hidden row, -1: none
   short *tok = row_of + a.M * kMoeMaxTopk;                  // [pairs]: token of a hidden row
-  short *ent_of = tok + pairs;                              // [pairs]: its entry
 
   uint32_t *const all_quant = a.sync;       // CTAs whose share of x is quantised
-  uint32_t *const all_done = a.sync + 1;    // epilogue warps without a run left
+  uint32_t *const all_done = a.sync + 1;    // CTAs without a run left
   uint32_t *const leaving = a.sync + 2;
-  uint32_t *const claim1 = a.sync + 3;      // short runs taken
-  uint32_t *const claim2 = a.sync + 4;
+  uint32_t *const claim = a.sync + 3;       // runs taken, past the first round
   uint32_t *const units_done = a.sync + 5;  // hidden groups published,
   uint32_t *const ready = a.sync + 32;      // [entries]: by entry
-  uint32_t *const unit_cnt = ready + a.max_entries;  // [entries * G1]: sums left, by epilogue warp
+  uint32_t *const unit_cnt = ready + a.max_entries;  // [entries * G1]: runs done
   const uint32_t quant_ctas = min(ctas, a.M * KB1);
 
   if (tid == 0) {
@@ -379,12 +353,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       mbar_init(&bars.empty[i], 1);
     }
     for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&bars.tfull[i], 1);
+      mbar_init(&bars.tfull[i], 2);  // the products, and the scales
       mbar_init(&bars.tempty[i], kEpiWarps);
     }
     for (int i = 0; i < kRunQueue; ++i) {
       mbar_init(&bars.run_full[i], 1);
-      mbar_init(&bars.run_empty[i], 1 + kIssuers + kEpiWarps);
+      mbar_init(&bars.run_empty[i], 3 + kIssuers + kEpiWarps);
+    }
+    for (int i = 0; i < kSignals; ++i) {
+      mbar_init(&bars.sig[i], kEpiWarps);
+      mbar_init(&bars.sig_free[i], 1);
     }
     mbar_init(&bars.drain, kIssuers);
     bars.abort = 0;
@@ -466,10 +444,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       if (e >= a.E) break;
       const int n = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
       first[e] = rr;
-      for (int k = 0; k < n; k += NT, ++ee) {
-        ent[ee] = Entry{e, rr + k, min(NT, n - k)};
-        for (int r = k; r < min(n, k + NT); ++r) ent_of[rr + r] = static_cast<short>(ee);
-      }
+      for (int k = 0; k < n; k += NT) ent[ee++] = Entry{e, rr + k, min(NT, n - k)};
       rr += n;
     }
   }
@@ -505,7 +480,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
 
   const int A = bars.entries;
-  const Deal d1(A * G1 * KB1, ctas, 6), d2(J * A * KB2, ctas, 4);
+  const int R1 = runs_of(KB1, A * G1, ctas, a.planes), R2 = runs_of(KB2, A * J, ctas, a.planes);
+  // a plane holds one run of every sum, by hidden row (and a spare row)
+  const int64_t plane1 = static_cast<int64_t>(pairs + 1) * 2 * a.I;
+  const int64_t plane2 = static_cast<int64_t>(pairs) * a.H;
+  const int all1 = A * G1 * R1, all_runs = all1 + A * J * R2;
   const uint32_t tmem = bars.tmem;
 
   if (warp == 0) {
@@ -532,36 +511,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         ++it;
         if (++st == a.stages) st = 0, ph ^= 1;
       };
-      for (uint32_t c = cta; c < d1.runs && ok;) {
-        const int b = d1.begin(c), e = d1.begin(c + 1);
-        hand(Run{1, static_cast<int>(c), b, e});
-        int u = b / KB1, kb = b - u * KB1, ei = u / G1, g = u - ei * G1;
-        for (int left = e - b; left > 0 && ok;) {
-          const int r = ent[ei].e * 2 * a.I + g * 128;
-          const float *sc = a.s13 + (static_cast<int64_t>(ent[ei].e) * 2 * G1 + g) * KB1 + kb;
-          prefetch_l2(sc);
-          prefetch_l2(sc + G1 * KB1);
-          for (; kb < KB1 && left > 0 && ok; ++kb, --left) stage(&map13, kb, r, r + a.I, true);
-          kb = 0;
-          if (++g == G1) g = 0, ++ei;
-        }
-        c = d1.runs > d1.parts ? d1.parts + atomicAdd(claim1, 1u) : d1.runs;
+      for (int pos = cta; pos < all_runs && ok;) {
+        const int next = ctas + static_cast<int>(atomicAdd(claim, 1u));
+        const bool one = pos < all1;
+        const int KB = one ? KB1 : KB2, R = one ? R1 : R2, U = one ? G1 : J;
+        const int q = one ? pos : pos - all1, u = q / R;
+        Run run;
+        run.product = one ? 1 : 2, run.plane = q - u * R;
+        run.ei = u / U, run.sub = u - run.ei * U;
+        run.kb = run.plane * KB / R, run.steps = (run.plane + 1) * KB / R - run.kb;
+        hand(run);
+        const int64_t e = ent[run.ei].e;
+        const int nb2 = (a.H + 127) / 128;
+        const float *sc = (one ? a.s13 + (e * 2 * G1 + run.sub) * KB1 : a.s2 + (e * nb2 + 2 * run.sub) * KB2) + run.kb;
+        prefetch_l2(sc);
+        if (one || run.sub * 2 + 1 < nb2) prefetch_l2(sc + (one ? G1 * KB1 : KB2));
+        const int r = static_cast<int>(one ? e * 2 * a.I + run.sub * 128 : e * a.H + run.sub * 256);
+        const CUtensorMap *map = one ? &map13 : &map2;
+        for (int i = 0; i < run.steps && ok; ++i)
+          stage(map, run.kb + i, r, one ? r + a.I : r + 128, one || run.sub * 256 + 128 < a.H);
+        pos = next;
       }
-      for (uint32_t c = cta; c < d2.runs && ok;) {
-        const int b = d2.begin(c), e = d2.begin(c + 1);
-        hand(Run{2, static_cast<int>(c), b, e});
-        int u = b / KB2, kb = b - u * KB2, j = u / A, ei = u - j * A;
-        for (int left = e - b; left > 0 && ok;) {
-          const int r = ent[ei].e * a.H + j * 256;
-          const bool two = j * 256 + 128 < a.H;
-          prefetch_l2(a.s2 + (static_cast<int64_t>(ent[ei].e) * ((a.H + 127) / 128) + 2 * j) * KB2);
-          for (; kb < KB2 && left > 0 && ok; ++kb, --left) stage(&map2, kb, r, r + 128, two);
-          kb = 0;
-          if (++ei == A) ei = 0, ++j;
-        }
-        c = d2.runs > d2.parts ? d2.parts + atomicAdd(claim2, 1u) : d2.runs;
-      }
-      if (ok) hand(Run{0, 0, 0, 0});
+      if (ok) hand(Run{0, 0, 0, 0, 0, 0});
       if (!ok)  // let the copies in flight land before this CTA's memory is given up
         for (int i = max(a.fault && cta == 0 ? 1 : 0, it - a.stages); i < it; ++i)
           mbar_wait(&bars.full_w[i % a.stages], (i / a.stages) & 1, never, limit);
@@ -579,35 +550,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         mbar_arrive(&bars.run_empty[qi]);
         if (++qi == kRunQueue) qi = 0, qph ^= 1;
         if (run.product == 0) break;
-        const CUtensorMap *map = run.product == 1 ? &mapx : &maph;
-        const int KB = run.product == 1 ? KB1 : KB2;
-        if (run.product == 1 && !quantised) {
-          ok = quantised = wait_count(all_quant, quant_ctas, abort, limit);
-          fence_proxy_async_all();
+        const CUtensorMap *map = &mapx;
+        int row = 0, boxes = xboxes;
+        if (run.product == 1) {
+          if (!quantised) {
+            ok = quantised = wait_count(all_quant, quant_ctas, abort, limit);
+            fence_proxy_async_all();
+          }
+        } else {
+          if (!hidden) {
+            hidden = ld_acquire_gpu(units_done) >= static_cast<uint32_t>(A * G1);
+            if (!hidden) ok = wait_count(&ready[run.ei], G1, abort, limit);
+            fence_proxy_async_all();
+          }
+          map = &maph, row = ent[run.ei].row, boxes = (ent[run.ei].n + 15) / 16;
         }
-        int u = run.begin / KB, kb = run.begin - u * KB, ei = u % A;
-        for (int left = run.end - run.begin; left > 0 && ok;) {
-          int row = 0, boxes = xboxes;
-          if (run.product == 2) {
-            if (!hidden) {
-              hidden = ld_acquire_gpu(units_done) >= static_cast<uint32_t>(A * G1);
-              if (!hidden) ok = wait_count(&ready[ei], G1, abort, limit);
-              fence_proxy_async_all();
-            }
-            row = ent[ei].row, boxes = (ent[ei].n + 15) / 16;
-          }
-          for (; kb < KB && left > 0 && ok; ++kb, --left) {
-            ok = mbar_wait(&bars.empty[st], ph, abort, limit);
-            if (!ok) break;
-            uint8_t *dst = ring + st * kStage + 2 * kTileBytes;
-            mbar_arrive_expect_tx(&bars.full_b[st], boxes * 2048);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(dst + i * 2048, map, &bars.full_b[st], kb * 128, row + i * 16);
-            ++it;
-            if (++st == a.stages) st = 0, ph ^= 1;
-          }
-          kb = 0;
-          if (++ei == A) ei = 0;
+        for (int i = 0; i < run.steps && ok; ++i) {
+          ok = mbar_wait(&bars.empty[st], ph, abort, limit);
+          if (!ok) break;
+          uint8_t *dst = ring + st * kStage + 2 * kTileBytes;
+          mbar_arrive_expect_tx(&bars.full_b[st], boxes * 2048);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(dst + b * 2048, map, &bars.full_b[st], (run.kb + i) * 128, row + b * 16);
+          ++it;
+          if (++st == a.stages) st = 0, ph ^= 1;
         }
       }
       if (!ok)
@@ -615,12 +581,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           mbar_wait(&bars.full_b[i % a.stages], (i / a.stages) & 1, never, limit);
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 3 || warp == 12) {
+  } else if (warp == 1 || warp == 3) {
     if (lane == 0) {  // ---- MMAs
       // A stage, and the TMEM buffer of the same number, belong to one issuer:
       // a parity wait tells two phases apart, not three, so whoever waits for
       // a stage's phase must have seen the one before.
-      const int st0 = warp < 4 ? warp >> 1 : warp - 10;
+      const int st0 = warp >> 1;
       int st = st0, ph = 0, it = st0;  // this issuer's next step
       int it0 = 0, qi = 0, qph = 0;    // the run's first step
       bool ok = true;
@@ -631,22 +597,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         mbar_arrive(&bars.run_empty[qi]);
         if (++qi == kRunQueue) qi = 0, qph ^= 1;
         if (run.product == 0) break;
-        const int it1 = it0 + run.end - run.begin;
-        while (it < it1 && st0 < a.stages) {
-          int n = a.M;
-          bool two = true;
-          if (run.product == 2) {
-            const int u = (run.begin + it - it0) / KB2, j = u / A;
-            n = ent[u - j * A].n;
-            two = j * 256 + 128 < a.H;
-          }
+        const int it1 = it0 + run.steps;
+        const int n = run.product == 1 ? a.M : ent[run.ei].n;
+        const bool two = run.product == 1 || run.sub * 256 + 128 < a.H;
+        const uint32_t idesc = idesc_f8f6f4_e4m3(128, (n + 15) / 16 * 16);
+        while (it < it1) {
           ok = mbar_wait(&bars.tempty[st], ph ^ 1, abort, limit) &&
                mbar_wait(&bars.full_w[st], ph, abort, limit) &&
                mbar_wait(&bars.full_b[st], ph, abort, limit);
           if (!ok) break;
           tc_fence_after();
           const uint32_t base = smem_u32(ring + st * kStage);
-          const uint32_t idesc = idesc_f8f6f4_e4m3(128, (n + 15) / 16 * 16);
           const uint64_t bd = sdesc_kmajor_sw128(base + 2 * kTileBytes);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -668,6 +629,85 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       mbar_wait(&bars.drain, 0, never, limit);
     }
     __syncwarp();
+  } else if (warp == 12) {
+    // ---- signals: a release at GPU scope takes microseconds while the weights
+    // stream (3.5 us measured; the epilogue, which did it itself, fell behind
+    // HBM), so this warp does it for the epilogue warps, a run of the first
+    // product at a time, and once more when all runs are done
+    if (lane == 0) {
+      int qi = 0, qph = 0, sg = 0, sph = 0;
+      bool more = true;
+      while (more && mbar_wait(&bars.run_full[qi], qph, abort, limit)) {
+        const Run run = bars.run[qi];
+        mbar_arrive(&bars.run_empty[qi]);
+        if (++qi == kRunQueue) qi = 0, qph ^= 1;
+        more = run.product != 0;
+        if (run.product == 2) continue;
+        if (!mbar_wait(&bars.sig[sg], sph, abort, limit)) break;
+        red_release_gpu(more ? &unit_cnt[run.ei * G1 + run.sub] : all_done, 1);
+        mbar_arrive(&bars.sig_free[sg]);
+        if (++sg == kSignals) sg = 0, sph ^= 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 13) {
+    // ---- scales: per step, weight tile and row the product of the weight
+    // block's scale and the row's, loaded three steps before they are stored
+    int st = 0, ph = 1, qi = 0, qph = 0;
+    bool quantised = false, hidden = false;
+    const int nbs2 = (a.H + 127) / 128;
+    while (__all_sync(0xFFFFFFFFu, mbar_wait(&bars.run_full[qi], qph, abort, limit))) {
+      const Run run = bars.run[qi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.run_empty[qi]);
+      if (++qi == kRunQueue) qi = 0, qph ^= 1;
+      if (run.product == 0) break;
+      const bool one = run.product == 1;
+      const Entry en = ent[run.ei];
+      if (one ? !quantised : !hidden) {
+        if (one) {
+          wait_count(all_quant, quant_ctas, abort, limit);
+          quantised = true;
+        } else {
+          hidden = __all_sync(0xFFFFFFFFu,
+                              ld_acquire_gpu(units_done) >= static_cast<uint32_t>(A * G1));
+          if (!hidden) wait_count(&ready[run.ei], G1, abort, limit);
+        }
+        __syncwarp();
+      }
+      {
+        const float *w0 = one ? a.s13 + (static_cast<int64_t>(en.e) * 2 * G1 + run.sub) * KB1
+                              : a.s2 + (static_cast<int64_t>(en.e) * nbs2 + 2 * run.sub) * KB2;
+        const float *w1 = one ? w0 + G1 * KB1 : 2 * run.sub + 1 < nbs2 ? w0 + KB2 : w0;
+        const float *x = one ? a.xs + (lane < en.n ? tok[en.row + lane] : 0) : a.hs + en.row + lane;
+        const int xstride = one ? a.M : pairs + 1, kb0 = run.kb, kb1 = run.kb + run.steps;
+        const bool mine = lane < en.n;
+        struct Three {
+          float x, w0, w1;
+        };
+        auto load = [&](int kb) {
+          Three v = {0.0f, 0.0f, 0.0f};
+          if (kb < kb1 && mine)
+            v = Three{__ldcg(x + kb * xstride), __ldg(w0 + kb), __ldg(w1 + kb)};
+          return v;
+        };
+        Three v0 = load(kb0), v1 = load(kb0 + 1), v2 = load(kb0 + 2);
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const Three v = v0;
+          v0 = v1, v1 = v2, v2 = load(kb + 3);
+          mbar_wait(&bars.tempty[st], ph, abort, limit);
+          __syncwarp();
+          if (lane < NT) {
+            scl[st * 2 * NT + lane] = v.x * v.w0;
+            scl[st * 2 * NT + NT + lane] = v.x * v.w1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.tfull[st]);
+          if (++st == a.stages) st = 0, ph ^= 1;
+        }
+      }
+    }
   } else if (warp >= 14) {
     // ---- h from the first product's sums: units cta, cta + ctas, ...; a warp a
     // row, four hidden columns a lane.  The first round is a rehearsal on a spare
@@ -675,24 +715,22 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     // swept it from since the last call, while these warps are idle.
     for (int u = cta - ctas; u < A * G1; u += ctas) {
       const bool real = u >= 0;
-      const Parts p(d1, real ? u : 0, KB1);
       const int ei = real ? u / G1 : 0, g = real ? u - ei * G1 : 0;
       const Entry en = real ? ent[ei] : Entry{0, pairs, 2};
-      if (real) wait_count(&unit_cnt[u], (p.c1 - p.c0 + 1) * kEpiWarps, abort, limit);
+      if (real) wait_count(&unit_cnt[u], R1, abort, limit);
       __syncwarp();
 #pragma unroll 1
       for (int n = warp - 14; n < en.n; n += 2) {
         float4 gate = make_float4(0.0f, 0.0f, 0.0f, 0.0f), up = gate;
+        const float *src = a.sums + static_cast<int64_t>(real ? en.row + n : pairs) * 2 * a.I +
+                           g * 128 + lane * 4;
 #pragma unroll 4
-        for (int c = p.c0; c <= p.c1; ++c) {
-          const float *src = a.part1 + part_at(c, c == p.c0 ? p.slot0 : 0, rows) + n * 256;
-          int far = 128;
-          if (p.c0 == p.c1)  // whole
-            src = a.sums + static_cast<int64_t>(en.row + (real ? n : 0)) * 2 * a.I + g * 128, far = a.I;
-          const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + lane * 4));
-          const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + far + lane * 4));
+        for (int c = 0; c < R1; ++c) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+          const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + a.I));
           gate.x += x.x, gate.y += x.y, gate.z += x.z, gate.w += x.w;
           up.x += y.x, up.y += y.y, up.z += y.z, up.w += y.w;
+          src += plane1;
         }
         hidden_row(a, gate, up, real ? en.row + n : pairs, g, pairs);
       }
@@ -710,61 +748,61 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const uint32_t tlane =
         tmem + ((static_cast<uint32_t>(warp & 3) * 32u) << 16) + tile * kCols;
 
-    int slot = 0, phase = 0;  // the next step's TMEM buffer
+    int st = 0, ph = 0;  // the next step's stage
     float acc[NT];
-    // acc[i] = sum over K blocks [kb0, kb1) of a unit: partial sums from TMEM
-    // times the weight block's scale (wscale[kb]) and row i's (xscale[kb *
-    // xstride + xrow], xrow held by lane i).  pick: row i's TMEM column is
-    // lane i's xrow (a token), else i.
-    auto sum_blocks = [&](int n, int kb0, int kb1, const float *wscale, const float *xscale,
-                          int xstride, int xrow, bool pick, bool on) {
+    int sg = 0, sph = 1;  // the next signal
+    auto signal = [&] {
+      __syncwarp();
+      mbar_wait(&bars.sig_free[sg], sph, abort, limit);
+      if (lane == 0) mbar_arrive(&bars.sig[sg]);
+      if (++sg == kSignals) sg = 0, sph ^= 1;
+    };
+    // acc[i] = sum over `steps` K blocks of row i's partial sums from TMEM times
+    // their scales.  pick: row i's TMEM column is lane i's xcol (a token), else i.
+    auto sum_blocks = [&](int n, int steps, int xcol, bool pick, bool on) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
-      auto xs_at = [&](int kb) {
-        return kb < kb1 && lane < n ? __ldcg(xscale + kb * xstride + xrow) : 0.0f;
-      };
-      // scales three blocks ahead
-      float x0 = xs_at(kb0), x1 = xs_at(kb0 + 1), x2 = xs_at(kb0 + 2), sw = 0.0f;
 #pragma unroll 1
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const float sx = x0;
-        x0 = x1, x1 = x2, x2 = xs_at(kb + 3);
-        if (((kb - kb0) & 31) == 0)
-          sw = on && kb + lane < kb1 ? __ldg(wscale + kb + lane) : 0.0f;
-        const int sl = slot;
-        mbar_wait(&bars.tfull[sl], phase, abort, limit);
+      for (int i = 0; i < steps; ++i) {
+        mbar_wait(&bars.tfull[st], ph, abort, limit);
         __syncwarp();
-        if (++slot == a.stages) slot = 0, phase ^= 1;
         tc_fence_after();
+        const float *sc = scl + (st * 2 + tile) * NT;
         uint32_t v[NT];
+        float w[NT];
         if (on) {
-          const uint32_t at = tlane + sl * 2 * kCols;
+          const uint32_t at = tlane + st * 2 * kCols;
           if (pick) {
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
               if (c >= n) break;
-              tmem_ld1(at + __shfl_sync(0xFFFFFFFFu, xrow, c), v[c]);
+              tmem_ld1(at + __shfl_sync(0xFFFFFFFFu, xcol, c), v[c]);
             }
           } else {
             tmem_ld16(at, v);
             if (NT > 16 && n > 16) tmem_ld16(at + 16, v + (NT > 16 ? 16 : 0));
           }
+#pragma unroll
+          for (int c = 0; c < NT; c += 4) {
+            if (c >= n) break;
+            const float4 q = *reinterpret_cast<const float4 *>(sc + c);
+            w[c] = q.x, w[c + 1] = q.y, w[c + 2] = q.z, w[c + 3] = q.w;
+          }
           tmem_ld_wait();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.tempty[sl]);
+        if (lane == 0) mbar_arrive(&bars.tempty[st]);
+        if (++st == a.stages) st = 0, ph ^= 1;
         if (!on) continue;
-        const float w = sx * __shfl_sync(0xFFFFFFFFu, sw, (kb - kb0) & 31);
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
           if (c >= n) break;
-          acc[c] = fmaf(__uint_as_float(v[c]), __shfl_sync(0xFFFFFFFFu, w, c), acc[c]);
+          acc[c] = fmaf(__uint_as_float(v[c]), w[c], acc[c]);
         }
       }
     };
 
-    bool quantised = false, hidden = false;
     int qi = 0, qph = 0;
     // (the vote: a warp leaves whole, also when a wait ran out)
     while (__all_sync(0xFFFFFFFFu, mbar_wait(&bars.run_full[qi], qph, abort, limit))) {
@@ -773,105 +811,62 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       if (lane == 0) mbar_arrive(&bars.run_empty[qi]);
       if (++qi == kRunQueue) qi = 0, qph ^= 1;
       if (run.product == 0) break;
-
-      if (run.product == 1) {
-        if (!quantised) {
-          wait_count(all_quant, quant_ctas, abort, limit);
-          __syncwarp();
-          quantised = true;
-        }
-        for (int s = run.begin; s < run.end;) {
-          const int u = s / KB1, kb0 = s - u * KB1, kb1 = min(KB1, kb0 + run.end - s);
-          const int ei = u / G1, g = u - ei * G1;
-          const Entry en = ent[ei];
-          sum_blocks(en.n, kb0, kb1,
-                     a.s13 + (static_cast<int64_t>(en.e) * 2 * G1 + tile * G1 + g) * KB1, a.xs,
-                     a.M, lane < en.n ? tok[en.row + lane] : 0, true, true);
-          float *dst;
-          int pitch;
-          if (kb1 - kb0 == KB1) {
-            dst = a.sums + static_cast<int64_t>(en.row) * 2 * a.I + tile * a.I + g * 128 + row;
-            pitch = 2 * a.I;
-          } else {
-            dst = a.part1 + part_at(run.id, run.begin / KB1 == u ? 0 : 1, rows) + et, pitch = 256;
-          }
+      const bool one = run.product == 1;
+      const Entry en = ent[run.ei];
+      sum_blocks(en.n, run.steps, one && lane < en.n ? tok[en.row + lane] : 0, one,
+                 one || run.sub * 256 + tile * 128 < a.H);
+      const int64_t pitch = one ? 2 * a.I : a.H;
+      float *dst = one ? a.sums + run.plane * plane1 + tile * a.I + run.sub * 128 + row
+                       : a.out + run.plane * plane2 + run.sub * 256 + et;
+      dst += en.row * pitch;
+      if (one || run.sub * 256 + et < a.H) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n >= en.n) break;
-            __stcg(dst + static_cast<int64_t>(n) * pitch, acc[n]);
-          }
-          __syncwarp();
-          if (lane == 0) red_release_gpu(&unit_cnt[u], 1);
-          s += kb1 - kb0;
+        for (int n = 0; n < NT; ++n) {
+          if (n >= en.n) break;
+          __stcg(dst, acc[n]);
+          dst += pitch;
         }
-        continue;
       }
-
-      for (int s = run.begin; s < run.end;) {
-        const int u = s / KB2, kb0 = s - u * KB2, kb1 = min(KB2, kb0 + run.end - s);
-        const int j = u / A, ei = u - j * A, col = j * 256 + et;
-        const Entry en = ent[ei];
-        const bool on = j * 256 + tile * 128 < a.H;
-        if (!hidden) {
-          hidden = __all_sync(0xFFFFFFFFu,
-                              ld_acquire_gpu(units_done) >= static_cast<uint32_t>(A * G1));
-          if (!hidden) wait_count(&ready[ei], G1, abort, limit);
-          __syncwarp();
-        }
-        sum_blocks(en.n, kb0, kb1,
-                   a.s2 + (static_cast<int64_t>(en.e) * ((a.H + 127) / 128) + 2 * j + tile) * KB2,
-                   a.hs, pairs + 1, en.row + lane, false, on);
-        // a whole sum is a row of `out`; a cut one a part of its run
-        float *dst;
-        int pitch;
-        if (kb1 - kb0 == KB2) {
-          dst = a.out + static_cast<int64_t>(en.row) * a.H + col, pitch = a.H;
-        } else {
-          dst = a.part2 + part_at(run.id, run.begin / KB2 == u ? 0 : 1, rows) + et, pitch = 256;
-        }
-        if (col < a.H) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n >= en.n) break;
-            __stcg(dst + static_cast<int64_t>(n) * pitch, acc[n]);
-          }
-        }
-        s += kb1 - kb0;
-      }
+      if (one) signal();
     }
+    signal();
 
     // ---- y when every run is done: 128 columns of a token a warp
-    __syncwarp();
-    if (lane == 0) red_release_gpu(all_done, 1);
-    wait_count(all_done, ctas * kEpiWarps, abort, limit);
+    wait_count(all_done, ctas, abort, limit);
     __syncwarp();
     const int blocks = (a.H + 127) / 128;
     for (int i = ew * ctas + cta; i < a.M * blocks; i += ctas * kEpiWarps) {
-      const int t = i / blocks, blk = i - t * blocks, j = blk / 2, col = blk * 128 + lane * 4;
-      // lane k finds the parts of choice k
-      const int rk = lane < kMoeMaxTopk ? row_of[t * kMoeMaxTopk + lane] : -1;
-      const int ek = rk >= 0 ? ent_of[rk] : 0;
-      const Parts pk(d2, j * A + ek, KB2);
-      const int nk = rk >= 0 ? rk - ent[ek].row : 0;
-      const float wk = rk >= 0 ? wrow[rk] : 0.0f;
+      const int t = i / blocks, col = (i - t * blocks) * 128 + lane * 4;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int k = 0; k < a.topk; ++k) {
-        const int r = __shfl_sync(0xFFFFFFFFu, rk, k), n = __shfl_sync(0xFFFFFFFFu, nk, k);
-        const int c0 = __shfl_sync(0xFFFFFFFFu, pk.c0, k), c1 = __shfl_sync(0xFFFFFFFFu, pk.c1, k);
-        const int slot0 = __shfl_sync(0xFFFFFFFFu, pk.slot0, k);
-        const float w = __shfl_sync(0xFFFFFFFFu, wk, k);
-        if (r < 0 || col >= a.H) continue;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int c = c0; c <= c1; ++c) {
-          const float *src = c0 == c1 ? a.out + static_cast<int64_t>(r) * a.H + col
-                                      : a.part2 + part_at(c, c == c0 ? slot0 : 0, rows) + n * 256 +
-                                            (blk & 1) * 128 + lane * 4;
-          const float4 q = __ldcg(reinterpret_cast<const float4 *>(src));
-          o.x += q.x, o.y += q.y, o.z += q.z, o.w += q.w;
+      if (col < a.H) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < a.topk; k0 += 4) {  // four choices' loads in flight
+          float4 o[4];
+          int r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r[i] = row_of[t * kMoeMaxTopk + k0 + i];  // -1 from topk on
+            o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+#pragma unroll 2
+          for (int c = 0; c < R2; ++c) {
+            const float *src = a.out + c * plane2 + col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (r[i] >= 0) {
+                const float4 q = __ldcg(
+                    reinterpret_cast<const float4 *>(src + static_cast<int64_t>(r[i]) * a.H));
+                o[i].x += q.x, o[i].y += q.y, o[i].z += q.z, o[i].w += q.w;
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r[i] >= 0) {
+              const float w = wrow[r[i]];
+              v.x = fmaf(w, o[i].x, v.x), v.y = fmaf(w, o[i].y, v.y);
+              v.z = fmaf(w, o[i].z, v.z), v.w = fmaf(w, o[i].w, v.w);
+            }
         }
-        v.x = fmaf(w, o.x, v.x), v.y = fmaf(w, o.y, v.y);
-        v.z = fmaf(w, o.z, v.z), v.w = fmaf(w, o.w, v.w);
       }
       const uint32_t lo = bf16_bits(v.x) | (static_cast<uint32_t>(bf16_bits(v.y)) << 16);
       const uint32_t hi = bf16_bits(v.z) | (static_cast<uint32_t>(bf16_bits(v.w)) << 16);
@@ -896,18 +891,17 @@ int tokens_per_entry(int64_t M) { return M <= 16 ? 16 : 32; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct MoeLayout {
-  size_t sync, xq, xs, hq, hs, sums, out, part1, part2, total;
-  int max_entries;
-  int sync_words;
+  size_t sync, xq, xs, hq, hs, sums, out, total;
+  int max_entries, sync_words, planes;
 };
 
 // Workspace: status word | counters | codes and scales of x (a row a
-// token) and h (a row a token and expert) | the sums of
-// both products by hidden row | parts of cut sums of both products, two for each run
+// token) and h (a row a token and expert) | the runs'
+// sums of both products, a plane for each run of a sum, by hidden row
 MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
   MoeLayout l;
   const int64_t P = M * topk, NT = tokens_per_entry(M);
-  const int64_t KB1 = (H + 127) / 128, G1 = I / 128, rows = M < NT ? M : NT;
+  const int64_t KB1 = (H + 127) / 128, G1 = I / 128;
   l.max_entries = static_cast<int>((E < P ? E : P) + P / NT);
   l.sync_words = static_cast<int>(32 + l.max_entries * (1 + G1));
   size_t at = 256;
@@ -921,10 +915,10 @@ MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
   l.xs = take(M * KB1 * 4);
   l.hq = take((P + 1) * I);  // and a spare row
   l.hs = take((P + 1) * G1 * 4);
-  l.sums = take((P + 1) * 2 * I * 4);
-  l.out = take(P * H * 4);
-  l.part1 = take(static_cast<int64_t>(kMaxRuns) * 2 * rows * 256 * 4);
-  l.part2 = take(static_cast<int64_t>(kMaxRuns) * 2 * rows * 256 * 4);
+  l.planes = M <= 16 ? 8 : 4;  // most runs of a sum
+  auto planes = [&](int64_t KB) { return KB < l.planes ? KB : l.planes; };
+  l.sums = take(planes(KB1) * (P + 1) * 2 * I * 4);
+  l.out = take(planes(G1) * P * H * 4);
   l.total = at;
   return l;
 }
@@ -948,16 +942,15 @@ cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *w
   a.hs = reinterpret_cast<float *>(base + l.hs);
   a.sums = reinterpret_cast<float *>(base + l.sums);
   a.out = reinterpret_cast<float *>(base + l.out);
-  a.part1 = reinterpret_cast<float *>(base + l.part1);
-  a.part2 = reinterpret_cast<float *>(base + l.part2);
+  a.planes = l.planes;
   a.max_entries = l.max_entries;
   a.sync_words = l.sync_words;
   const int64_t P = static_cast<int64_t>(a.M) * a.topk, KB1 = (a.H + 127) / 128;
   const int NT = tokens_per_entry(a.M);
-  const size_t fixed = 1024 + static_cast<size_t>(a.M) * kMoeMaxTopk * 8 + P * 8 +
+  const size_t fixed = 1024 + static_cast<size_t>(a.M) * kMoeMaxTopk * 8 + P * 6 +
                        static_cast<size_t>(l.max_entries) * sizeof(Entry) +
                        static_cast<size_t>(a.E) * 12;
-  const size_t stage = NT == 16 ? MoeCfg<16>::kStage : MoeCfg<32>::kStage;
+  const size_t stage = (NT == 16 ? MoeCfg<16>::kStage : MoeCfg<32>::kStage) + 2 * NT * 4;
   const size_t room = dev.max_smem_optin - 1024;  // the static part
   a.stages = static_cast<int>((room - fixed) / stage);
   const int most = NT == 16 ? MoeCfg<16>::kMaxStages : MoeCfg<32>::kMaxStages;
