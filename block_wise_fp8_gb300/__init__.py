@@ -188,6 +188,7 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
+_POS = (torch.int32, torch.int64)
 
 
 def _kb(K: int) -> int:
@@ -604,16 +605,58 @@ def fp8bq_grouped_gemm_masked(q, s_x, w, s_w, masked_m, y, ws, s_layout: int = S
 
 
 # ---------------------------------------------------------------- beside the linears
+#
+# Calls of a few microseconds: the checks first run as plain comparisons (about
+# 0.4 us a tensor), and `_validate`, which names what is wrong, only where one
+# of them fails.
+
+def _fits(dev, contig, rows=()):
+    """Whether every (tensor, dtypes, shape) of `contig` is a contiguous tensor,
+    and of `rows` a matrix with unit column stride, of that type and shape on
+    device `dev`."""
+    try:
+        for t, dtypes, shape in contig:
+            if (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or
+                    t.get_device() != dev):
+                return False
+        for t, dtypes, shape in rows:
+            if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev:
+                return False
+            pitch, one = t.stride()
+            if one != 1 or pitch < shape[1]:
+                return False
+    except AttributeError:  # None, or no tensor
+        return False
+    return True
+
+
+def _call_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _device():
+    # before the first use of CUDA every tensor is a host one, which the checks find
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _opt_ptr(t):
+    return None if t is None else t.data_ptr()
+
 
 def _heads(t, name):
     """(tokens, heads, head size) of a 3-D argument whose shape sets the call's sizes."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a 3-D tensor [tokens, heads, head size]")
-    return (int(v) for v in t.shape)
+    return t.shape
 
 
-def _strides(t):
-    return (0, 0) if t is None else (t.stride(0), t.stride(1))
+def _fit_heads(t, shape, dev):
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        return False
+    a, b, one = t.stride()
+    return one == 1 and a >= 0 and b >= 0
 
 
 def fp8bq_qk_norm_rope(q, k, q_gamma, k_gamma, table, positions, q_out, k_out, eps: float = 1e-6,
@@ -626,25 +669,43 @@ def fp8bq_qk_norm_rope(q, k, q_gamma, k_gamma, table, positions, q_out, k_out, e
     T, HQ, D = _heads(q, "q")
     HK = 0
     if k is not None:
-        _, HK, _ = _heads(k, "k")
+        HK = _heads(k, "k")[1]
     P, rot = _mat(table, "table")
-    _validate("fp8bq_qk_norm_rope", [
-        _Spec("q", q, _BF16, (T, HQ, D), kind="heads"),
-        _Spec("k", k, _BF16, (T, HK, D), kind="heads", optional=True),
-        _Spec("q_gamma", q_gamma, _BF16, numel=D, optional=True),
-        _Spec("k_gamma", k_gamma, _BF16, numel=D, optional=True),
-        _Spec("table", table, _F32, (P, rot)),
-        _Spec("positions", positions, (torch.int32, torch.int64), (T,)),
-        _Spec("q_out", q_out, _BF16, (T, HQ, D), kind="heads"),
-        _Spec("k_out", k_out, _BF16, (T, HK, D), kind="heads", optional=k is None)], stream)
-    if k is None and k_out is not None:
-        raise ValueError("fp8bq_qk_norm_rope: k_out without k")
-    _check(_lib.fp8bq_qk_norm_rope(
-        _ptr(q), *_strides(q), HQ, _ptr(k), *_strides(k), HK, _ptr(q_gamma), _ptr(k_gamma),
-        float(eps), _ptr(table), P, rot, _ptr(positions),
-        32 if positions.dtype == torch.int32 else 64, int(interleaved), _ptr(q_out),
-        *_strides(q_out), _ptr(k_out), *_strides(k_out), T, D, _stream(stream)),
-        "fp8bq_qk_norm_rope")
+    dev = _device()
+    contig = [(table, _F32, (P, rot)), (positions, _POS, (T,))]
+    if q_gamma is not None:
+        contig.append((q_gamma, _BF16, (D,)))
+    if k_gamma is not None:
+        contig.append((k_gamma, _BF16, (D,)))
+    if not (stream is None and _fits(dev, contig) and q_out is not None and
+            _fit_heads(q, (T, HQ, D), dev) and _fit_heads(q_out, (T, HQ, D), dev) and
+            (k is None) == (k_out is None) and
+            (k is None or (_fit_heads(k, (T, HK, D), dev) and _fit_heads(k_out, (T, HK, D), dev)))):
+        _validate("fp8bq_qk_norm_rope", [
+            _Spec("q", q, _BF16, (T, HQ, D), kind="heads"),
+            _Spec("k", k, _BF16, (T, HK, D), kind="heads", optional=True),
+            _Spec("q_gamma", q_gamma, _BF16, numel=D, optional=True),
+            _Spec("k_gamma", k_gamma, _BF16, numel=D, optional=True),
+            _Spec("table", table, _F32, (P, rot)),
+            _Spec("positions", positions, _POS, (T,)),
+            _Spec("q_out", q_out, _BF16, (T, HQ, D), kind="heads"),
+            _Spec("k_out", k_out, _BF16, (T, HK, D), kind="heads", optional=k is None)], stream)
+        if k is None and k_out is not None:
+            raise ValueError("fp8bq_qk_norm_rope: k_out without k")
+    qt, qh, _ = q.stride()
+    ot, oh, _ = q_out.stride()
+    kp = kop = None
+    kt = kh = kot = koh = 0
+    if k is not None:
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        kt, kh, _ = k.stride()
+        kot, koh, _ = k_out.stride()
+    status = _lib.fp8bq_qk_norm_rope(
+        q.data_ptr(), qt, qh, HQ, kp, kt, kh, HK, _opt_ptr(q_gamma), _opt_ptr(k_gamma), eps,
+        table.data_ptr(), P, rot, positions.data_ptr(),
+        64 if positions.dtype is torch.int64 else 32, interleaved, q_out.data_ptr(), ot, oh, kop,
+        kot, koh, T, D, _call_stream(stream, dev))
+    _check(status, "fp8bq_qk_norm_rope")
 
 
 def fp8bq_lora_group(ids, order, offsets, stream=None):
@@ -654,12 +715,16 @@ def fp8bq_lora_group(ids, order, offsets, stream=None):
         raise ValueError("ids must be a 1-D tensor")
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must be a 1-D tensor of L + 1 elements")
-    M, L = ids.numel(), offsets.numel() - 1
-    _validate("fp8bq_lora_group", [
-        _Spec("ids", ids, _I32, (M,)), _Spec("order", order, _I32, (M,)),
-        _Spec("offsets", offsets, _I32, (L + 1,))], stream)
-    _check(_lib.fp8bq_lora_group(_ptr(ids), M, L, _ptr(order), _ptr(offsets), _stream(stream)),
-           "fp8bq_lora_group")
+    M, L = ids.shape[0], offsets.shape[0] - 1
+    dev = _device()
+    if stream is not None or not _fits(dev, ((ids, _I32, (M,)), (order, _I32, (M,)),
+                                             (offsets, _I32, (L + 1,)))):
+        _validate("fp8bq_lora_group", [
+            _Spec("ids", ids, _I32, (M,)), _Spec("order", order, _I32, (M,)),
+            _Spec("offsets", offsets, _I32, (L + 1,))], stream)
+    status = _lib.fp8bq_lora_group(ids.data_ptr(), M, L, order.data_ptr(), offsets.data_ptr(),
+                                   _call_stream(stream, dev))
+    _check(status, "fp8bq_lora_group")
 
 
 def fp8bq_lora_add(x, a, b, scales, order, offsets, base, y, ws, ranks=None, stream=None):
@@ -670,18 +735,31 @@ def fp8bq_lora_add(x, a, b, scales, order, offsets, base, y, ws, ranks=None, str
     N = _mat(y, "y")[1]
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
         raise ValueError("a must be a 3-D tensor [L, R, K]")
-    L, R = int(a.shape[0]), int(a.shape[1])
-    _validate("fp8bq_lora_add", [
-        _Spec("x", x, _BF16, (M, K), kind="rows"),
-        _Spec("a", a, _BF16, (L, R, K)), _Spec("b", b, _BF16, (L, N, R)),
-        _Spec("scales", scales, _F32, (L,)), _Spec("ranks", ranks, _I32, (L,), optional=True),
-        _Spec("order", order, _I32, (M,)), _Spec("offsets", offsets, _I32, (L + 1,)),
-        _Spec("base", base, _BF16, (M, N), kind="rows"),
-        _Spec("y", y, _BF16, (M, N), kind="rows"), _ws(ws)], stream)
-    _check(_lib.fp8bq_lora_add(
-        _ptr(x), _ld(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(ranks), _ptr(order), _ptr(offsets),
-        _ptr(base), _ld(base), _ptr(y), _ld(y), M, N, K, L, R, _ptr(ws), _nbytes(ws),
-        _stream(stream)), "fp8bq_lora_add")
+    L, R, _ = a.shape
+    dev = _device()
+    contig = [(a, _BF16, (L, R, K)), (b, _BF16, (L, N, R)), (scales, _F32, (L,)),
+              (order, _I32, (M,)), (offsets, _I32, (L + 1,)), (ws, _U8, (_len(ws),))]
+    if ranks is not None:
+        contig.append((ranks, _I32, (L,)))
+    if stream is not None or not _fits(dev, contig, ((x, _BF16, (M, K)), (base, _BF16, (M, N)),
+                                                     (y, _BF16, (M, N)))):
+        _validate("fp8bq_lora_add", [
+            _Spec("x", x, _BF16, (M, K), kind="rows"),
+            _Spec("a", a, _BF16, (L, R, K)), _Spec("b", b, _BF16, (L, N, R)),
+            _Spec("scales", scales, _F32, (L,)),
+            _Spec("ranks", ranks, _I32, (L,), optional=True),
+            _Spec("order", order, _I32, (M,)), _Spec("offsets", offsets, _I32, (L + 1,)),
+            _Spec("base", base, _BF16, (M, N), kind="rows"),
+            _Spec("y", y, _BF16, (M, N), kind="rows"), _ws(ws)], stream)
+    status = _lib.fp8bq_lora_add(
+        x.data_ptr(), x.stride(0), a.data_ptr(), b.data_ptr(), scales.data_ptr(), _opt_ptr(ranks),
+        order.data_ptr(), offsets.data_ptr(), base.data_ptr(), base.stride(0), y.data_ptr(),
+        y.stride(0), M, N, K, L, R, ws.data_ptr(), _nbytes(ws), _call_stream(stream, dev))
+    _check(status, "fp8bq_lora_add")
+
+
+def _len(t):
+    return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() else 0
 
 
 def fp8bq_moe_workspace_bytes(M: int, E: int, H: int, I: int, topk: int) -> int:
@@ -695,17 +773,32 @@ def new_moe_workspace(M: int, E: int, H: int, I: int, topk: int, device="cuda", 
     return ws
 
 
-def _moe_specs(x, w13, s13, w2, s2, y, ws):
+def _moe_sizes(x, w13):
     M, H = _mat(x, "x")
     E, I2, _ = _experts_w(w13)
-    I = I2 // 2
-    return M, E, H, I, [
+    return M, E, H, I2 // 2
+
+
+def _moe_check(what, M, E, H, I, x, w13, s13, w2, s2, y, ws, more, stream, dev):
+    """`more`: (name, tensor, dtypes, shape) of the form's own arguments, None left out."""
+    KI, KH = _kb(I), _kb(H)
+    contig = [(w13, _E4M3, (E, 2 * I, H)), (s13, _F32, (E, _kb(2 * I), KH)),
+              (w2, _E4M3, (E, H, I)), (s2, _F32, (E, KH, KI)), (y, _BF16, (M, H)),
+              (ws, _U8, (_len(ws),))]
+    contig += [m[1:] for m in more if m[1] is not None]
+    if stream is None and _fits(dev, contig, ((x, _BF16, (M, H)),)):
+        return
+    _validate(what, [
         _Spec("x", x, _BF16, (M, H), kind="rows"),
         _Spec("w13", w13, _E4M3, (E, 2 * I, H)),
-        _Spec("s13", s13, _F32, (E, _kb(2 * I), _kb(H))),
+        _Spec("s13", s13, _F32, (E, _kb(2 * I), KH)),
         _Spec("w2", w2, _E4M3, (E, H, I)),
-        _Spec("s2", s2, _F32, (E, _kb(H), _kb(I))),
-        _Spec("y", y, _BF16, (M, H)), _ws(ws)]
+        _Spec("s2", s2, _F32, (E, KH, KI)),
+        _Spec("y", y, _BF16, (M, H)), _ws(ws)] +
+        [_Spec(n, t, d, sh, optional=n in _MOE_OPTIONAL) for n, t, d, sh in more], stream)
+
+
+_MOE_OPTIONAL = ("bias", "ids_out", "weights_out")
 
 
 def fp8bq_moe_layer(x, logits, w13, s13, w2, s2, y, ws, topk: int, score: int = MOE_SOFTMAX,
@@ -716,29 +809,37 @@ def fp8bq_moe_layer(x, logits, w13, s13, w2, s2, y, ws, topk: int, score: int = 
     w2 [E, H, I], weighted sum into y.  bias [E] (MOE_SIGMOID): added to the
     score for the choice only.  ids_out / weights_out [M, topk] receive the
     routing.  Workspace: new_moe_workspace(M, E, H, I, topk)."""
-    M, E, H, I, specs = _moe_specs(x, w13, s13, w2, s2, y, ws)
-    _validate("fp8bq_moe_layer", specs + [
-        _Spec("logits", logits, _F32, (M, E)),
-        _Spec("bias", bias, _F32, (E,), optional=True),
-        _Spec("ids_out", ids_out, _I32, (M, topk), optional=True),
-        _Spec("weights_out", weights_out, _F32, (M, topk), optional=True)], stream)
-    _check(_lib.fp8bq_moe_layer(
-        _ptr(x), _ld(x), _ptr(logits), _ptr(bias), score, int(renormalize), float(routed_scale),
-        topk, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(y), _ptr(ids_out),
-        _ptr(weights_out), M, E, H, I, _ptr(ws), _nbytes(ws), _stream(stream)),
-        "fp8bq_moe_layer")
+    M, E, H, I = _moe_sizes(x, w13)
+    dev = _device()
+    _moe_check("fp8bq_moe_layer", M, E, H, I, x, w13, s13, w2, s2, y, ws, (
+        ("logits", logits, _F32, (M, E)), ("bias", bias, _F32, (E,)),
+        ("ids_out", ids_out, _I32, (M, topk)), ("weights_out", weights_out, _F32, (M, topk))),
+        stream, dev)
+    if logits is None:
+        raise ValueError("fp8bq_moe_layer: logits is required")
+    status = _lib.fp8bq_moe_layer(
+        x.data_ptr(), x.stride(0), logits.data_ptr(), _opt_ptr(bias), score, renormalize,
+        routed_scale, topk, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
+        y.data_ptr(), _opt_ptr(ids_out), _opt_ptr(weights_out), M, E, H, I, ws.data_ptr(),
+        _nbytes(ws), _call_stream(stream, dev))
+    _check(status, "fp8bq_moe_layer")
 
 
 def fp8bq_moe_experts(x, ids, weights, w13, s13, w2, s2, y, ws, stream=None):
     """The layer for tokens already routed: ids int32 [M, topk] (values outside
     [0, E) are left out) and weights FP32 [M, topk]."""
-    M, E, H, I, specs = _moe_specs(x, w13, s13, w2, s2, y, ws)
+    M, E, H, I = _moe_sizes(x, w13)
     topk = _mat(ids, "ids")[1]
-    _validate("fp8bq_moe_experts", specs + [
-        _Spec("ids", ids, _I32, (M, topk)), _Spec("weights", weights, _F32, (M, topk))], stream)
-    _check(_lib.fp8bq_moe_experts(
-        _ptr(x), _ld(x), _ptr(ids), _ptr(weights), topk, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
-        _ptr(y), M, E, H, I, _ptr(ws), _nbytes(ws), _stream(stream)), "fp8bq_moe_experts")
+    dev = _device()
+    _moe_check("fp8bq_moe_experts", M, E, H, I, x, w13, s13, w2, s2, y, ws, (
+        ("ids", ids, _I32, (M, topk)), ("weights", weights, _F32, (M, topk))), stream, dev)
+    if weights is None:
+        raise ValueError("fp8bq_moe_experts: weights is required")
+    status = _lib.fp8bq_moe_experts(
+        x.data_ptr(), x.stride(0), ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(),
+        s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr(), M, E, H, I, ws.data_ptr(),
+        _nbytes(ws), _call_stream(stream, dev))
+    _check(status, "fp8bq_moe_experts")
 
 
 # ---------------------------------------------------------------- residual add + RMSNorm

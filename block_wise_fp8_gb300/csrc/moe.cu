@@ -45,6 +45,8 @@
 //
 // Routing is computed by every CTA for itself: at these sizes that is cheaper
 // than one CTA's result handed to the others.
+#include <atomic>
+
 #include "common.cuh"
 #include "ptx.cuh"
 #include "quant_math.cuh"
@@ -62,7 +64,7 @@ constexpr int kSignals = 4;
 constexpr int kEpi = 256;
 constexpr int kEpiWarps = 8;
 constexpr int kTileBytes = 128 * 128;
-constexpr int kMaxRing = 8;
+constexpr int kMaxRing = 4;
 constexpr int kRunQueue = 4;
 // The codes never leave the layer, so the scale is a product with the binary32
 // reciprocal, not the quantisers' division: it may differ from theirs by one
@@ -80,6 +82,16 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p) {
 __device__ __forceinline__ void red_release_gpu(uint32_t *p, uint32_t v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+
+// Asynchronous 4-byte copy global -> shared; an arrival on `bar` once all of this
+// thread's copies so far have landed (counted in the barrier's init count).
+__device__ __forceinline__ void copy4_async(float *dst, const float *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_when_copied(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Bounded wait until *p reaches `target` (counters only grow during a launch).
 __device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t target,
@@ -137,12 +149,12 @@ struct Entry {
   int e, row, n;
 };
 
-// Runs a unit of KB steps is cut into: runs of about 12 steps, or shorter ones
+// Runs a unit of KB steps is cut into: runs of about 8 steps, or shorter ones
 // where all units together give a CTA less than 12 steps; `most` bounds the
 // workspace.
 __device__ __forceinline__ int runs_of(int KB, int units, int ctas, int most) {
   const int each = (units * KB + ctas - 1) / ctas;
-  return min(most, (KB + (each < 12 ? max(each, 1) : 12) - 1) / (each < 12 ? max(each, 1) : 12));
+  return min(most, (KB + (each < 12 ? max(each, 1) : 8) - 1) / (each < 12 ? max(each, 1) : 8));
 }
 
 // What the weight warp hands to the others: a run of one of the products
@@ -289,14 +301,14 @@ __device__ void route_tokens(const MoeArgs &a, int t0, int step, short *id, floa
 
 // One hidden row's 128 columns of group g by a warp: h = silu(gate) * up, codes
 // and scale.
-__device__ void hidden_row(const MoeArgs &a, float4 gate, float4 up, int row, int g, int pairs) {
+__device__ void hidden_row(const MoeArgs &a, float4 gate, float4 up, int row, int g, float *scale) {
   const int lane = threadIdx.x & 31;
   const float f[4] = {gate.x * sigmoid(gate.x) * up.x, gate.y * sigmoid(gate.y) * up.y,
                       gate.z * sigmoid(gate.z) * up.z, gate.w * sigmoid(gate.w) * up.w};
   float sc;
   const uint32_t code = quant4(f, &sc);
   *reinterpret_cast<uint32_t *>(a.hq + static_cast<int64_t>(row) * a.I + g * 128 + lane * 4) = code;
-  if (lane == 0) a.hs[g * (pairs + 1) + row] = sc;
+  if (lane == 0) *scale = sc;
 }
 
 template <int NT>
@@ -304,7 +316,7 @@ struct MoeCfg {
   static constexpr int kTokens = NT == 16 ? 16 : kMoeMaxTokens;
   static constexpr int kStage = 2 * kTileBytes + kTokens * 128;
   static constexpr int kCols = kTokens;              // TMEM columns of one partial tile
-  static constexpr int kMaxStages = NT == 16 ? 8 : 4;  // a stage has a TMEM buffer of two tiles
+  static constexpr int kMaxStages = 4;  // a stage has a TMEM buffer of two tiles
 };
 
 template <int NT>
@@ -327,8 +339,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const int J = (a.H + 255) / 256;
 
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float *scl = reinterpret_cast<float *>(ring + a.stages * kStage);  // [stages][2][NT] scales
-  float *wgt = scl + a.stages * 2 * NT;                     // [M][16]: weight by choice
+  float *scl = reinterpret_cast<float *>(ring + a.stages * kStage);  // [stages][NT + 4] scales
+  float *wgt = scl + a.stages * (NT + 4);                    // [M][16]: weight by choice
   float *wrow = wgt + a.M * kMoeMaxTopk;                    // [pairs]: by hidden row
   Entry *ent = reinterpret_cast<Entry *>(wrow + pairs);     // [max_entries]
   uint32_t *mask = reinterpret_cast<uint32_t *>(ent + a.max_entries);  // [E][2]: tokens' bits
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       mbar_init(&bars.empty[i], 1);
     }
     for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&bars.tfull[i], 2);  // the products, and the scales
+      mbar_init(&bars.tfull[i], 1 + 32);  // the products, and the scale warp's lanes
       mbar_init(&bars.tempty[i], kEpiWarps);
     }
     for (int i = 0; i < kRunQueue; ++i) {
@@ -651,8 +663,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
     __syncwarp();
   } else if (warp == 13) {
-    // ---- scales: per step, weight tile and row the product of the weight
-    // block's scale and the row's, loaded three steps before they are stored
+    // ---- scales: per step the rows' and the two weight blocks', copied
+    // asynchronously into the stage's own place as soon as the epilogue has
+    // left it, so that up to a ring's length of copies is in flight (loads
+    // through registers were 3 us late where the weights streamed)
     int st = 0, ph = 1, qi = 0, qph = 0;
     bool quantised = false, hidden = false;
     const int nbs2 = (a.H + 127) / 128;
@@ -663,7 +677,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       if (++qi == kRunQueue) qi = 0, qph ^= 1;
       if (run.product == 0) break;
       const bool one = run.product == 1;
-      const Entry en = ent[run.ei];
       if (one ? !quantised : !hidden) {
         if (one) {
           wait_count(all_quant, quant_ctas, abort, limit);
@@ -675,39 +688,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         }
         __syncwarp();
       }
-      {
-        const float *w0 = one ? a.s13 + (static_cast<int64_t>(en.e) * 2 * G1 + run.sub) * KB1
-                              : a.s2 + (static_cast<int64_t>(en.e) * nbs2 + 2 * run.sub) * KB2;
-        const float *w1 = one ? w0 + G1 * KB1 : 2 * run.sub + 1 < nbs2 ? w0 + KB2 : w0;
-        const float *x = one ? a.xs + (lane < en.n ? tok[en.row + lane] : 0) : a.hs + en.row + lane;
-        const int xstride = one ? a.M : pairs + 1, kb0 = run.kb, kb1 = run.kb + run.steps;
-        const bool mine = lane < en.n;
-        struct Three {
-          float x, w0, w1;
-        };
-        auto load = [&](int kb) {
-          Three v = {0.0f, 0.0f, 0.0f};
-          if (kb < kb1 && mine)
-            v = Three{__ldcg(x + kb * xstride), __ldg(w0 + kb), __ldg(w1 + kb)};
-          return v;
-        };
-        Three v0 = load(kb0), v1 = load(kb0 + 1), v2 = load(kb0 + 2);
-#pragma unroll 1
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const Three v = v0;
-          v0 = v1, v1 = v2, v2 = load(kb + 3);
-          mbar_wait(&bars.tempty[st], ph, abort, limit);
-          __syncwarp();
-          if (lane < NT) {
-            scl[st * 2 * NT + lane] = v.x * v.w0;
-            scl[st * 2 * NT + NT + lane] = v.x * v.w1;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.tfull[st]);
-          if (++st == a.stages) st = 0, ph ^= 1;
-        }
+      const Entry en = ent[run.ei];
+      const int64_t e = en.e;
+      const float *w0 =
+          (one ? a.s13 + (e * 2 * G1 + run.sub) * KB1 : a.s2 + (e * nbs2 + 2 * run.sub) * KB2) + run.kb;
+      const float *w1 = one ? w0 + G1 * KB1 : 2 * run.sub + 1 < nbs2 ? w0 + KB2 : w0;
+      // an entry's scales of one block of h have a cache line of their own: these
+      // copies pass through L1, which must not keep a line that is still written to
+      const int xstride = one ? a.M : 32;
+      const float *x = (one ? a.xs + (lane < en.n ? tok[en.row + lane] : 0)
+                            : a.hs + run.ei * G1 * 32 + lane) + run.kb * xstride;
+      for (int i = 0; i < run.steps; ++i) {
+        mbar_wait(&bars.tempty[st], ph, abort, limit);
+        __syncwarp();
+        float *dst = scl + st * (NT + 4);
+        if (lane < en.n) copy4_async(dst + lane, x);
+        if (lane < 2) copy4_async(dst + NT + lane, lane ? w1 : w0);
+        arrive_when_copied(&bars.tfull[st]);
+        x += xstride, ++w0, ++w1;
+        if (++st == a.stages) st = 0, ph ^= 1;
       }
     }
+    copies_landed();
   } else if (warp >= 14) {
     // ---- h from the first product's sums: units cta, cta + ctas, ...; a warp a
     // row, four hidden columns a lane.  The first round is a rehearsal on a spare
@@ -732,7 +734,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           up.x += y.x, up.y += y.y, up.z += y.z, up.w += y.w;
           src += plane1;
         }
-        hidden_row(a, gate, up, real ? en.row + n : pairs, g, pairs);
+        hidden_row(a, gate, up, real ? en.row + n : pairs, g,
+                   a.hs + ((real ? ei : a.max_entries) * G1 + g) * 32 + n);
       }
       fence_proxy_async_all();
       named_bar_sync(2, 64);
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         mbar_wait(&bars.tfull[st], ph, abort, limit);
         __syncwarp();
         tc_fence_after();
-        const float *sc = scl + (st * 2 + tile) * NT;
+        const float *sc = scl + st * (NT + 4);
         uint32_t v[NT];
         float w[NT];
         if (on) {
@@ -782,11 +785,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             tmem_ld16(at, v);
             if (NT > 16 && n > 16) tmem_ld16(at + 16, v + (NT > 16 ? 16 : 0));
           }
+          const float sw = sc[NT + tile];
 #pragma unroll
           for (int c = 0; c < NT; c += 4) {
             if (c >= n) break;
             const float4 q = *reinterpret_cast<const float4 *>(sc + c);
-            w[c] = q.x, w[c + 1] = q.y, w[c + 2] = q.z, w[c + 3] = q.w;
+            w[c] = q.x * sw, w[c + 1] = q.y * sw, w[c + 2] = q.z * sw, w[c + 3] = q.w * sw;
           }
           tmem_ld_wait();
         }
@@ -914,7 +918,7 @@ MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
   l.xq = take(M * KB1 * 128);
   l.xs = take(M * KB1 * 4);
   l.hq = take((P + 1) * I);  // and a spare row
-  l.hs = take((P + 1) * G1 * 4);
+  l.hs = take((l.max_entries + 1) * G1 * 32 * 4);
   l.planes = M <= 16 ? 8 : 4;  // most runs of a sum
   auto planes = [&](int64_t KB) { return KB < l.planes ? KB : l.planes; };
   l.sums = take(planes(KB1) * (P + 1) * 2 * I * 4);
@@ -950,11 +954,12 @@ cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *w
   const size_t fixed = 1024 + static_cast<size_t>(a.M) * kMoeMaxTopk * 8 + P * 6 +
                        static_cast<size_t>(l.max_entries) * sizeof(Entry) +
                        static_cast<size_t>(a.E) * 12;
-  const size_t stage = (NT == 16 ? MoeCfg<16>::kStage : MoeCfg<32>::kStage) + 2 * NT * 4;
+  const size_t stage = (NT == 16 ? MoeCfg<16>::kStage : MoeCfg<32>::kStage) + (NT + 4) * 4;
   const size_t room = dev.max_smem_optin - 1024;  // the static part
   a.stages = static_cast<int>((room - fixed) / stage);
   const int most = NT == 16 ? MoeCfg<16>::kMaxStages : MoeCfg<32>::kMaxStages;
   if (a.stages > most) a.stages = most;
+
   const size_t smem = fixed + a.stages * stage;
 
   CUtensorMap m13, m2, mx, mh;
@@ -963,9 +968,18 @@ cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *w
       !make_kmajor_map(&mx, a.xq, a.M, KB1 * 128, 16) || !make_kmajor_map(&mh, a.hq, P + 1, a.I, 16))
     return cudaErrorInvalidValue;
   auto run = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    // by kernel and device: it may use all shared memory
+    static std::atomic<uint64_t> sets[2];
+    std::atomic<uint64_t> &set = sets[NT == 32];
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
     if (e != cudaSuccess) return e;
+    if (!(set.load(std::memory_order_relaxed) >> d & 1)) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(dev.max_smem_optin) - 1024);
+      if (e != cudaSuccess) return e;
+      set.fetch_or(uint64_t(1) << d, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident, or an error
