@@ -113,7 +113,11 @@ struct LoraArgs {
   int splits, kb_split;  // K blocks of 64: split s takes kb_split of them
   int ngroups;           // 32-column groups an expand CTA walks
   int copy_rest;         // y is not base: rows without an adapter are copied
+  uint32_t *status;
+  uint64_t wait_limit_ns;
 };
+constexpr int64_t kLoraLarge = 256;  // tokens from which the form of lora_large.cu runs
+cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st);
 // K splits of the first product (a pure function, so that the workspace's size
 // and the launch agree)
 int lora_splits(int64_t M, int64_t K, int *kb_split);

@@ -253,7 +253,7 @@ int check_grouped(const void *q, const float *s_x, int s_layout, const void *w, 
   return FP8BQ_OK;
 }
 
-// Adapters: a status word (never set: these kernels have no waits), then the
+// Adapters: a status word, then the
 // first product's FP32 sums, one [M, R] plane per K split.
 size_t lora_workspace(int64_t M, int64_t R, int64_t K) {
   int per;
@@ -1001,6 +1001,7 @@ int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, con
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
   p.M = M, p.N = static_cast<int>(N), p.K = static_cast<int>(K);
   p.L = static_cast<int>(L), p.R = static_cast<int>(R);
+  p.status = static_cast<uint32_t *>(ws), p.wait_limit_ns = wait_limit_ns();
   return finish_launch(0, launch_lora_add(p, dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -20,15 +20,12 @@
 // significant bits; the rounding left is 2^-17 of t, below the FP32 sums' own
 // noise at these lengths and far below the output's 2^-9), so that y carries
 // one BF16 rounding, its own.
-#include "common.cuh"
-#include "ptx.cuh"
-#include "quant_math.cuh"
+#include "lora.cuh"
 
 namespace fp8bq {
 namespace {
 
-constexpr int kTile = 128;      // tokens of one adapter that a CTA takes
-constexpr int kWarpTokens = 32; // two 16-row MMA tiles
+constexpr int kWarpTokens = 32;  // two 16-row MMA tiles
 constexpr int kLoraThreads = 128;
 
 // D (16x8, FP32) += A (16x16, BF16) B (16x8, BF16)
@@ -39,65 +36,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-struct Tile {
-  int a, start, count;  // adapter (L: no adapter), first sorted row, rows
-};
-
-// The idx-th tile of the segments (rows offsets[a] .. offsets[a+1]-1 of
-// adapter a, cut into tiles of kTile rows; with `rest`, the rows after the
-// last segment as adapter L).  One warp; count 0 when there is no such tile.
-// Bounds outside [0, M] are clamped.
-__device__ Tile find_tile(const int *offsets, int L, int M, int idx, bool rest) {
-  const int lane = threadIdx.x & 31;
-  const int segs = L + (rest ? 1 : 0);
-  const int per = (segs + 31) / 32;
-  auto bound = [&](int k) { return k > L ? M : min(max(__ldg(offsets + k), 0), M); };
-  int n = 0;
-  for (int i = 0; i < per; ++i) {
-    const int k = lane * per + i;
-    if (k < segs) n += (max(bound(k + 1) - bound(k), 0) + kTile - 1) / kTile;
-  }
-  int upto = n;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-    if (lane >= d) upto += v;
-  }
-  const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > idx);
-  Tile t = {L, 0, 0};
-  if (past == 0) return t;
-  const int owner = __ffs(past) - 1;
-  if (lane == owner) {
-    int left = idx - (upto - n);
-    for (int i = 0; i < per; ++i) {
-      const int k = lane * per + i;
-      if (k >= segs) break;
-      const int s = bound(k), len = max(bound(k + 1) - s, 0);
-      const int tiles = (len + kTile - 1) / kTile;
-      if (left < tiles) {
-        t = {k, s + left * kTile, min(kTile, len - left * kTile)};
-        break;
-      }
-      left -= tiles;
-    }
-  }
-  t.a = __shfl_sync(0xFFFFFFFFu, t.a, owner);
-  t.start = __shfl_sync(0xFFFFFFFFu, t.start, owner);
-  t.count = __shfl_sync(0xFFFFFFFFu, t.count, owner);
-  return t;
-}
-
-__device__ __forceinline__ int rank_of(const LoraArgs &p, int a) {
-  if (a >= p.L) return 0;
-  return p.ranks ? min(max(__ldg(p.ranks + a), 0), p.R) : p.R;
 }
 
 // t = A_a x over one K split, 64 ranks at most (a higher rank takes a second
@@ -282,7 +220,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
           float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           if (row < here && k < p.R) {
             const float *at = src + static_cast<int64_t>(row) * p.R + k;
-#pragma unroll 4
+#pragma unroll 8
             for (int s = 0; s < p.splits; ++s) {
               const float4 f = __ldcg(reinterpret_cast<const float4 *>(at + s * p.M * p.R));
               v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
@@ -466,14 +404,16 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const int *id
 
 }  // namespace
 
-// Enough splits that few tokens still fill the GPU (four K blocks a split at
-// least, one for each warp), and four from 512 tokens on, where the token
-// tiles do.
+// Splits of the first product.  Few tokens: enough that each warp has a K block
+// (four a split) up to 8 tokens, fewer above, where there are more tiles and the
+// second product reads every split's sums for every column group.  Many: a CTA
+// an SM over about M / 128 + 2 tiles.
 int lora_splits(int64_t M, int64_t K, int *kb_split) {
   const int kbs = static_cast<int>((K + 63) / 64);
-  int splits = M >= 512 ? 4 : (kbs + 3) / 4;
+  int splits = M < kLoraLarge ? (M <= 8 ? 24 : 8) : static_cast<int>(152 / (M / 128 + 2));
   if (splits > 24) splits = 24;
-  if (splits > kbs) splits = kbs;
+  if (splits > (kbs + 3) / 4) splits = (kbs + 3) / 4;
+  if (splits < 1) splits = 1;
   const int per = (kbs + splits - 1) / splits;
   *kb_split = per;
   return (kbs + per - 1) / per;
@@ -482,6 +422,7 @@ int lora_splits(int64_t M, int64_t K, int *kb_split) {
 cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
   a.splits = lora_splits(a.M, a.K, &a.kb_split);
   a.copy_rest = a.y != a.base;
+  if (a.M >= kLoraLarge) return launch_lora_large(a, num_sms, st);
   // each segment adds at most one partly filled tile; none is empty
   const int64_t full = (a.M + kTile - 1) / kTile;
   const int64_t shrink_tiles = full + a.L < a.M ? full + a.L : a.M;

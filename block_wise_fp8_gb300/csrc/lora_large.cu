@@ -1,0 +1,497 @@
+// lora_large.cu -- the low-rank adapters' two products for many tokens (lora.cu
+// has the formulas and the form for few), on tcgen05 with TMEM accumulators.
+//
+// Both are bound by HBM: the first reads x once, the second reads base and
+// writes y once, and the rank is too small to keep the tensor cores busy.  What
+// carries them is bytes in flight, all of it asynchronous:
+//
+//   shrink  a CTA takes 128 tokens and one of the K splits.  Eight warps copy the
+//           tokens' rows (in the order's order) and A_a's rows into a ring of
+//           128-byte-swizzled stages with cp.async, one thread issues the MMAs
+//           (128 tokens x rank, K = 64 a stage).
+//   expand  persistent CTAs take equal runs of (128 tokens, 128 columns) blocks.
+//           Four warps own a token a thread: a thread copies its row's 256 bytes
+//           of base into shared memory with a bulk copy, two blocks or more
+//           ahead, adds the product's row from TMEM in place and sends it off
+//           with a bulk store, so that rows need not lie next to each other and
+//           no access is narrower than a row of the block.  B_a's rows come by
+//           cp.async; what lies past the adapter's rank is not read but filled
+//           with zeros by the copy.
+//
+// The direct form reads operands straight into registers, which leaves little in
+// flight: 46 + 140 us at 4096 tokens, 6144 -> 24576, rank 64, where these take
+// the times that the notes on each kernel give.
+#include "lora.cuh"
+
+namespace fp8bq {
+namespace {
+
+// Instruction descriptor, kind::f16: D = F32 (bits 4-5 = 1), A and B BF16 (bits
+// 7-9, 10-12 = 1), both K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+__device__ __forceinline__ uint32_t idesc_bf16(uint32_t M, uint32_t N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 bytes global -> shared, of which the first `bytes` (0 .. 16) are read and
+// the rest are zeros.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_store_1d(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_group_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows with the
+// 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// ---------------------------------------------------------------- shrink
+
+constexpr int kShrinkStages = 6;
+constexpr int kShrinkLag = kShrinkStages - 2;  // stages whose copies may be in flight
+constexpr int kShrinkThreads = 288;            // 8 copying warps, 1 issuing
+
+struct ShrinkBars {
+  uint64_t full[kShrinkStages], empty[kShrinkStages], done;
+  uint32_t tmem, abort, never;
+};
+
+__global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(const LoraArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ ShrinkBars bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int M = static_cast<int>(p.M), Rp = (p.R + 15) / 16 * 16;
+  volatile uint32_t *abort = &bars.abort;
+  const uint64_t limit = p.wait_limit_ns;
+  const int stage = 128 * 128 + Rp * 128;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  if (tid == 0) {
+    for (int i = 0; i < kShrinkStages; ++i) {
+      mbar_init(&bars.full[i], 256);
+      mbar_init(&bars.empty[i], 1);
+    }
+    mbar_init(&bars.done, 1);
+    bars.abort = bars.never = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&bars.tmem, 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  griddep_wait();
+  griddep_launch_dependents();
+  const Tile t = find_tile(p.offsets, p.L, M, blockIdx.x, false);
+  const int rank = rank_of(p, t.a);
+  const int kb0 = blockIdx.y * p.kb_split;
+  const int steps = t.count > 0 && rank > 0 ? min((p.K + 63) / 64, kb0 + p.kb_split) - kb0 : 0;
+
+  if (steps > 0 && warp < 8) {
+    // thread: chunk c (8 values) of rows r, r + 32, ... of both operands
+    const int r = tid >> 3, c = tid & 7;
+    const uint16_t *xr[4], *ar[4];
+    uint32_t xb[4], ab[4];  // bytes read of a chunk: 16, or 0 where the row is none
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r + 32 * i;
+      const int tok = row < t.count ? __ldg(p.order + t.start + row) : -1;
+      const bool on = tok >= 0 && tok < M;
+      xr[i] = on ? p.x + tok * p.ldx : p.x;
+      xb[i] = on ? 16 : 0;
+      ar[i] = p.a + (static_cast<int64_t>(t.a) * p.R + (row < rank ? row : 0)) * p.K;
+      ab[i] = row < rank ? 16 : 0;
+    }
+    bool ok = true;
+    int issued = 0;
+    for (int s = 0; s < steps; ++s) {
+      const int st = s % kShrinkStages;
+      if (s >= kShrinkStages)
+        ok = mbar_wait(&bars.empty[st], (s / kShrinkStages & 1) ^ 1, abort, limit);
+      if (!ok) break;
+      const uint32_t xs = ring + st * stage, as = xs + 128 * 128;
+      const int k = (kb0 + s) * 64 + c * 8;
+      const bool in = k < p.K;  // K is a multiple of 16
+      const int ko = in ? k : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy16_async(xs + sw128(r + 32 * i, c), xr[i] + ko, in ? xb[i] : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r + 32 * i < Rp) copy16_async(as + sw128(r + 32 * i, c), ar[i] + ko, in ? ab[i] : 0);
+      copies_commit();
+      ++issued;
+      if (s >= kShrinkLag) {
+        copies_wait<kShrinkLag>();
+        fence_proxy_async_smem();
+        mbar_arrive(&bars.full[(s - kShrinkLag) % kShrinkStages]);
+      }
+    }
+    copies_wait<0>();
+    fence_proxy_async_smem();
+    if (ok)
+      for (int s = max(0, issued - kShrinkLag); s < issued; ++s)
+        mbar_arrive(&bars.full[s % kShrinkStages]);
+  } else if (steps > 0 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(128, Rp);
+    for (int s = 0; s < steps; ++s) {
+      const int st = s % kShrinkStages;
+      if (!mbar_wait(&bars.full[st], s / kShrinkStages & 1, abort, limit)) break;
+      tc_fence_after();
+      const uint64_t xd = sdesc_kmajor_sw128(ring + st * stage);
+      const uint64_t ad = sdesc_kmajor_sw128(ring + st * stage + 128 * 128);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_bf16(tmem, xd + 2 * k, ad + 2 * k, idesc, s > 0 || k > 0);
+      umma_commit(&bars.empty[st]);
+    }
+    umma_commit(&bars.done);
+  }
+  __syncwarp();
+  if (steps > 0 && warp < 4) {
+    mbar_wait(&bars.done, 0, abort, limit);
+    __syncwarp();
+    tc_fence_after();
+    const int row = warp * 32 + lane;
+    float *out = p.part + (static_cast<int64_t>(blockIdx.y) * p.M + t.start + row) * p.R;
+    for (int c0 = 0; c0 < Rp; c0 += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
+      tmem_ld_wait();
+      if (row < t.count) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          if (c0 + i < p.R)
+            *reinterpret_cast<uint4 *>(out + c0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  if (steps > 0 && warp == 8 && lane == 0)  // the MMAs are done before the memory is given up
+    mbar_wait(&bars.done, 0, &bars.never, limit);
+  __syncthreads();
+  if (tid == 0 && *abort) atomicMax(p.status, kStatusTimeout);
+  if (warp == 8) tmem_dealloc(tmem, 128);
+}
+
+// ---------------------------------------------------------------- expand
+
+constexpr int kExpandThreads = 288;  // 4 row warps, 1 issuing, 4 copying B
+constexpr int kBlockCols = 128;
+constexpr int kRowPitch = kBlockCols * 2 + 16;  // bytes: 16-byte reads of 8 rows meet no bank twice
+constexpr int kBaseBufs = 4;
+constexpr int kBStages = 2;
+
+struct ExpandBars {
+  uint64_t base[kBaseBufs][4];  // by row warp
+  uint64_t bfull[kBStages], bempty[kBStages];
+  uint64_t dfull[2], dempty[2];
+  uint64_t sfull, done;
+  uint32_t tmem, abort, never;
+};
+
+// Tiles of all segments (and of the rows without an adapter), by one warp.
+__device__ int count_tiles(const int *offsets, int L, int M, bool rest) {
+  const int lane = threadIdx.x & 31;
+  auto bound = [&](int k) { return k > L ? M : min(max(__ldg(offsets + k), 0), M); };
+  int n = 0;
+  for (int k = lane; k < L + (rest ? 1 : 0); k += 32)
+    n += (max(bound(k + 1) - bound(k), 0) + kTile - 1) / kTile;
+  return __reduce_add_sync(0xFFFFFFFFu, n);
+}
+
+// KT: 64-wide tiles of the rank (R <= 64 KT); NB: base buffers in use
+template <int KT, int NB>
+__global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(const LoraArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ ExpandBars bars;
+  constexpr int kOperand = KT * 128 * 128;  // bytes of one 128-row operand
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int M = static_cast<int>(p.M);
+  volatile uint32_t *abort = &bars.abort;
+  const uint64_t limit = p.wait_limit_ns;
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *s_hi = smem, *s_lo = smem + kOperand, *b_ring = smem + 2 * kOperand;
+  uint8_t *base_ring = b_ring + kBStages * kOperand;
+  if (tid == 0) {
+    for (int i = 0; i < NB; ++i)
+      for (int w = 0; w < 4; ++w) mbar_init(&bars.base[i][w], 32);
+    for (int i = 0; i < kBStages; ++i) {
+      mbar_init(&bars.bfull[i], 128);
+      mbar_init(&bars.bempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.dfull[i], 1);
+      mbar_init(&bars.dempty[i], 4);
+    }
+    mbar_init(&bars.sfull, 128);
+    mbar_init(&bars.done, 1);
+    bars.abort = bars.never = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(&bars.tmem, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  griddep_launch_dependents();
+  // (as in the direct form, all but t is visible here already)
+  const int tiles = count_tiles(p.offsets, p.L, M, p.copy_rest != 0);
+  const int nblk = (p.N + kBlockCols - 1) / kBlockCols;
+  const int64_t work = static_cast<int64_t>(tiles) * nblk;
+  const int64_t w0 = work * blockIdx.x / gridDim.x, w1 = work * (blockIdx.x + 1) / gridDim.x;
+
+  if (warp < 4) {
+    // ---- rows: this thread's token in the tile is `tid`
+    int db = 0, dph = 0;          // product buffer and its phase
+    int bufs = 0;                 // blocks whose base was asked for, and
+    int seen = 0;                 // those that arrived
+    bool ok = true, waited = false;
+    for (int64_t w = w0; w < w1 && ok;) {
+      const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
+      const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
+      w += blk1 - blk0;
+      const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
+      const int rank = rank_of(p, t.a);
+      int tok = tid < t.count ? __ldg(p.order + t.start + tid) : -1;
+      if (tok >= M) tok = -1;
+      const uint16_t *src = p.base + (tok < 0 ? 0 : tok * p.ldbase);
+      uint16_t *dst = p.y + (tok < 0 ? 0 : tok * p.ldy);
+      auto ask = [&](int blk) {  // base of block blk into the next buffer
+        const int b = bufs % NB;
+        const uint32_t bytes = min(kBlockCols, p.N - blk * kBlockCols) * 2;
+        uint64_t *bar = &bars.base[b][warp];
+        if (tok >= 0) {
+          mbar_arrive_expect_tx(bar, bytes);
+          bulk_load_1d(base_ring + (b * 128 + tid) * kRowPitch, src + blk * kBlockCols, bytes, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+        ++bufs;
+      };
+      // a new tile's first blocks: the buffers' last stores must have read them
+      bulk_wait_group_read<0>();
+      int asked = blk0;
+      for (; asked < blk1 && asked < blk0 + NB - 1; ++asked) ask(asked);
+      if (!waited) griddep_wait();
+      waited = true;
+      if (rank > 0) {
+        const float scale = __ldg(p.scales + t.a);
+        const float *at = p.part + (static_cast<int64_t>(t.start) + tid) * p.R;
+        const int chunks = (rank + 15) / 16 * 2;
+        for (int c = 0; c < chunks; ++c) {
+          float v[8] = {};
+          if (tok >= 0 && c * 8 < p.R) {
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s) {
+              const float4 *q = reinterpret_cast<const float4 *>(at + s * p.M * p.R + c * 8);
+              const float4 f = __ldcg(q), g = __ldcg(q + 1);
+              v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+              v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
+            }
+          }
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = c * 8 + 2 * i < rank ? v[2 * i] * scale : 0.0f;
+            float y = c * 8 + 2 * i + 1 < rank ? v[2 * i + 1] * scale : 0.0f;
+            hi[i] = pack_bf16(x, y);
+            lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+          }
+          const uint32_t off = (c >> 3) * 128 * 128 + sw128(tid, c & 7);
+          *reinterpret_cast<uint4 *>(s_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(s_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars.sfull);
+      }
+      for (int blk = blk0; blk < blk1; ++blk) {
+        const int b = seen % NB;
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait(&bars.base[b][warp], seen / NB & 1, abort, limit));
+        if (!ok) break;
+        ++seen;
+        uint8_t *my = base_ring + (b * 128 + tid) * kRowPitch;
+        const int cols = min(kBlockCols, p.N - blk * kBlockCols);
+        if (rank > 0) {
+          mbar_wait(&bars.dfull[db], dph, abort, limit);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < kBlockCols; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + db * 128 + c0, v);
+            tmem_ld_wait();
+            if (c0 + 32 >= kBlockCols) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.dempty[db]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 *q = reinterpret_cast<uint4 *>(my + (c0 + i * 8) * 2);
+              const uint4 h = *q;
+              const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                o[j] = pack_bf16(bf16_lo(hw[j]) + __uint_as_float(v[i * 8 + 2 * j]),
+                                 bf16_hi(hw[j]) + __uint_as_float(v[i * 8 + 2 * j + 1]));
+              *q = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          db ^= 1;
+          dph ^= db == 0;
+        }
+        fence_proxy_async_smem();
+        if (tok >= 0) bulk_store_1d(dst + blk * kBlockCols, my, cols * 2);
+        bulk_commit_group();
+        if (asked < blk1) {  // into the buffer whose store is the last but one
+          bulk_wait_group_read<1>();
+          ask(asked++);
+        }
+      }
+    }
+    if (!waited) griddep_wait();
+    // copies still in flight land before the memory is given up
+    for (; seen < bufs; ++seen)
+      mbar_wait(&bars.base[seen % NB][warp], seen / NB & 1, &bars.never, limit);
+    bulk_wait_group0();
+  } else if (warp == 4) {
+    // ---- MMAs: t's high and low halves against the same rows of B
+    const uint32_t idesc = idesc_bf16(128, kBlockCols);
+    const uint64_t hd = sdesc_kmajor_sw128(smem_u32(s_hi)), ld = sdesc_kmajor_sw128(smem_u32(s_lo));
+    int st = 0, ph = 0, db = 0, dph = 0, sph = 0;
+    bool ok = true;
+    for (int64_t w = w0; w < w1 && ok;) {
+      const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
+      const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
+      w += blk1 - blk0;
+      const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
+      const int rank = rank_of(p, t.a), ks = (rank + 15) / 16;
+      if (rank == 0) continue;
+      if (lane == 0) {
+        ok = mbar_wait(&bars.sfull, sph, abort, limit);
+        for (int blk = blk0; blk < blk1 && ok; ++blk) {
+          ok = mbar_wait(&bars.bfull[st], ph, abort, limit) &&
+               mbar_wait(&bars.dempty[db], dph ^ 1, abort, limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bd = sdesc_kmajor_sw128(smem_u32(b_ring + st * kOperand));
+          for (int k = 0; k < ks; ++k) {
+            const uint64_t off = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+            umma_bf16(tmem + db * 128, hd + off, bd + off, idesc, k > 0);
+            umma_bf16(tmem + db * 128, ld + off, bd + off, idesc, 1);
+          }
+          umma_commit(&bars.bempty[st]);
+          umma_commit(&bars.dfull[db]);
+          if (++st == kBStages) st = 0, ph ^= 1;
+          db ^= 1;
+          dph ^= db == 0;
+        }
+      }
+      sph ^= 1;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
+    if (lane == 0) {
+      umma_commit(&bars.done);
+      mbar_wait(&bars.done, 0, &bars.never, limit);
+    }
+    __syncwarp();
+  } else {
+    // ---- B_a's rows: thread = chunk (8 ranks) c of rows r, r + 16, ...
+    const int bt = tid - 160, r = bt >> 3, c = bt & 7;
+    int st = 0, ph = 1, filled = 0, given = 0;
+    bool ok = true;
+    for (int64_t w = w0; w < w1 && ok;) {
+      const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
+      const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
+      w += blk1 - blk0;
+      const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
+      const int rank = rank_of(p, t.a);
+      if (rank == 0) continue;
+      const uint16_t *b = p.b + static_cast<int64_t>(t.a) * p.N * p.R;
+      for (int blk = blk0; blk < blk1; ++blk) {
+        ok = mbar_wait(&bars.bempty[st], ph, abort, limit);
+        if (!ok) break;
+        const uint32_t to = smem_u32(b_ring + st * kOperand);
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+          const int k = kt * 64 + c * 8;
+          if (k >= (rank + 15) / 16 * 16) continue;  // a step that no MMA takes
+          const int bytes = min(max(rank - k, 0), 8) * 2;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int n = blk * kBlockCols + r + 16 * i;
+            const bool in = n < p.N && bytes > 0;
+            copy16_async(to + kt * 128 * 128 + sw128(r + 16 * i, c),
+                         in ? b + static_cast<int64_t>(n) * p.R + k : b, in ? bytes : 0);
+          }
+        }
+        copies_commit();
+        ++filled;
+        if (++st == kBStages) st = 0, ph ^= 1;
+        if (filled - given == kBStages) {  // the oldest has landed
+          copies_wait<kBStages - 1>();
+          fence_proxy_async_smem();
+          mbar_arrive(&bars.bfull[given++ % kBStages]);
+        }
+      }
+    }
+    copies_wait<0>();
+    fence_proxy_async_smem();
+    for (; given < filled; ++given) mbar_arrive(&bars.bfull[given % kBStages]);
+  }
+  __syncthreads();
+  if (tid == 0 && *abort) atomicMax(p.status, kStatusTimeout);
+  if (warp == 4) tmem_dealloc(tmem, 256);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st) {
+  const int64_t full = (a.M + kTile - 1) / kTile;
+  const int64_t tiles = full + a.L < a.M ? full + a.L : a.M;
+  const int Rp = (a.R + 15) / 16 * 16;
+  const int smem1 = kShrinkStages * (128 * 128 + Rp * 128) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(lora_shrink_large_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(lora_shrink_large_kernel, dim3(static_cast<unsigned>(tiles), a.splits),
+                 dim3(kShrinkThreads), smem1, st, a);
+  if (e != cudaSuccess) return e;
+  auto run = [&](auto kern, int KT, int NB) {
+    const int smem = (2 + kBStages) * KT * 128 * 128 + NB * 128 * kRowPitch + 1024;
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) return r;
+    return launch_pdl(kern, dim3(num_sms), dim3(kExpandThreads), smem, st, a);
+  };
+  if (a.R <= 64) return run(lora_expand_large_kernel<1, 4>, 1, 4);
+  return run(lora_expand_large_kernel<2, 2>, 2, 2);
+}
+
+}  // namespace fp8bq
