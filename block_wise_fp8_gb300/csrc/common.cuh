@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -42,6 +43,19 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Lets a kernel use `bytes` (always the same) of dynamic shared memory, asked for
+// once a device.
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess || (d < 64 && done.load(std::memory_order_relaxed) >> d & 1)) return e;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && d < 64) done.fetch_or(uint64_t(1) << d, std::memory_order_relaxed);
+  return e;
 }
 
 // ---------------------------------------------------------------- quant kernels
@@ -108,6 +122,8 @@ struct LoraArgs {
   const float *scales;
   const int *order, *offsets, *ranks;  // ranks may be nullptr: every rank is R
   float *part;                         // [splits][M][R]
+  uint16_t *t;                         // many tokens: [M][2][R rounded up to 16], BF16 halves
+  uint32_t *tickets;                   // many tokens: splits done, by tile
   int64_t M;
   int L, R, K, N;
   int splits, kb_split;  // K blocks of 64: split s takes kb_split of them
@@ -116,6 +132,7 @@ struct LoraArgs {
   uint32_t *status;
   uint64_t wait_limit_ns;
 };
+constexpr int kLoraTickets = 1024;   // more than the tiles of any call with several splits
 constexpr int64_t kLoraLarge = 256;  // tokens from which the form of lora_large.cu runs
 cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st);
 // K splits of the first product (a pure function, so that the workspace's size

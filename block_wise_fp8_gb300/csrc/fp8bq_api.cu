@@ -253,13 +253,24 @@ int check_grouped(const void *q, const float *s_x, int s_layout, const void *w, 
   return FP8BQ_OK;
 }
 
-// Adapters: a status word, then the
-// first product's FP32 sums, one [M, R] plane per K split.
-size_t lora_workspace(int64_t M, int64_t R, int64_t K) {
+// Adapters: a status word | tickets of the token tiles (their place and size are
+// the same for all shapes, so that one workspace serves calls of several) | the first product's FP32 sums, one [M, R] plane per K split | for
+// many tokens, their total as BF16 halves.
+struct LoraLayout {
+  size_t tickets, part, t, total;
+};
+LoraLayout lora_layout(int64_t M, int64_t R, int64_t K) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   int per;
   const size_t planes = static_cast<size_t>(lora_splits(M, K, &per));
-  return 256 + (planes * static_cast<size_t>(M) * static_cast<size_t>(R) * 4 + 255) / 256 * 256;
+  LoraLayout l;
+  l.tickets = 256;
+  l.part = l.tickets + kLoraTickets * 4;
+  l.t = l.part + up(planes * static_cast<size_t>(M) * static_cast<size_t>(R) * 4);
+  l.total = l.t + (M < kLoraLarge ? 0 : up(static_cast<size_t>(M) * ((R + 15) / 16 * 16) * 4));
+  return l;
 }
+size_t lora_workspace(int64_t M, int64_t R, int64_t K) { return lora_layout(M, R, K).total; }
 
 int check_moe_shape(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
   constexpr int64_t kMax = (int64_t(1) << 31) - 1;
@@ -998,7 +1009,11 @@ int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, con
   p.base = static_cast<const uint16_t *>(base), p.ldbase = ld_base;
   p.y = static_cast<uint16_t *>(y), p.ldy = ldy;
   p.scales = scales, p.ranks = ranks, p.order = order, p.offsets = offsets;
-  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+  const LoraLayout l = lora_layout(M, R, K);
+  uint8_t *at = static_cast<uint8_t *>(ws);
+  p.tickets = reinterpret_cast<uint32_t *>(at + l.tickets);
+  p.part = reinterpret_cast<float *>(at + l.part);
+  p.t = reinterpret_cast<uint16_t *>(at + l.t);
   p.M = M, p.N = static_cast<int>(N), p.K = static_cast<int>(K);
   p.L = static_cast<int>(L), p.R = static_cast<int>(R);
   p.status = static_cast<uint32_t *>(ws), p.wait_limit_ns = wait_limit_ns();

@@ -442,19 +442,19 @@ cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(expand_tiles), (groups + a.ngroups - 1) / a.ngroups),
       block(kLoraThreads);
   const int ks = (a.R + 15) / 16;
-  auto run = [&](auto kern, int KS) {
-    const size_t smem = static_cast<size_t>(KS) * 2 * 2 * 32 * 16 * 4;
+  auto expand = [&](auto k) {
+    constexpr int KS = decltype(k)::value;
+    constexpr int smem = KS * 2 * 2 * 32 * 16 * 4;
     if (smem > 48 * 1024) {
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+      cudaError_t e = allow_smem<lora_expand_kernel<KS>>(smem);
       if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kern, grid, block, smem, st, a);
+    return launch_pdl(lora_expand_kernel<KS>, grid, block, smem, st, a);
   };
-  if (ks <= 1) return run(lora_expand_kernel<1>, 1);
-  if (ks <= 2) return run(lora_expand_kernel<2>, 2);
-  if (ks <= 4) return run(lora_expand_kernel<4>, 4);
-  return run(lora_expand_kernel<8>, 8);
+  if (ks <= 1) return expand(std::integral_constant<int, 1>{});
+  if (ks <= 2) return expand(std::integral_constant<int, 2>{});
+  if (ks <= 4) return expand(std::integral_constant<int, 4>{});
+  return expand(std::integral_constant<int, 8>{});
 }
 
 cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int *offsets,
@@ -463,9 +463,7 @@ cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int 
   const int warps = each ? static_cast<int>((M + each - 1) / each) : 0;
   const size_t smem = static_cast<size_t>(warps) * (L + 1) * sizeof(int);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(lora_group_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = allow_smem<lora_group_kernel>(32 * (kMaxAdapters + 1) * sizeof(int));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(lora_group_kernel, dim3(1), dim3(kGroupThreads), smem, st, ids,

@@ -9,8 +9,10 @@
 //           tokens' rows (in the order's order) and A_a's rows into a ring of
 //           128-byte-swizzled stages with cp.async, one thread issues the MMAs
 //           (128 tokens x rank, K = 64 a stage).
+//           The last split of a tile to finish adds them up and writes t as the
+//           second product's operand, so that no CTA of that one adds again.
 //   expand  persistent CTAs take equal runs of (128 tokens, 128 columns) blocks.
-//           Four warps own a token a thread: a thread copies its row's 256 bytes
+//           Two groups of four warps have a token a thread: a thread copies its row's 256 bytes
 //           of base into shared memory with a bulk copy, two blocks or more
 //           ahead, adds the product's row from TMEM in place and sends it off
 //           with a bulk store, so that rows need not lie next to each other and
@@ -74,7 +76,7 @@ constexpr int kShrinkThreads = 288;            // 8 copying warps, 1 issuing
 
 struct ShrinkBars {
   uint64_t full[kShrinkStages], empty[kShrinkStages], done;
-  uint32_t tmem, abort, never;
+  uint32_t tmem, abort, never, last;
 };
 
 __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(const LoraArgs p) {
@@ -188,6 +190,45 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
     }
     tc_fence_before();
   }
+  if (steps > 0 && warp < 8) {
+    // the last of the tile's splits adds them all, in order, and leaves t as the
+    // second product's operand: scaled, zeros past the rank, high and low halves
+    named_bar_sync(1, 256);
+    if (tid == 0) {
+      bars.last = gridDim.y == 1 || atom_add_acq_rel_gpu(&p.tickets[blockIdx.x], 1) == gridDim.y - 1;
+      if (bars.last && gridDim.y > 1) p.tickets[blockIdx.x] = 0;
+    }
+    named_bar_sync(1, 256);
+    if (bars.last) {
+      const float scale = __ldg(p.scales + t.a);
+      const int per = Rp / 8;
+      for (int i = tid; i < t.count * per; i += 256) {
+        const int row = i / per, c = i - row * per;
+        float v[8] = {};
+        if (c * 8 < p.R) {
+          const float *at = p.part + (static_cast<int64_t>(t.start) + row) * p.R + c * 8;
+#pragma unroll 4
+          for (int s = 0; s < p.splits; ++s) {
+            const float4 *q = reinterpret_cast<const float4 *>(at + s * p.M * p.R);
+            const float4 f = __ldcg(q), g = __ldcg(q + 1);
+            v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+            v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
+          }
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = c * 8 + 2 * j < rank ? v[2 * j] * scale : 0.0f;
+          const float y = c * 8 + 2 * j + 1 < rank ? v[2 * j + 1] * scale : 0.0f;
+          hi[j] = pack_bf16(x, y);
+          lo[j] = pack_bf16(x - bf16_lo(hi[j]), y - bf16_hi(hi[j]));
+        }
+        uint16_t *out = p.t + (static_cast<int64_t>(t.start) + row) * 2 * Rp + c * 8;
+        *reinterpret_cast<uint4 *>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(out + Rp) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+  }
   if (steps > 0 && warp == 8 && lane == 0)  // the MMAs are done before the memory is given up
     mbar_wait(&bars.done, 0, &bars.never, limit);
   __syncthreads();
@@ -197,14 +238,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
 
 // ---------------------------------------------------------------- expand
 
-constexpr int kExpandThreads = 288;  // 4 row warps, 1 issuing, 4 copying B
+constexpr int kExpandThreads = 416;  // 8 row warps, 1 issuing, 4 copying B
+constexpr int kRowThreads = 256;
 constexpr int kBlockCols = 128;
 constexpr int kRowPitch = kBlockCols * 2 + 16;  // bytes: 16-byte reads of 8 rows meet no bank twice
-constexpr int kBaseBufs = 4;
 constexpr int kBStages = 2;
 
 struct ExpandBars {
-  uint64_t base[kBaseBufs][4];  // by row warp
+  uint64_t base[2][2][4];  // by row group, its buffer, warp
   uint64_t bfull[kBStages], bempty[kBStages];
   uint64_t dfull[2], dempty[2];
   uint64_t sfull, done;
@@ -221,22 +262,21 @@ __device__ int count_tiles(const int *offsets, int L, int M, bool rest) {
   return __reduce_add_sync(0xFFFFFFFFu, n);
 }
 
-// KT: 64-wide tiles of the rank (R <= 64 KT); NB: base buffers in use
+// KT: 64-wide tiles of the rank (R <= 64 KT); NB: base buffers of a row group
 template <int KT, int NB>
 __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(const LoraArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ ExpandBars bars;
   constexpr int kOperand = KT * 128 * 128;  // bytes of one 128-row operand
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int M = static_cast<int>(p.M);
+  const int M = static_cast<int>(p.M), Rp = (p.R + 15) / 16 * 16;
   volatile uint32_t *abort = &bars.abort;
   const uint64_t limit = p.wait_limit_ns;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *s_hi = smem, *s_lo = smem + kOperand, *b_ring = smem + 2 * kOperand;
   uint8_t *base_ring = b_ring + kBStages * kOperand;
   if (tid == 0) {
-    for (int i = 0; i < NB; ++i)
-      for (int w = 0; w < 4; ++w) mbar_init(&bars.base[i][w], 32);
+    for (int i = 0; i < 16; ++i) mbar_init(&bars.base[i >> 3][i >> 2 & 1][i & 3], 32);
     for (int i = 0; i < kBStages; ++i) {
       mbar_init(&bars.bfull[i], 128);
       mbar_init(&bars.bempty[i], 1);
@@ -245,12 +285,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
       mbar_init(&bars.dfull[i], 1);
       mbar_init(&bars.dempty[i], 4);
     }
-    mbar_init(&bars.sfull, 128);
+    mbar_init(&bars.sfull, kRowThreads);
     mbar_init(&bars.done, 1);
     bars.abort = bars.never = 0;
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(&bars.tmem, 256);
     tmem_relinquish();
   }
@@ -265,127 +305,123 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
   const int64_t work = static_cast<int64_t>(tiles) * nblk;
   const int64_t w0 = work * blockIdx.x / gridDim.x, w1 = work * (blockIdx.x + 1) / gridDim.x;
 
-  if (warp < 4) {
-    // ---- rows: this thread's token in the tile is `tid`
-    int db = 0, dph = 0;          // product buffer and its phase
-    int bufs = 0;                 // blocks whose base was asked for, and
-    int seen = 0;                 // those that arrived
-    bool ok = true, waited = false;
-    for (int64_t w = w0; w < w1 && ok;) {
+  if (warp < 8) {
+    // ---- rows: two groups of four warps take the blocks in turn, each with its
+    // own product buffer and base buffers; a thread has a token of the tile
+    const int grp = warp >> 2, wg = warp & 3, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(wg * 32) << 16;
+    uint8_t *const mine = base_ring + (grp * NB * 128 + row) * kRowPitch;
+    int dph = 0;            // the product buffer's phase
+    int bufs = 0, seen = 0; // blocks whose base was asked for, and those that arrived
+    int64_t q = 0;          // blocks of this CTA so far, both groups'
+    bool ok = true;         // a thread that gave up waiting goes on to the barriers alone
+    griddep_wait();
+    for (int64_t w = w0; w < w1;) {
       const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
       const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
       w += blk1 - blk0;
       const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
       const int rank = rank_of(p, t.a);
-      int tok = tid < t.count ? __ldg(p.order + t.start + tid) : -1;
+      int tok = row < t.count ? __ldg(p.order + t.start + row) : -1;
       if (tok >= M) tok = -1;
       const uint16_t *src = p.base + (tok < 0 ? 0 : tok * p.ldbase);
       uint16_t *dst = p.y + (tok < 0 ? 0 : tok * p.ldy);
       auto ask = [&](int blk) {  // base of block blk into the next buffer
         const int b = bufs % NB;
         const uint32_t bytes = min(kBlockCols, p.N - blk * kBlockCols) * 2;
-        uint64_t *bar = &bars.base[b][warp];
+        uint64_t *bar = &bars.base[grp][b][wg];
         if (tok >= 0) {
           mbar_arrive_expect_tx(bar, bytes);
-          bulk_load_1d(base_ring + (b * 128 + tid) * kRowPitch, src + blk * kBlockCols, bytes, bar);
+          bulk_load_1d(mine + b * 128 * kRowPitch, src + blk * kBlockCols, bytes, bar);
         } else {
           mbar_arrive(bar);
         }
         ++bufs;
       };
-      // a new tile's first blocks: the buffers' last stores must have read them
-      bulk_wait_group_read<0>();
-      int asked = blk0;
-      for (; asked < blk1 && asked < blk0 + NB - 1; ++asked) ask(asked);
-      if (!waited) griddep_wait();
-      waited = true;
+      const int first = blk0 + (static_cast<int>(q ^ grp) & 1);
+      int asked = first;
+      bulk_wait_group_read<0>();  // the buffers' last stores have read them
+      for (; ok && asked < blk1 && asked < first + 2 * (NB - 1); asked += 2) ask(asked);
+      if (NB == 1 && ok && asked < blk1) ask(asked), asked += 2;
+      // t's rows of the tile, once the last tile's products are done
+      named_bar_sync(1, kRowThreads);
       if (rank > 0) {
-        const float scale = __ldg(p.scales + t.a);
-        const float *at = p.part + (static_cast<int64_t>(t.start) + tid) * p.R;
-        const int chunks = (rank + 15) / 16 * 2;
-        for (int c = 0; c < chunks; ++c) {
-          float v[8] = {};
-          if (tok >= 0 && c * 8 < p.R) {
-#pragma unroll 4
-            for (int s = 0; s < p.splits; ++s) {
-              const float4 *q = reinterpret_cast<const float4 *>(at + s * p.M * p.R + c * 8);
-              const float4 f = __ldcg(q), g = __ldcg(q + 1);
-              v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-              v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
-            }
-          }
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = c * 8 + 2 * i < rank ? v[2 * i] * scale : 0.0f;
-            float y = c * 8 + 2 * i + 1 < rank ? v[2 * i + 1] * scale : 0.0f;
-            hi[i] = pack_bf16(x, y);
-            lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
-          }
-          const uint32_t off = (c >> 3) * 128 * 128 + sw128(tid, c & 7);
-          *reinterpret_cast<uint4 *>(s_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(s_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int per = (rank + 15) / 16 * 2;
+        for (int i = tid; i < 128 * per; i += kRowThreads) {
+          const int r = i / per, c = i - r * per;
+          const uint32_t off = (c >> 3) * 128 * 128 + sw128(r, c & 7);
+          const uint16_t *from = p.t + (static_cast<int64_t>(t.start) + (r < t.count ? r : 0)) * 2 * Rp + c * 8;
+          const uint32_t bytes = r < t.count ? 16 : 0;
+          copy16_async(smem_u32(s_hi) + off, from, bytes);
+          copy16_async(smem_u32(s_lo) + off, from + Rp, bytes);
         }
+        copies_commit();
+        copies_wait<0>();
         fence_proxy_async_smem();
         mbar_arrive(&bars.sfull);
       }
-      for (int blk = blk0; blk < blk1; ++blk) {
+      for (int blk = first; blk < blk1; blk += 2) {
         const int b = seen % NB;
-        ok = __all_sync(0xFFFFFFFFu,
-                        mbar_wait(&bars.base[b][warp], seen / NB & 1, abort, limit));
-        if (!ok) break;
+        if (ok) ok = mbar_wait(&bars.base[grp][b][wg], seen / NB & 1, abort, limit);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) continue;
         ++seen;
-        uint8_t *my = base_ring + (b * 128 + tid) * kRowPitch;
+        uint8_t *my = mine + b * 128 * kRowPitch;
         const int cols = min(kBlockCols, p.N - blk * kBlockCols);
         if (rank > 0) {
-          mbar_wait(&bars.dfull[db], dph, abort, limit);
+          mbar_wait(&bars.dfull[grp], dph, abort, limit);
           __syncwarp();
+          dph ^= 1;
           tc_fence_after();
+          uint32_t v[2][32];
+          tmem_ld32(tmem + lanes + grp * 128, v[0]);
 #pragma unroll
           for (int c0 = 0; c0 < kBlockCols; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + db * 128 + c0, v);
             tmem_ld_wait();
-            if (c0 + 32 >= kBlockCols) {
+            if (c0 + 32 < kBlockCols) {
+              tmem_ld32(tmem + lanes + grp * 128 + c0 + 32, v[(c0 / 32 + 1) & 1]);
+            } else {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&bars.dempty[db]);
+              if (lane == 0) mbar_arrive(&bars.dempty[grp]);
             }
+            const uint32_t *d = v[c0 / 32 & 1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint4 *q = reinterpret_cast<uint4 *>(my + (c0 + i * 8) * 2);
-              const uint4 h = *q;
+              uint4 *at = reinterpret_cast<uint4 *>(my + (c0 + i * 8) * 2);
+              const uint4 h = *at;
               const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
               uint32_t o[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                o[j] = pack_bf16(bf16_lo(hw[j]) + __uint_as_float(v[i * 8 + 2 * j]),
-                                 bf16_hi(hw[j]) + __uint_as_float(v[i * 8 + 2 * j + 1]));
-              *q = make_uint4(o[0], o[1], o[2], o[3]);
+                o[j] = pack_bf16(bf16_lo(hw[j]) + __uint_as_float(d[i * 8 + 2 * j]),
+                                 bf16_hi(hw[j]) + __uint_as_float(d[i * 8 + 2 * j + 1]));
+              *at = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
-          db ^= 1;
-          dph ^= db == 0;
         }
         fence_proxy_async_smem();
         if (tok >= 0) bulk_store_1d(dst + blk * kBlockCols, my, cols * 2);
         bulk_commit_group();
-        if (asked < blk1) {  // into the buffer whose store is the last but one
-          bulk_wait_group_read<1>();
-          ask(asked++);
+        if (asked < blk1) {  // into the buffer of the store before (of this one, if it is the only)
+          bulk_wait_group_read<NB - 1>();
+          ask(asked);
+          asked += 2;
         }
       }
+      q += blk1 - blk0;
     }
-    if (!waited) griddep_wait();
     // copies still in flight land before the memory is given up
     for (; seen < bufs; ++seen)
-      mbar_wait(&bars.base[seen % NB][warp], seen / NB & 1, &bars.never, limit);
+      mbar_wait(&bars.base[grp][seen % NB][wg], seen / NB & 1, &bars.never, limit);
     bulk_wait_group0();
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ---- MMAs: t's high and low halves against the same rows of B
     const uint32_t idesc = idesc_bf16(128, kBlockCols);
     const uint64_t hd = sdesc_kmajor_sw128(smem_u32(s_hi)), ld = sdesc_kmajor_sw128(smem_u32(s_lo));
-    int st = 0, ph = 0, db = 0, dph = 0, sph = 0;
+    int st = 0, ph = 0, sph = 0;
+    uint32_t dph = 0;  // the product buffers' phases, a bit each
+    int64_t q = 0;     // blocks so far: block q goes to buffer q % 2
     bool ok = true;
     for (int64_t w = w0; w < w1 && ok;) {
       const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
@@ -393,13 +429,16 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
       w += blk1 - blk0;
       const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
       const int rank = rank_of(p, t.a), ks = (rank + 15) / 16;
+      q += blk1 - blk0;
       if (rank == 0) continue;
       if (lane == 0) {
         ok = mbar_wait(&bars.sfull, sph, abort, limit);
         for (int blk = blk0; blk < blk1 && ok; ++blk) {
+          const int db = static_cast<int>(q - (blk1 - blk)) & 1;
           ok = mbar_wait(&bars.bfull[st], ph, abort, limit) &&
-               mbar_wait(&bars.dempty[db], dph ^ 1, abort, limit);
+               mbar_wait(&bars.dempty[db], (dph >> db & 1) ^ 1, abort, limit);
           if (!ok) break;
+          dph ^= 1u << db;
           tc_fence_after();
           const uint64_t bd = sdesc_kmajor_sw128(smem_u32(b_ring + st * kOperand));
           for (int k = 0; k < ks; ++k) {
@@ -410,8 +449,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
           umma_commit(&bars.bempty[st]);
           umma_commit(&bars.dfull[db]);
           if (++st == kBStages) st = 0, ph ^= 1;
-          db ^= 1;
-          dph ^= db == 0;
         }
       }
       sph ^= 1;
@@ -424,7 +461,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
     __syncwarp();
   } else {
     // ---- B_a's rows: thread = chunk (8 ranks) c of rows r, r + 16, ...
-    const int bt = tid - 160, r = bt >> 3, c = bt & 7;
+    const int bt = tid - 288, r = bt >> 3, c = bt & 7;
     int st = 0, ph = 1, filled = 0, given = 0;
     bool ok = true;
     for (int64_t w = w0; w < w1 && ok;) {
@@ -468,7 +505,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
   }
   __syncthreads();
   if (tid == 0 && *abort) atomicMax(p.status, kStatusTimeout);
-  if (warp == 4) tmem_dealloc(tmem, 256);
+  if (warp == 8) tmem_dealloc(tmem, 256);
 }
 
 }  // namespace
@@ -478,20 +515,21 @@ cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st) {
   const int64_t tiles = full + a.L < a.M ? full + a.L : a.M;
   const int Rp = (a.R + 15) / 16 * 16;
   const int smem1 = kShrinkStages * (128 * 128 + Rp * 128) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(lora_shrink_large_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+  cudaError_t e = allow_smem<lora_shrink_large_kernel>(kShrinkStages * (128 * 128 * 2) + 1024);
   if (e != cudaSuccess) return e;
   e = launch_pdl(lora_shrink_large_kernel, dim3(static_cast<unsigned>(tiles), a.splits),
                  dim3(kShrinkThreads), smem1, st, a);
   if (e != cudaSuccess) return e;
-  auto run = [&](auto kern, int KT, int NB) {
-    const int smem = (2 + kBStages) * KT * 128 * 128 + NB * 128 * kRowPitch + 1024;
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto expand = [&](auto kt) {
+    constexpr int KT = decltype(kt)::value, NB = KT == 1 ? 2 : 1;
+    constexpr int smem = (2 + kBStages) * KT * 128 * 128 + 2 * NB * 128 * kRowPitch + 1024;
+    cudaError_t r = allow_smem<lora_expand_large_kernel<KT, NB>>(smem);
     if (r != cudaSuccess) return r;
-    return launch_pdl(kern, dim3(num_sms), dim3(kExpandThreads), smem, st, a);
+    return launch_pdl(lora_expand_large_kernel<KT, NB>, dim3(num_sms), dim3(kExpandThreads), smem,
+                      st, a);
   };
-  if (a.R <= 64) return run(lora_expand_large_kernel<1, 4>, 1, 4);
-  return run(lora_expand_large_kernel<2, 2>, 2, 2);
+  return a.R <= 64 ? expand(std::integral_constant<int, 1>{})
+                   : expand(std::integral_constant<int, 2>{});
 }
 
 }  // namespace fp8bq

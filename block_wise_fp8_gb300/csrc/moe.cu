@@ -45,8 +45,6 @@
 //
 // Routing is computed by every CTA for itself: at these sizes that is cheaper
 // than one CTA's result handed to the others.
-#include <atomic>
-
 #include "common.cuh"
 #include "ptx.cuh"
 #include "quant_math.cuh"
@@ -899,6 +897,11 @@ struct MoeLayout {
   int max_entries, sync_words, planes;
 };
 
+// Counters of the largest call.  Their place and size are the same for all
+// shapes, so that one workspace serves calls of several: they are zero between
+// calls, and nothing else of any call lies there.
+constexpr int kMoeSyncWords = 32 + (kMaxMoeExperts + kMoeMaxTokens * kMoeMaxTopk / 32) * (1 + 65536 / 128);
+
 // Workspace: status word | counters | codes and scales of x (a row a
 // token) and h (a row a token and expert) | the runs'
 // sums of both products, a plane for each run of a sum, by hidden row
@@ -914,7 +917,7 @@ MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk) {
     at += up256(static_cast<size_t>(bytes));
     return here;
   };
-  l.sync = take(l.sync_words * 4);
+  l.sync = take(kMoeSyncWords * 4);
   l.xq = take(M * KB1 * 128);
   l.xs = take(M * KB1 * 4);
   l.hq = take((P + 1) * I);  // and a spare row
@@ -967,19 +970,11 @@ cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *w
       !make_kmajor_map(&m2, w2, static_cast<int64_t>(a.E) * a.H, a.I, 128) ||
       !make_kmajor_map(&mx, a.xq, a.M, KB1 * 128, 16) || !make_kmajor_map(&mh, a.hq, P + 1, a.I, 16))
     return cudaErrorInvalidValue;
-  auto run = [&](auto kern) {
-    // by kernel and device: it may use all shared memory
-    static std::atomic<uint64_t> sets[2];
-    std::atomic<uint64_t> &set = sets[NT == 32];
-    int d = 0;
-    cudaError_t e = cudaGetDevice(&d);
+  auto run = [&](auto nt) {
+    constexpr auto kern = moe_layer_kernel<decltype(nt)::value>;
+    cudaError_t e = allow_smem<moe_layer_kernel<decltype(nt)::value>>(
+        static_cast<int>(dev.max_smem_optin) - 1024);
     if (e != cudaSuccess) return e;
-    if (!(set.load(std::memory_order_relaxed) >> d & 1)) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(dev.max_smem_optin) - 1024);
-      if (e != cudaSuccess) return e;
-      set.fetch_or(uint64_t(1) << d, std::memory_order_relaxed);
-    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident, or an error
@@ -992,7 +987,7 @@ cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *w
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, m13, m2, mx, mh, a);
   };
-  return NT == 16 ? run(moe_layer_kernel<16>) : run(moe_layer_kernel<32>);
+  return NT == 16 ? run(std::integral_constant<int, 16>{}) : run(std::integral_constant<int, 32>{});
 }
 
 }  // namespace fp8bq

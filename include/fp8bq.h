@@ -483,7 +483,8 @@ FP8BQ_API int fp8bq_lora_group(const int32_t *ids, int64_t M, int64_t L, int32_t
  * Offsets outside [0, M] are clamped and order entries outside [0, M) skipped.
  * K % 16 == 0, N % 8 == 0, R % 8 == 0, pitches multiples of 8, pointers 16-byte
  * aligned (ERR_ALIGN); 1 <= R <= 128, 1 <= L <= 512 (ERR_SHAPE).  Workspace:
- * fp8bq_workspace_bytes(FP8BQ_OP_LORA_ADD, M, R, K); two launches. */
+ * fp8bq_workspace_bytes(FP8BQ_OP_LORA_ADD, M, R, K), zeroed once; one that is
+ * large enough serves calls of any shapes.  Two launches. */
 FP8BQ_API int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b,
                              const float *scales, const int32_t *ranks, const int32_t *order,
                              const int32_t *offsets, const void *base, int64_t ld_base, void *y,
@@ -518,7 +519,8 @@ enum { FP8BQ_MOE_SOFTMAX = 0, FP8BQ_MOE_SIGMOID = 1 };
  * M <= 64 (ERR_UNSUPPORTED; for more tokens, fp8bq_grouped_gemm), E <= 512,
  * topk <= min(E, 16), H and I <= 65536 (ERR_SHAPE), H % 16 == 0, I % 128 == 0
  * (ERR_ALIGN).  Workspace: fp8bq_moe_workspace_bytes(M, E, H, I, topk), zeroed
- * once with fp8bq_workspace_init.  The launch is cooperative (one CTA an SM;
+ * once with fp8bq_workspace_init; one that is large enough serves calls of any
+ * sizes.  The launch is cooperative (one CTA an SM;
  * ERR_CUDA where the device cannot hold it). */
 FP8BQ_API int fp8bq_moe_layer(const void *x, int64_t ldx, const float *logits, const float *bias,
                               int score, int renormalize, float routed_scale, int64_t topk,

@@ -91,14 +91,14 @@ def check(y, ref, bound):
     (1, 1, 8, 16, 8), (1, 4, 16, 6144, 6144), (2, 3, 24, 272, 40), (17, 2, 32, 1040, 136),
     (33, 1, 64, 528, 104), (64, 32, 16, 512, 1000), (129, 2, 40, 256, 264),
     (300, 3, 128, 400, 72), (517, 5, 72, 320, 328), (1500, 4, 64, 640, 512),
-    (700, 200, 16, 128, 64)])
+    (700, 200, 16, 128, 64), (256, 1, 8, 64, 8), (1000, 2, 120, 2064, 1160), (9000, 5, 48, 192, 400)])
 def test_products(M, L, R, K, N):
     d = inputs(M, L, R, K, N, seed=M + R)
     y = run(d)
     check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
 
 
-@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("M", [5, 200, 900])
 def test_ranks_hide_what_lies_past_them(M):
     L, R, K, N = 6, 64, 256, 128
     d = inputs(M, L, R, K, N, seed=M, low=0)
@@ -112,7 +112,7 @@ def test_ranks_hide_what_lies_past_them(M):
     assert torch.equal(y[d["ids"] == 0], d["base"][d["ids"] == 0])
 
 
-@pytest.mark.parametrize("M", [3, 190])
+@pytest.mark.parametrize("M", [3, 190, 530])
 def test_in_place_and_pitched(M):
     L, R, K, N = 3, 16, 144, 80
     d = inputs(M, L, R, K, N, seed=9)
@@ -125,36 +125,39 @@ def test_in_place_and_pitched(M):
     assert bool((wide[:, N:] == 3.0).all())
 
 
-def test_no_token_has_an_adapter():
-    d = inputs(70, 4, 16, 128, 96, seed=1)
+@pytest.mark.parametrize("M", [70, 700])
+def test_no_token_has_an_adapter(M):
+    d = inputs(M, 4, 16, 128, 96, seed=1)
     d["ids"].fill_(-1)
     assert torch.equal(run(d), d["base"])
     keep = d["base"].clone()
     assert torch.equal(run(d, y=keep, base=keep), d["base"])
 
 
-def test_bounds_and_indices_outside_the_tokens_touch_nothing():
-    d = inputs(40, 2, 16, 128, 64, seed=2, low=0)
-    order = torch.arange(40, device="cuda", dtype=I32)
+@pytest.mark.parametrize("M", [40, 400])
+def test_bounds_and_indices_outside_the_tokens_touch_nothing(M):
+    d = inputs(M, 2, 16, 128, 64, seed=2, low=0)
+    order = torch.arange(M, device="cuda", dtype=I32)
     order[3], order[5] = -4, 4000
     offsets = torch.tensor([-9, 20, 900], device="cuda", dtype=I32)
-    ids = torch.where(torch.arange(40, device="cuda") < 20, 0, 1).to(I32)
+    ids = torch.where(torch.arange(M, device="cuda") < 20, 0, 1).to(I32)
     ref, bound = reference(d["x"], d["a"], d["b"], d["scales"], ids, d["base"], None)
     y = torch.full_like(d["base"], 5.0)
-    ws = fb.new_workspace(fb.OP_LORA_ADD, 40, 16, 128)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, M, 16, 128)
     fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
-    left = torch.ones(40, dtype=torch.bool, device="cuda")
+    left = torch.ones(M, dtype=torch.bool, device="cuda")
     left[[3, 5]] = False
     check(y[left], ref[left], bound[left])
     assert bool((y[~left] == 5.0).all())
 
 
-def test_repeats_are_identical_and_capture_replays():
-    d = inputs(130, 3, 32, 512, 256, seed=5)
+@pytest.mark.parametrize("M", [130, 1100])
+def test_repeats_are_identical_and_capture_replays(M):
+    d = inputs(M, 3, 32, 512, 256, seed=5)
     first = run(d)
     assert torch.equal(first, run(d))
     order, offsets = group(d["ids"], 3)
-    ws = fb.new_workspace(fb.OP_LORA_ADD, 130, 32, 512)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, M, 32, 512)
     y = torch.empty_like(first)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -164,6 +167,20 @@ def test_repeats_are_identical_and_capture_replays():
     d["ids"].copy_((d["ids"] + 2) % 3)
     graph.replay()
     check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
+
+
+def test_one_workspace_serves_calls_of_several_shapes():
+    shapes = [(600, 3, 64, 1024, 264), (5, 2, 128, 6144, 64), (2000, 40, 16, 256, 136),
+              (260, 200, 72, 640, 48), (64, 7, 24, 512, 96)]
+    ws = torch.zeros(max(fb.fp8bq_workspace_bytes(fb.OP_LORA_ADD, M, R, K)
+                         for M, _, R, K, _ in shapes), dtype=torch.uint8, device="cuda")
+    for i, (M, L, R, K, N) in enumerate(shapes + shapes[::-1]):
+        d = inputs(M, L, R, K, N, seed=40 + i)
+        order, offsets = group(d["ids"], L)
+        y = torch.empty_like(d["base"])
+        fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
+        check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
+    assert fb.fp8bq_poll_status(ws) == 0
 
 
 def test_a_stream_of_its_own():

@@ -170,6 +170,16 @@ def test_one_workspace_serves_changing_routes_and_repeats_are_identical():
         assert torch.equal(got[0], run(d, 4, ws=ws)[0])
 
 
+def test_one_workspace_serves_calls_of_several_sizes():
+    sizes = [(64, 40, 256, 256, 16), (1, 3, 1040, 512, 2), (20, 64, 128, 128, 5), (64, 8, 512, 128, 8),
+             (1, 1, 16, 128, 1), (33, 40, 256, 384, 16)]
+    ws = torch.empty(max(fb.fp8bq_moe_workspace_bytes(*v) for v in sizes), dtype=U8, device="cuda")
+    ws.zero_()
+    for i, (M, E, H, I, topk) in enumerate(sizes + sizes[::-1]):
+        d, _ = inputs(M, E, H, I, seed=60 + i)
+        check_all(d, topk, run(d, topk, ws=ws), False, True, 1.0)
+
+
 def test_choice_by_bias_and_close_scores():
     d, g = inputs(32, 96, 256, 128, seed=2)
     bias = torch.randn(96, generator=g, device="cuda") * 0.3
