@@ -286,6 +286,10 @@ struct LaunchShape {
 // K-major E4M3 matrix [rows, K] (pitch K bytes) as a TMA map with a
 // [box_rows x 128 B] box and 128-byte swizzling.
 bool make_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows);
+// BF16 matrix [rows, cols] (row pitch `pitch` elements, a multiple of 8) with a
+// [box_rows x box_cols] box and 128-byte swizzling (box_cols = 64).
+bool make_bf16_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t pitch,
+                   int box_cols, int box_rows);
 // The same through a small per-process cache of recently encoded maps.
 bool cached_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K,
                        int box_rows);

@@ -61,6 +61,19 @@ bool make_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, 
   return r == CUDA_SUCCESS;
 }
 
+bool make_bf16_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t pitch,
+                   int box_cols, int box_rows) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Small cache of encoded tensor maps keyed by (base, rows, K, box rows): repeated
 // calls on the same tensors (every forward of a layer) skip the host-side encode.
 bool cached_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K,

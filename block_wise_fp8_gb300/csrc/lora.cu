@@ -204,6 +204,39 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
       tok[m][r] = v < M ? v : -1;
     }
 
+  const int groups = (p.N + 31) / 32;
+  const int g0 = blockIdx.y * p.ngroups;
+  const int g1 = min(groups, g0 + p.ngroups);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint16_t *bw = p.b + static_cast<int64_t>(t.a) * p.N * p.R + 4 * q;
+  uint4 bs[2][2];
+  uint2 bv[KS][4];
+  // a column group's base and B: not t's, so the first group's are asked for
+  // while the first product still runs
+  auto load = [&](int cg) {
+    const int n0 = cg * 32, nc = n0 + 8 * q;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        bs[m][r] = tok[m][r] >= 0 && nc < p.N
+                       ? *reinterpret_cast<const uint4 *>(p.base + tok[m][r] * p.ldbase + nc)
+                       : zero;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+        const int k = ks * 16 + 4 * q;
+        bv[ks][j] = make_uint2(0, 0);
+        if (col < p.N && k < rank)
+          bv[ks][j] = __ldg(reinterpret_cast<const uint2 *>(
+              bw + static_cast<int64_t>(col) * p.R + ks * 16));
+      }
+  };
+  int cg = g0 + (by_n ? w : 0);
+  if (cg < g1) load(cg);
+
   griddep_wait();
   if (rank > 0) {
     const float scale = __ldg(p.scales + t.a);
@@ -242,39 +275,22 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
   }
   // each lane reads back only what it wrote: no barrier
 
-  const int groups = (p.N + 31) / 32;
-  const int g0 = blockIdx.y * p.ngroups;
-  const int g1 = min(groups, g0 + p.ngroups);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint16_t *bw = p.b + static_cast<int64_t>(t.a) * p.N * p.R + 4 * q;
-  for (int cg = g0 + (by_n ? w : 0); cg < g1; cg += by_n ? 4 : 1) {
-    const int n0 = cg * 32;
-    const int nc = n0 + 8 * q;  // this lane's 8 output columns
-    uint4 bs[2][2];
+  for (bool first = true; cg < g1; cg += by_n ? 4 : 1, first = false) {
+    const int nc = cg * 32 + 8 * q;  // this lane's 8 output columns
+    if (!first) load(cg);
+    if (rank & 15) {  // columns past the rank are not used as numbers
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        bs[m][r] = tok[m][r] >= 0 && nc < p.N
-                       ? *reinterpret_cast<const uint4 *>(p.base + tok[m][r] * p.ldbase + nc)
-                       : zero;
-    uint2 bv[KS][4];
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+      for (int ks = 0; ks < KS; ++ks) {
         const int k = ks * 16 + 4 * q;
-        bv[ks][j] = make_uint2(0, 0);
-        if (col < p.N && k < rank)
-          bv[ks][j] = __ldg(reinterpret_cast<const uint2 *>(
-              bw + static_cast<int64_t>(col) * p.R + ks * 16));
-        if (k + 4 > rank) {  // columns past the rank are not read as numbers
+        if (k + 4 <= rank) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
           if (k + 3 >= rank) bv[ks][j].y &= 0xFFFFu;
           if (k + 2 >= rank) bv[ks][j].y = 0;
           if (k + 1 >= rank) bv[ks][j].x &= 0xFFFFu;
         }
       }
+    }
     float acc[2][4][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)

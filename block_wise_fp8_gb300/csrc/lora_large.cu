@@ -12,13 +12,11 @@
 //           The last split of a tile to finish adds them up and writes t as the
 //           second product's operand, so that no CTA of that one adds again.
 //   expand  persistent CTAs take equal runs of (128 tokens, 128 columns) blocks.
-//           Two groups of four warps have a token a thread: a thread copies its row's 256 bytes
-//           of base into shared memory with a bulk copy, two blocks or more
-//           ahead, adds the product's row from TMEM in place and sends it off
-//           with a bulk store, so that rows need not lie next to each other and
-//           no access is narrower than a row of the block.  B_a's rows come by
-//           cp.async; what lies past the adapter's rank is not read but filled
-//           with zeros by the copy.
+//           Two groups of four warps have a token a thread: base comes into
+//           shared memory by TMA, a block of the group's ahead, the product's row
+//           is added to it from TMEM in place, and TMA takes it to y.  B_a's rows
+//           come by cp.async; what lies past the adapter's rank is not read but
+//           filled with zeros by the copy.
 //
 // The direct form reads operands straight into registers, which leaves little in
 // flight: 46 + 140 us at 4096 tokens, 6144 -> 24576, rank 64, where these take
@@ -54,10 +52,9 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void bulk_store_1d(void *dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-               "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
+// An arrival on `bar` once all of this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_when_copied(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void bulk_wait_group_read() {
@@ -241,12 +238,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
 constexpr int kExpandThreads = 416;  // 8 row warps, 1 issuing, 4 copying B
 constexpr int kRowThreads = 256;
 constexpr int kBlockCols = 128;
-constexpr int kRowPitch = kBlockCols * 2 + 16;  // bytes: 16-byte reads of 8 rows meet no bank twice
-constexpr int kBStages = 2;
+constexpr int kGroupBytes = 8 * kBlockCols * 2;  // eight rows of a block
+constexpr int kBufBytes = 16 * kGroupBytes;
+constexpr int kMaxBStages = 3;
 
 struct ExpandBars {
   uint64_t base[2][2][4];  // by row group, its buffer, warp
-  uint64_t bfull[kBStages], bempty[kBStages];
+  uint64_t bfull[kMaxBStages], bempty[kMaxBStages];
   uint64_t dfull[2], dempty[2];
   uint64_t sfull, done;
   uint32_t tmem, abort, never;
@@ -264,10 +262,13 @@ __device__ int count_tiles(const int *offsets, int L, int M, bool rest) {
 
 // KT: 64-wide tiles of the rank (R <= 64 KT); NB: base buffers of a row group
 template <int KT, int NB>
-__global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(const LoraArgs p) {
+__global__ void __launch_bounds__(kExpandThreads, 1)
+    lora_expand_large_kernel(const __grid_constant__ CUtensorMap base_map,
+                             const __grid_constant__ CUtensorMap y_map, const LoraArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ ExpandBars bars;
   constexpr int kOperand = KT * 128 * 128;  // bytes of one 128-row operand
+  constexpr int kBStages = KT == 1 ? 3 : 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int M = static_cast<int>(p.M), Rp = (p.R + 15) / 16 * 16;
   volatile uint32_t *abort = &bars.abort;
@@ -310,7 +311,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
     // own product buffer and base buffers; a thread has a token of the tile
     const int grp = warp >> 2, wg = warp & 3, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(wg * 32) << 16;
-    uint8_t *const mine = base_ring + (grp * NB * 128 + row) * kRowPitch;
+    uint8_t *const mine = base_ring + grp * NB * kBufBytes + (wg * 4 + (lane >> 3)) * kGroupBytes;
+    const int gr = lane & 7;  // row of its eight, and those
+    const uint32_t peers = 0xFFu << (lane & 24);
     int dph = 0;            // the product buffer's phase
     int bufs = 0, seen = 0; // blocks whose base was asked for, and those that arrived
     int64_t q = 0;          // blocks of this CTA so far, both groups'
@@ -324,23 +327,45 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
       const int rank = rank_of(p, t.a);
       int tok = row < t.count ? __ldg(p.order + t.start + row) : -1;
       if (tok >= M) tok = -1;
-      const uint16_t *src = p.base + (tok < 0 ? 0 : tok * p.ldbase);
-      uint16_t *dst = p.y + (tok < 0 ? 0 : tok * p.ldy);
+      // eight tokens that lie next to each other move as two boxes of 64 columns,
+      // 128-byte swizzled; others by plain 16-byte accesses of their eight lanes,
+      // held in the same way (a bulk copy a row costs the copy unit about 10 ns:
+      // 256 of them a block took 2.4 us against the 1.5 us that HBM needs)
+      const int tok0 = __shfl_sync(0xFFFFFFFFu, tok, lane & 24);
+      const uint32_t next = __ballot_sync(0xFFFFFFFFu, tok >= 0 && tok == tok0 + gr);
+      const bool box = (next >> (lane & 24) & 0xFFu) == 0xFFu;
       auto ask = [&](int blk) {  // base of block blk into the next buffer
         const int b = bufs % NB;
-        const uint32_t bytes = min(kBlockCols, p.N - blk * kBlockCols) * 2;
         uint64_t *bar = &bars.base[grp][b][wg];
-        if (tok >= 0) {
-          mbar_arrive_expect_tx(bar, bytes);
-          bulk_load_1d(mine + b * 128 * kRowPitch, src + blk * kBlockCols, bytes, bar);
+        uint8_t *to = mine + b * kBufBytes;
+        if (box) {
+          if (gr == 0) {
+            mbar_arrive_expect_tx(bar, kGroupBytes);
+            tma_load_2d(to, &base_map, bar, blk * kBlockCols, tok);
+            tma_load_2d(to + 1024, &base_map, bar, blk * kBlockCols + 64, tok);
+          } else {
+            mbar_arrive(bar);
+          }
         } else {
-          mbar_arrive(bar);
+          const int cols = min(kBlockCols, p.N - blk * kBlockCols);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int rt = __shfl_sync(peers, tok, (lane & 24) + r);
+            if (rt < 0) continue;
+            const uint16_t *from = p.base + rt * p.ldbase + blk * kBlockCols;
+#pragma unroll
+            for (int c = gr; c < kBlockCols / 8; c += 8)
+              if (c * 8 < cols)
+                copy16_async(smem_u32(to) + (c >> 3) * 1024 + sw128(r, gr), from + c * 8, 16);
+          }
+          arrive_when_copied(bar);
         }
         ++bufs;
       };
       const int first = blk0 + (static_cast<int>(q ^ grp) & 1);
       int asked = first;
       bulk_wait_group_read<0>();  // the buffers' last stores have read them
+      __syncwarp();
       for (; ok && asked < blk1 && asked < first + 2 * (NB - 1); asked += 2) ask(asked);
       if (NB == 1 && ok && asked < blk1) ask(asked), asked += 2;
       // t's rows of the tile, once the last tile's products are done
@@ -366,7 +391,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) continue;
         ++seen;
-        uint8_t *my = mine + b * 128 * kRowPitch;
+        uint8_t *const my = mine + b * kBufBytes;
         const int cols = min(kBlockCols, p.N - blk * kBlockCols);
         if (rank > 0) {
           mbar_wait(&bars.dfull[grp], dph, abort, limit);
@@ -386,25 +411,51 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
               if (lane == 0) mbar_arrive(&bars.dempty[grp]);
             }
             const uint32_t *d = v[c0 / 32 & 1];
+            // chunk c0 / 8 + i of this row
+            uint4 *at[4], h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint4 *at = reinterpret_cast<uint4 *>(my + (c0 + i * 8) * 2);
-              const uint4 h = *at;
-              const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+              const int c = c0 / 8 + i;
+              at[i] = reinterpret_cast<uint4 *>(
+                  my + (c >> 3) * 1024 + sw128(gr, c & 7));
+              h[i] = *at[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t hw[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
               uint32_t o[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 o[j] = pack_bf16(bf16_lo(hw[j]) + __uint_as_float(d[i * 8 + 2 * j]),
                                  bf16_hi(hw[j]) + __uint_as_float(d[i * 8 + 2 * j + 1]));
-              *at = make_uint4(o[0], o[1], o[2], o[3]);
+              *at[i] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
         }
         fence_proxy_async_smem();
-        if (tok >= 0) bulk_store_1d(dst + blk * kBlockCols, my, cols * 2);
+        __syncwarp();
+        if (box) {
+          if (gr == 0) {
+            tma_store_2d(&y_map, my, blk * kBlockCols, tok);
+            if (cols > 64) tma_store_2d(&y_map, my + 1024, blk * kBlockCols + 64, tok);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int rt = __shfl_sync(peers, tok, (lane & 24) + r);
+            if (rt < 0) continue;
+            uint16_t *out = p.y + rt * p.ldy + blk * kBlockCols;
+#pragma unroll
+            for (int c = gr; c < kBlockCols / 8; c += 8)
+              if (c * 8 < cols)
+                *reinterpret_cast<uint4 *>(out + c * 8) =
+                    *reinterpret_cast<const uint4 *>(my + (c >> 3) * 1024 + sw128(r, gr));
+          }
+        }
         bulk_commit_group();
         if (asked < blk1) {  // into the buffer of the store before (of this one, if it is the only)
           bulk_wait_group_read<NB - 1>();
+          __syncwarp();
           ask(asked);
           asked += 2;
         }
@@ -412,6 +463,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
       q += blk1 - blk0;
     }
     // copies still in flight land before the memory is given up
+    copies_wait<0>();
     for (; seen < bufs; ++seen)
       mbar_wait(&bars.base[grp][seen % NB][wg], seen / NB & 1, &bars.never, limit);
     bulk_wait_group0();
@@ -492,8 +544,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_large_kernel(co
         copies_commit();
         ++filled;
         if (++st == kBStages) st = 0, ph ^= 1;
-        if (filled - given == kBStages) {  // the oldest has landed
-          copies_wait<kBStages - 1>();
+        if (filled - given == 2) {  // the one before has landed
+          copies_wait<1>();
           fence_proxy_async_smem();
           mbar_arrive(&bars.bfull[given++ % kBStages]);
         }
@@ -520,13 +572,17 @@ cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st) {
   e = launch_pdl(lora_shrink_large_kernel, dim3(static_cast<unsigned>(tiles), a.splits),
                  dim3(kShrinkThreads), smem1, st, a);
   if (e != cudaSuccess) return e;
+  CUtensorMap base_map, y_map;
+  if (!make_bf16_map(&base_map, a.base, a.M, a.N, a.ldbase, 64, 8) ||
+      !make_bf16_map(&y_map, a.y, a.M, a.N, a.ldy, 64, 8))
+    return cudaErrorInvalidValue;
   auto expand = [&](auto kt) {
     constexpr int KT = decltype(kt)::value, NB = KT == 1 ? 2 : 1;
-    constexpr int smem = (2 + kBStages) * KT * 128 * 128 + 2 * NB * 128 * kRowPitch + 1024;
+    constexpr int smem = (2 + (KT == 1 ? 3 : 2)) * KT * 128 * 128 + 2 * NB * kBufBytes + 1024;
     cudaError_t r = allow_smem<lora_expand_large_kernel<KT, NB>>(smem);
     if (r != cudaSuccess) return r;
     return launch_pdl(lora_expand_large_kernel<KT, NB>, dim3(num_sms), dim3(kExpandThreads), smem,
-                      st, a);
+                      st, base_map, y_map, a);
   };
   return a.R <= 64 ? expand(std::integral_constant<int, 1>{})
                    : expand(std::integral_constant<int, 2>{});

@@ -199,3 +199,19 @@ def test_no_tokens():
     none = torch.empty(0, device="cuda", dtype=I32)
     fb.fp8bq_lora_add(e, d["a"], d["b"], d["scales"], none, torch.zeros(3, device="cuda", dtype=I32),
                       e, e, fb.new_workspace(fb.OP_LORA_ADD, 0, 16, 64))
+
+
+@pytest.mark.parametrize("N", [40, 72, 128, 200, 1160])
+def test_neighbouring_tokens_go_as_boxes(N):
+    """Requests of many tokens in order: whole warps of neighbours, their ends,
+    and rows in between that are left alone (pitched y, in place too)."""
+    M, L, R, K = 1000, 3, 32, 192
+    d = inputs(M, L, R, K, N, seed=N)
+    d["ids"] = (torch.arange(M, device="cuda") // 237 % (L + 1) - 1).to(I32)
+    ref = reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None)
+    check(run(d), *ref)
+    wide = torch.full((M, N + 24), 3.0, device="cuda", dtype=BF16)
+    wide[:, :N] = d["base"]
+    run(d, y=wide[:, :N], base=wide[:, :N])
+    check(wide[:, :N], *ref)
+    assert bool((wide[:, N:] == 3.0).all())
