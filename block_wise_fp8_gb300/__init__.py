@@ -632,13 +632,17 @@ def _fits(dev, contig, rows=()):
 
 def _call_stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return torch._C._cuda_getCurrentRawStream(dev if dev >= 0 else torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _device():
-    # before the first use of CUDA every tensor is a host one, which the checks find
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+def _device(t) -> int:
+    """Device index of `t` where that is the current device, else -2: the checks
+    then say what is wrong."""
+    if not isinstance(t, torch.Tensor):
+        return -2
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -2
 
 
 def _opt_ptr(t):
@@ -671,7 +675,7 @@ def fp8bq_qk_norm_rope(q, k, q_gamma, k_gamma, table, positions, q_out, k_out, e
     if k is not None:
         HK = _heads(k, "k")[1]
     P, rot = _mat(table, "table")
-    dev = _device()
+    dev = _device(q)
     contig = [(table, _F32, (P, rot)), (positions, _POS, (T,))]
     if q_gamma is not None:
         contig.append((q_gamma, _BF16, (D,)))
@@ -716,7 +720,7 @@ def fp8bq_lora_group(ids, order, offsets, stream=None):
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must be a 1-D tensor of L + 1 elements")
     M, L = ids.shape[0], offsets.shape[0] - 1
-    dev = _device()
+    dev = _device(ids)
     if stream is not None or not _fits(dev, ((ids, _I32, (M,)), (order, _I32, (M,)),
                                              (offsets, _I32, (L + 1,)))):
         _validate("fp8bq_lora_group", [
@@ -736,7 +740,7 @@ def fp8bq_lora_add(x, a, b, scales, order, offsets, base, y, ws, ranks=None, str
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
         raise ValueError("a must be a 3-D tensor [L, R, K]")
     L, R, _ = a.shape
-    dev = _device()
+    dev = _device(x)
     contig = [(a, _BF16, (L, R, K)), (b, _BF16, (L, N, R)), (scales, _F32, (L,)),
               (order, _I32, (M,)), (offsets, _I32, (L + 1,)), (ws, _U8, (_len(ws),))]
     if ranks is not None:
@@ -810,7 +814,7 @@ def fp8bq_moe_layer(x, logits, w13, s13, w2, s2, y, ws, topk: int, score: int = 
     score for the choice only.  ids_out / weights_out [M, topk] receive the
     routing.  Workspace: new_moe_workspace(M, E, H, I, topk)."""
     M, E, H, I = _moe_sizes(x, w13)
-    dev = _device()
+    dev = _device(x)
     _moe_check("fp8bq_moe_layer", M, E, H, I, x, w13, s13, w2, s2, y, ws, (
         ("logits", logits, _F32, (M, E)), ("bias", bias, _F32, (E,)),
         ("ids_out", ids_out, _I32, (M, topk)), ("weights_out", weights_out, _F32, (M, topk))),
@@ -830,7 +834,7 @@ def fp8bq_moe_experts(x, ids, weights, w13, s13, w2, s2, y, ws, stream=None):
     [0, E) are left out) and weights FP32 [M, topk]."""
     M, E, H, I = _moe_sizes(x, w13)
     topk = _mat(ids, "ids")[1]
-    dev = _device()
+    dev = _device(x)
     _moe_check("fp8bq_moe_experts", M, E, H, I, x, w13, s13, w2, s2, y, ws, (
         ("ids", ids, _I32, (M, topk)), ("weights", weights, _F32, (M, topk))), stream, dev)
     if weights is None:

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
   const int kb0 = blockIdx.y * p.kb_split;
   const int kb1 = min((p.K + 63) / 64, kb0 + p.kb_split);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  constexpr int kUnroll = NT <= 2 ? 2 : 1;
+  constexpr int kUnroll = NT <= 4 ? 2 : 1;
 #pragma unroll kUnroll
   for (int kb = kb0 + (by_k ? w : 0); kb < kb1; kb += by_k ? 4 : 1) {
     const int k = kb * 64;
@@ -452,7 +452,7 @@ cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   const int groups = (a.N + 31) / 32;
-  int64_t ng = (groups * expand_tiles + num_sms * 8 - 1) / (num_sms * 8);
+  int64_t ng = (groups * expand_tiles + num_sms * 4 - 1) / (num_sms * 4);
   ng = (ng + 3) / 4 * 4;
   a.ngroups = static_cast<int>(ng < groups ? ng : groups);
   const dim3 grid(static_cast<unsigned>(expand_tiles), (groups + a.ngroups - 1) / a.ngroups),
