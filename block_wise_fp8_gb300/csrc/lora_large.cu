@@ -238,8 +238,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
 constexpr int kExpandThreads = 416;  // 8 row warps, 1 issuing, 4 copying B
 constexpr int kRowThreads = 256;
 constexpr int kBlockCols = 128;
-constexpr int kGroupBytes = 8 * kBlockCols * 2;  // eight rows of a block
-constexpr int kBufBytes = 16 * kGroupBytes;
+constexpr int kWarpBytes = 32 * kBlockCols * 2;  // a warp's rows of a block: two halves of 64 columns
+constexpr int kHalfBytes = kWarpBytes / 2;
+constexpr int kBufBytes = 4 * kWarpBytes;
 constexpr int kMaxBStages = 3;
 
 struct ExpandBars {
@@ -263,8 +264,10 @@ __device__ int count_tiles(const int *offsets, int L, int M, bool rest) {
 // KT: 64-wide tiles of the rank (R <= 64 KT); NB: base buffers of a row group
 template <int KT, int NB>
 __global__ void __launch_bounds__(kExpandThreads, 1)
-    lora_expand_large_kernel(const __grid_constant__ CUtensorMap base_map,
-                             const __grid_constant__ CUtensorMap y_map, const LoraArgs p) {
+    lora_expand_large_kernel(const __grid_constant__ CUtensorMap base8,
+                             const __grid_constant__ CUtensorMap y8,
+                             const __grid_constant__ CUtensorMap base32,
+                             const __grid_constant__ CUtensorMap y32, const LoraArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ ExpandBars bars;
   constexpr int kOperand = KT * 128 * 128;  // bytes of one 128-row operand
@@ -311,9 +314,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     // own product buffer and base buffers; a thread has a token of the tile
     const int grp = warp >> 2, wg = warp & 3, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(wg * 32) << 16;
-    uint8_t *const mine = base_ring + grp * NB * kBufBytes + (wg * 4 + (lane >> 3)) * kGroupBytes;
-    const int gr = lane & 7;  // row of its eight, and those
-    const uint32_t peers = 0xFFu << (lane & 24);
+    uint8_t *const mine = base_ring + grp * NB * kBufBytes + wg * kWarpBytes;
+    const int gr = lane & 7, g8 = lane & 24;  // row of its eight, and those
+    const uint32_t peers = 0xFFu << g8;
     int dph = 0;            // the product buffer's phase
     int bufs = 0, seen = 0; // blocks whose base was asked for, and those that arrived
     int64_t q = 0;          // blocks of this CTA so far, both groups'
@@ -327,22 +330,26 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int rank = rank_of(p, t.a);
       int tok = row < t.count ? __ldg(p.order + t.start + row) : -1;
       if (tok >= M) tok = -1;
-      // eight tokens that lie next to each other move as two boxes of 64 columns,
-      // 128-byte swizzled; others by plain 16-byte accesses of their eight lanes,
-      // held in the same way (a bulk copy a row costs the copy unit about 10 ns:
-      // 256 of them a block took 2.4 us against the 1.5 us that HBM needs)
-      const int tok0 = __shfl_sync(0xFFFFFFFFu, tok, lane & 24);
-      const uint32_t next = __ballot_sync(0xFFFFFFFFu, tok >= 0 && tok == tok0 + gr);
-      const bool box = (next >> (lane & 24) & 0xFFu) == 0xFFu;
+      // 32 tokens that lie next to each other move as two boxes of 64 columns,
+      // 128-byte swizzled, a thread's two instructions; so do eight; others go by
+      // plain 16-byte accesses of their eight lanes, held in the same way (a bulk
+      // copy a row costs the copy unit about 10 ns: 256 of them a block took 2.4
+      // us against the 1.5 us that HBM needs)
+      const int tok0 = __shfl_sync(0xFFFFFFFFu, tok, 0), tok8 = __shfl_sync(0xFFFFFFFFu, tok, g8);
+      const bool all = __ballot_sync(0xFFFFFFFFu, tok >= 0 && tok == tok0 + lane) == 0xFFFFFFFFu;
+      const uint32_t next = __ballot_sync(0xFFFFFFFFu, tok >= 0 && tok == tok8 + gr);
+      const bool box = (next >> g8 & 0xFFu) == 0xFFu;
+      const bool lead = all ? lane == 0 : box && gr == 0;  // issues for its rows
       auto ask = [&](int blk) {  // base of block blk into the next buffer
         const int b = bufs % NB;
         uint64_t *bar = &bars.base[grp][b][wg];
         uint8_t *to = mine + b * kBufBytes;
         if (box) {
-          if (gr == 0) {
-            mbar_arrive_expect_tx(bar, kGroupBytes);
-            tma_load_2d(to, &base_map, bar, blk * kBlockCols, tok);
-            tma_load_2d(to + 1024, &base_map, bar, blk * kBlockCols + 64, tok);
+          if (lead) {
+            const CUtensorMap *map = all ? &base32 : &base8;
+            mbar_arrive_expect_tx(bar, all ? kWarpBytes : kWarpBytes / 4);
+            tma_load_2d(to + g8 * 128, map, bar, blk * kBlockCols, tok);
+            tma_load_2d(to + kHalfBytes + g8 * 128, map, bar, blk * kBlockCols + 64, tok);
           } else {
             mbar_arrive(bar);
           }
@@ -350,13 +357,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
           const int cols = min(kBlockCols, p.N - blk * kBlockCols);
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const int rt = __shfl_sync(peers, tok, (lane & 24) + r);
+            const int rt = __shfl_sync(peers, tok, g8 + r);
             if (rt < 0) continue;
             const uint16_t *from = p.base + rt * p.ldbase + blk * kBlockCols;
 #pragma unroll
             for (int c = gr; c < kBlockCols / 8; c += 8)
               if (c * 8 < cols)
-                copy16_async(smem_u32(to) + (c >> 3) * 1024 + sw128(r, gr), from + c * 8, 16);
+                copy16_async(smem_u32(to) + (c >> 3) * kHalfBytes + sw128(g8 + r, gr), from + c * 8, 16);
           }
           arrive_when_copied(bar);
         }
@@ -366,8 +373,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       int asked = first;
       bulk_wait_group_read<0>();  // the buffers' last stores have read them
       __syncwarp();
-      for (; ok && asked < blk1 && asked < first + 2 * (NB - 1); asked += 2) ask(asked);
-      if (NB == 1 && ok && asked < blk1) ask(asked), asked += 2;
+      for (; ok && asked < blk1 && asked < first + 2 * NB; asked += 2) ask(asked);
       // t's rows of the tile, once the last tile's products are done
       named_bar_sync(1, kRowThreads);
       if (rank > 0) {
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             for (int i = 0; i < 4; ++i) {
               const int c = c0 / 8 + i;
               at[i] = reinterpret_cast<uint4 *>(
-                  my + (c >> 3) * 1024 + sw128(gr, c & 7));
+                  my + (c >> 3) * kHalfBytes + sw128(lane, c & 7));
               h[i] = *at[i];
             }
 #pragma unroll
@@ -435,26 +441,27 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (box) {
-          if (gr == 0) {
-            tma_store_2d(&y_map, my, blk * kBlockCols, tok);
-            if (cols > 64) tma_store_2d(&y_map, my + 1024, blk * kBlockCols + 64, tok);
+          if (lead) {
+            const CUtensorMap *map = all ? &y32 : &y8;
+            tma_store_2d(map, my + g8 * 128, blk * kBlockCols, tok);
+            if (cols > 64) tma_store_2d(map, my + kHalfBytes + g8 * 128, blk * kBlockCols + 64, tok);
           }
         } else {
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const int rt = __shfl_sync(peers, tok, (lane & 24) + r);
+            const int rt = __shfl_sync(peers, tok, g8 + r);
             if (rt < 0) continue;
             uint16_t *out = p.y + rt * p.ldy + blk * kBlockCols;
 #pragma unroll
             for (int c = gr; c < kBlockCols / 8; c += 8)
               if (c * 8 < cols)
                 *reinterpret_cast<uint4 *>(out + c * 8) =
-                    *reinterpret_cast<const uint4 *>(my + (c >> 3) * 1024 + sw128(r, gr));
+                    *reinterpret_cast<const uint4 *>(my + (c >> 3) * kHalfBytes + sw128(g8 + r, gr));
           }
         }
         bulk_commit_group();
-        if (asked < blk1) {  // into the buffer of the store before (of this one, if it is the only)
-          bulk_wait_group_read<NB - 1>();
+        if (asked < blk1) {  // into the same buffer, which the store leaves within 0.1 us
+          bulk_wait_group_read<0>();
           __syncwarp();
           ask(asked);
           asked += 2;
@@ -572,9 +579,11 @@ cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st) {
   e = launch_pdl(lora_shrink_large_kernel, dim3(static_cast<unsigned>(tiles), a.splits),
                  dim3(kShrinkThreads), smem1, st, a);
   if (e != cudaSuccess) return e;
-  CUtensorMap base_map, y_map;
-  if (!make_bf16_map(&base_map, a.base, a.M, a.N, a.ldbase, 64, 8) ||
-      !make_bf16_map(&y_map, a.y, a.M, a.N, a.ldy, 64, 8))
+  CUtensorMap base8, y8, base32, y32;
+  if (!make_bf16_map(&base8, a.base, a.M, a.N, a.ldbase, 64, 8) ||
+      !make_bf16_map(&y8, a.y, a.M, a.N, a.ldy, 64, 8) ||
+      !make_bf16_map(&base32, a.base, a.M, a.N, a.ldbase, 64, 32) ||
+      !make_bf16_map(&y32, a.y, a.M, a.N, a.ldy, 64, 32))
     return cudaErrorInvalidValue;
   auto expand = [&](auto kt) {
     constexpr int KT = decltype(kt)::value, NB = KT == 1 ? 2 : 1;
@@ -582,7 +591,7 @@ cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st) {
     cudaError_t r = allow_smem<lora_expand_large_kernel<KT, NB>>(smem);
     if (r != cudaSuccess) return r;
     return launch_pdl(lora_expand_large_kernel<KT, NB>, dim3(num_sms), dim3(kExpandThreads), smem,
-                      st, base_map, y_map, a);
+                      st, base8, y8, base32, y32, a);
   };
   return a.R <= 64 ? expand(std::integral_constant<int, 1>{})
                    : expand(std::integral_constant<int, 2>{});
