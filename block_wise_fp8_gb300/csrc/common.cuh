@@ -133,11 +133,11 @@ struct LoraArgs {
   uint64_t wait_limit_ns;
 };
 constexpr int kLoraTickets = 1024;   // more than the tiles of any call with several splits
-constexpr int64_t kLoraLarge = 256;  // tokens from which the form of lora_large.cu runs
+bool lora_is_large(int64_t M, int64_t L);  // whether the form of lora_large.cu runs
 cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st);
 // K splits of the first product (a pure function, so that the workspace's size
 // and the launch agree)
-int lora_splits(int64_t M, int64_t K, int *kb_split);
+int lora_splits(int64_t M, int64_t K, bool large, int *kb_split);
 cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st);
 cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int *offsets,
                               cudaStream_t st);

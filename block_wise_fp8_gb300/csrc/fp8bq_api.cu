@@ -262,12 +262,14 @@ struct LoraLayout {
 LoraLayout lora_layout(int64_t M, int64_t R, int64_t K) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   int per;
-  const size_t planes = static_cast<size_t>(lora_splits(M, K, &per));
+  // either form's, since the number of adapters is the call's
+  const int direct = lora_splits(M, K, false, &per), large = lora_splits(M, K, true, &per);
+  const size_t planes = static_cast<size_t>(direct > large ? direct : large);
   LoraLayout l;
   l.tickets = 256;
   l.part = l.tickets + kLoraTickets * 4;
   l.t = l.part + up(planes * static_cast<size_t>(M) * static_cast<size_t>(R) * 4);
-  l.total = l.t + (M < kLoraLarge ? 0 : up(static_cast<size_t>(M) * ((R + 15) / 16 * 16) * 4));
+  l.total = l.t + (lora_is_large(M, 1) ? up(static_cast<size_t>(M) * ((R + 15) / 16 * 16) * 4) : 0);
   return l;
 }
 size_t lora_workspace(int64_t M, int64_t R, int64_t K) { return lora_layout(M, R, K).total; }

@@ -420,13 +420,20 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const int *id
 
 }  // namespace
 
-// Splits of the first product.  Few tokens: enough that each warp has a K block
+// Which form runs.  The form for many tokens moves 128 tokens of an adapter at a
+// time and is better where its tiles are full enough: 192 tokens of 4 adapters,
+// 6144 -> 6144, rank 32, take it 16.6 us and the direct form 21.5, 1024 tokens of
+// 4 23.8 and 36.8; but 1024 tokens of 32 adapters, all in the batch, 50 and 27, 256
+// of 32 62 and 15.  At 128 tokens of 4 adapters both take 15 us.
+bool lora_is_large(int64_t M, int64_t L) { return M >= 128 && M >= 48 * L; }
+
+// Splits of the first product.  Direct form: enough that each warp has a K block
 // (four a split) up to 8 tokens, fewer above, where there are more tiles and the
-// second product reads every split's sums for every column group.  Many: a CTA
-// an SM over about M / 128 + 2 tiles.
-int lora_splits(int64_t M, int64_t K, int *kb_split) {
+// second product reads every split's sums for every column group.  Many tokens: a
+// CTA an SM over about M / 128 + 2 tiles.
+int lora_splits(int64_t M, int64_t K, bool large, int *kb_split) {
   const int kbs = static_cast<int>((K + 63) / 64);
-  int splits = M < kLoraLarge ? (M <= 8 ? 24 : 8) : static_cast<int>(152 / (M / 128 + 2));
+  int splits = !large ? (M <= 8 ? 24 : 8) : static_cast<int>(152 / (M / 128 + 2));
   if (splits > 24) splits = 24;
   if (splits > (kbs + 3) / 4) splits = (kbs + 3) / 4;
   if (splits < 1) splits = 1;
@@ -436,9 +443,10 @@ int lora_splits(int64_t M, int64_t K, int *kb_split) {
 }
 
 cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
-  a.splits = lora_splits(a.M, a.K, &a.kb_split);
+  const bool large = lora_is_large(a.M, a.L);
+  a.splits = lora_splits(a.M, a.K, large, &a.kb_split);
   a.copy_rest = a.y != a.base;
-  if (a.M >= kLoraLarge) return launch_lora_large(a, num_sms, st);
+  if (large) return launch_lora_large(a, num_sms, st);
   // each segment adds at most one partly filled tile; none is empty
   const int64_t full = (a.M + kTile - 1) / kTile;
   const int64_t shrink_tiles = full + a.L < a.M ? full + a.L : a.M;

@@ -91,7 +91,8 @@ def check(y, ref, bound):
     (1, 1, 8, 16, 8), (1, 4, 16, 6144, 6144), (2, 3, 24, 272, 40), (17, 2, 32, 1040, 136),
     (33, 1, 64, 528, 104), (64, 32, 16, 512, 1000), (129, 2, 40, 256, 264),
     (300, 3, 128, 400, 72), (517, 5, 72, 320, 328), (1500, 4, 64, 640, 512),
-    (700, 200, 16, 128, 64), (256, 1, 8, 64, 8), (1000, 2, 120, 2064, 1160), (9000, 5, 48, 192, 400)])
+    (700, 200, 16, 128, 64), (256, 1, 8, 64, 8), (1000, 2, 120, 2064, 1160), (9000, 5, 48, 192, 400), (2500, 500, 16, 128, 72),
+    (127, 1, 16, 256, 64), (128, 1, 16, 256, 64), (191, 4, 16, 256, 64), (192, 4, 16, 256, 64)])
 def test_products(M, L, R, K, N):
     d = inputs(M, L, R, K, N, seed=M + R)
     y = run(d)
@@ -215,3 +216,23 @@ def test_neighbouring_tokens_go_as_boxes(N):
     run(d, y=wide[:, :N], base=wide[:, :N])
     check(wide[:, :N], *ref)
     assert bool((wide[:, N:] == 3.0).all())
+
+
+@pytest.mark.parametrize("M,L,R,N,free", [(2100, 3, 16, 9000, 0.5), (1300, 6, 72, 16392, 0.1),
+                                          (5000, 2, 24, 4104, 0.95), (3000, 40, 32, 8200, 0.3)])
+def test_many_blocks_are_shared_out(M, L, R, N, free):
+    """Enough blocks that CTAs take some of them in turn, among them runs of rows
+    without an adapter and of adapters of rank 0."""
+    d = inputs(M, L, R, 64, N, seed=M)
+    g = torch.Generator("cuda").manual_seed(1)
+    d["ids"] = torch.where(torch.rand(M, generator=g, device="cuda") < free, -1, d["ids"]).to(I32)
+    ranks = torch.tensor([R - 8 * (i % 3) if i != 1 else 0 for i in range(L)], device="cuda", dtype=I32)
+    order, offsets = group(d["ids"], L)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, M, R, 64)
+    ref = reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], ranks)
+    for _ in range(2):
+        y = torch.full_like(d["base"], 5.0)
+        fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws,
+                          ranks=ranks)
+        assert fb.fp8bq_poll_status(ws) == 0
+        check(y, *ref)
