@@ -131,6 +131,7 @@ struct LoraArgs {
   int copy_rest;         // y is not base: rows without an adapter are copied
   uint32_t *status;
   uint64_t wait_limit_ns;
+  int fault;             // fault injection, as GemmArgs::fault_skip_first_load
 };
 constexpr int kLoraTickets = 1024;   // more than the tiles of any call with several splits
 bool lora_is_large(int64_t M, int64_t L);  // whether the form of lora_large.cu runs

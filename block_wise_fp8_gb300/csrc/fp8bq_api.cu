@@ -1001,6 +1001,7 @@ int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, con
       !aligned(y, 16) || !aligned(scales, 4) || !aligned(ranks, 4) || !aligned(order, 4) ||
       !aligned(offsets, 4))
     return FP8BQ_ERR_ALIGN;
+  if (y == base && ldy != ld_base) return FP8BQ_ERR_SHAPE;
   if (!ws || ws_bytes < lora_workspace(M, R, K)) return FP8BQ_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return FP8BQ_ERR_ALIGN;
   DeviceInfo dev;
@@ -1019,6 +1020,7 @@ int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, con
   p.M = M, p.N = static_cast<int>(N), p.K = static_cast<int>(K);
   p.L = static_cast<int>(L), p.R = static_cast<int>(R);
   p.status = static_cast<uint32_t *>(ws), p.wait_limit_ns = wait_limit_ns();
+  if (lora_is_large(M, L)) p.fault = fault_skip_first_load();  // the other form has no waits
   return finish_launch(0, launch_lora_add(p, dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 

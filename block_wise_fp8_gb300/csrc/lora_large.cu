@@ -126,6 +126,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
     }
     bool ok = true;
     int issued = 0;
+    auto give = [&](int s) {  // fault injection: the first stage's wait runs out
+      if (!(p.fault && blockIdx.x == 0 && blockIdx.y == 0 && s == 0))
+        mbar_arrive(&bars.full[s % kShrinkStages]);
+    };
     for (int s = 0; s < steps; ++s) {
       const int st = s % kShrinkStages;
       if (s >= kShrinkStages)
@@ -145,14 +149,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
       if (s >= kShrinkLag) {
         copies_wait<kShrinkLag>();
         fence_proxy_async_smem();
-        mbar_arrive(&bars.full[(s - kShrinkLag) % kShrinkStages]);
+        give(s - kShrinkLag);
       }
     }
     copies_wait<0>();
     fence_proxy_async_smem();
     if (ok)
-      for (int s = max(0, issued - kShrinkLag); s < issued; ++s)
-        mbar_arrive(&bars.full[s % kShrinkStages]);
+      for (int s = max(0, issued - kShrinkLag); s < issued; ++s) give(s);
   } else if (steps > 0 && lane == 0) {
     const uint32_t idesc = idesc_bf16(128, Rp);
     for (int s = 0; s < steps; ++s) {

@@ -22,7 +22,10 @@
  *   (§分块 GEMM 的后端分派), the residual add + RMSNorm that precedes the
  *   activation quantiser, fused with it ("GLM-5.3 推理全链路(十七)", §第1站),
  *   and the grouped (MoE) block GEMM over experts' weights [E, N, K]
- *   ("SGLang 源码完全拆解(十九)", §MoE:专家权重多一个维度).
+ *   ("SGLang 源码完全拆解(十九)", §MoE:专家权重多一个维度).  Beside the linear
+ *   stand a whole mixture-of-experts layer for a few tokens, low-rank adapters
+ *   of many requests, and the norm of query and key heads with the rotary
+ *   embedding.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -62,7 +65,8 @@
  *    the environment, read once.  After a timeout the outputs are undefined
  *    and the workspace must be zeroed again (fp8bq_workspace_init).  For
  *    tests, FP8BQ_FAULT_INJECT=skip_first_load:<n> (read once) makes the next
- *    n GEMM launches skip one tile copy so that their waits run out.
+ *    n GEMM launches (and MoE layers, and adapter calls in their form for many
+ *    tokens) skip one tile copy so that their waits run out.
  *  - No C++ exception crosses this interface.
  */
 #ifndef FP8BQ_H
@@ -479,7 +483,8 @@ FP8BQ_API int fp8bq_lora_group(const int32_t *ids, int64_t M, int64_t L, int32_t
  * x: BF16 [M, K] pitch ldx; a: BF16 [L, R, K]; b: BF16 [L, N, R]; scales: FP32
  * [L]; ranks: DEVICE int32 [L], clamped to [0, R], or NULL (every rank is R) --
  * rows and columns past a rank are never used, whatever they hold; base: BF16
- * [M, N] pitch ld_base; y: BF16 [M, N] pitch ldy, which may be base itself.
+ * [M, N] pitch ld_base; y: BF16 [M, N] pitch ldy, which may be base itself (with
+ * its pitch: ERR_SHAPE).
  * Offsets outside [0, M] are clamped and order entries outside [0, M) skipped.
  * K % 16 == 0, N % 8 == 0, R % 8 == 0, pitches multiples of 8, pointers 16-byte
  * aligned (ERR_ALIGN); 1 <= R <= 128, 1 <= L <= 512 (ERR_SHAPE).  Workspace:

@@ -4,6 +4,11 @@ Bound of y: half a BF16 step of the result (2^-8), t = A x held with 16
 significant bits (2^-17 of each term b t), and binary32 sums of K and of R + 1
 terms: (K + R + 64) * 2^-23 of the sums of magnitudes (one step, not half, a
 term: the tensor instruction may truncate)."""
+import json
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -11,6 +16,7 @@ import block_wise_fp8_gb300 as fb
 
 pytestmark = pytest.mark.gpu
 BF16, I32 = torch.bfloat16, torch.int32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def group_ref(ids, L):
@@ -236,3 +242,30 @@ def test_many_blocks_are_shared_out(M, L, R, N, free):
                           ranks=ranks)
         assert fb.fp8bq_poll_status(ws) == 0
         check(y, *ref)
+
+
+CHILD = r"""
+import json, torch
+import block_wise_fp8_gb300 as fb
+from test_gpu_lora import inputs, group, run, check, reference
+d = inputs(700, 2, 32, 2048, 256, seed=1)
+order, offsets = group(d["ids"], 2)
+ws = fb.new_workspace(fb.OP_LORA_ADD, 700, 32, 2048)
+y = torch.empty_like(d["base"])
+fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
+res = [fb.fp8bq_poll_status(ws)]
+check(run(d), *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
+print("RESULT " + json.dumps(res))
+"""
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """The first CTA never hands over its first stage: the waits behind it are
+    bounded, the status says so, and the next call on a fresh workspace is right."""
+    env = dict(os.environ, FP8BQ_FAULT_INJECT="skip_first_load:1", FP8BQ_WAIT_LIMIT_MS="50",
+               PYTHONPATH=ROOT + os.pathsep + os.path.join(ROOT, "tests"))
+    p = subprocess.run([sys.executable, "-c", CHILD], env=env, cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
+    line = [v for v in p.stdout.splitlines() if v.startswith("RESULT ")][0]
+    assert json.loads(line[7:]) == [8]

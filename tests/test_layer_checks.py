@@ -114,7 +114,7 @@ def c_lora(x=A, ldx=64, a=A, b=A, sc=A, ranks=0, order=A, off=A, base=A, ldb=40,
 def test_lora_abi():
     assert c_lora(M=0, x=0, y=0, ws=0) == OK
     for kw in (dict(M=-1), dict(L=0), dict(L=513), dict(R=0), dict(R=136), dict(ldb=32),
-               dict(ldy=32), dict(ldx=48), dict(K=0), dict(Nn=0)):
+               dict(ldy=32), dict(ldy=48), dict(ldx=48), dict(K=0), dict(Nn=0)):
         assert c_lora(**kw) == SHAPE, kw
     for kw in (dict(R=12), dict(K=56), dict(Nn=36), dict(ldb=44), dict(x=A + 2), dict(a=A + 8),
                dict(b=A + 8), dict(base=A + 4), dict(y=A + 4), dict(order=A + 2), dict(ws=A + 16),
