@@ -314,7 +314,11 @@ struct MoeCfg {
   static constexpr int kTokens = NT == 16 ? 16 : kMoeMaxTokens;
   static constexpr int kStage = 2 * kTileBytes + kTokens * 128;
   static constexpr int kCols = kTokens;              // TMEM columns of one partial tile
-  static constexpr int kMaxStages = 4;  // a stage has a TMEM buffer of two tiles
+  // Four stages (64 KB and more of weights in flight an SM): with six the copies
+  // queue for 8 us and more in HBM, which delays everything else (67.6 against
+  // 73.7 us at one token of 8 experts of 7168 x 2048), with three HBM idles (74).
+  static constexpr int kMaxStages = kMaxRing;  // a stage has a TMEM buffer of two tiles
+  static constexpr int kTmemCols = kMaxStages * 2 * kCols;
 };
 
 template <int NT>
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   uint32_t *const all_done = a.sync + 1;    // CTAs without a run left
   uint32_t *const leaving = a.sync + 2;
   uint32_t *const claim = a.sync + 3;       // runs taken, past the first round
-  uint32_t *const units_done = a.sync + 5;  // hidden groups published,
+  uint32_t *const units_done = a.sync + 4;  // hidden groups published,
   uint32_t *const ready = a.sync + 32;      // [entries]: by entry
   uint32_t *const unit_cnt = ready + a.max_entries;  // [entries * G1]: runs done
   const uint32_t quant_ctas = min(ctas, a.M * KB1);
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     tma_prefetch_desc(&maph);
   }
   if (warp == 1) {
-    tmem_alloc(&bars.tmem, 512);
+    tmem_alloc(&bars.tmem, C::kTmemCols);
     tmem_relinquish();
   }
   for (int e = tid; e < 2 * a.E; e += kMoeThreads) mask[e] = 0;
@@ -882,7 +886,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (*abort) atomicMax(a.status, kStatusTimeout);
     bars.last = atom_add_acq_rel_gpu(leaving, 1) == static_cast<uint32_t>(ctas - 1);
   }
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
   __syncthreads();
   if (bars.last)  // the last CTA leaves the counters as it found them
     for (int i = tid; i < a.sync_words; i += kMoeThreads) a.sync[i] = 0;
