@@ -16,6 +16,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// What BF16(v) = hi leaves of v; nothing of an infinite one, which would make
+// inf - inf of it.
+__device__ __forceinline__ float low_half(float v, float hi) {
+  return isinf(hi) ? 0.0f : v - hi;
+}
+
 struct Tile {
   int a, start, count;  // adapter (L: no adapter), first sorted row, rows
 };

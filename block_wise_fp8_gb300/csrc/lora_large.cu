@@ -19,8 +19,10 @@
 //           filled with zeros by the copy.
 //
 // The direct form reads operands straight into registers, which leaves little in
-// flight: 46 + 140 us at 4096 tokens, 6144 -> 24576, rank 64, where these take
-// the times that the notes on each kernel give.
+// flight: 46 + 140 us at 4096 tokens, 6144 -> 24576, rank 64, where these take 17
+// + 62 us (x at 3.0 TB/s: 32 tiles of tokens in a few splits are too few bytes in
+// flight for more; base and y at 6.6 TB/s, HBM's rate) and 95 us with the two
+// launches and the hand-over of t between them.
 #include "lora.cuh"
 
 namespace fp8bq {
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
           const float x = c * 8 + 2 * j < rank ? v[2 * j] * scale : 0.0f;
           const float y = c * 8 + 2 * j + 1 < rank ? v[2 * j + 1] * scale : 0.0f;
           hi[j] = pack_bf16(x, y);
-          lo[j] = pack_bf16(x - bf16_lo(hi[j]), y - bf16_hi(hi[j]));
+          lo[j] = pack_bf16(low_half(x, bf16_lo(hi[j])), low_half(y, bf16_hi(hi[j])));
         }
         uint16_t *out = p.t + (static_cast<int64_t>(t.start) + row) * 2 * Rp + c * 8;
         *reinterpret_cast<uint4 *>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);

@@ -119,6 +119,23 @@ def test_ranks_hide_what_lies_past_them(M):
     assert torch.equal(y[d["ids"] == 0], d["base"][d["ids"] == 0])
 
 
+@pytest.mark.parametrize("M", [5, 200, 900])
+def test_an_infinite_input_stays_infinite_and_in_its_row(M):
+    L, R, K, N = 2, 16, 256, 128
+    d = inputs(M, L, R, K, N, seed=M, low=0)
+    d["a"][:, :, 7] = 0.5
+    d["b"][:, ::2, :] = d["b"][:, ::2, :].abs() + 0.25   # same signs: every term is +inf
+    d["scales"].fill_(1.5)
+    clean = run(d)
+    d["x"][3, 7] = float("inf")
+    y = run(d)
+    assert bool((y[3, ::2] == float("inf")).all())
+    ref, _ = reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None)
+    assert torch.equal(y[3].isnan(), ref[3].isnan())
+    rest = torch.arange(M, device="cuda") != 3
+    assert torch.equal(y[rest], clean[rest])
+
+
 @pytest.mark.parametrize("M", [3, 190, 530])
 def test_in_place_and_pitched(M):
     L, R, K, N = 3, 16, 144, 80

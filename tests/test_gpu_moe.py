@@ -239,6 +239,19 @@ def test_tokens_routed_by_the_caller(M, E, H, I, topk):
     check(y, *reference(d, ids.long(), w))
 
 
+@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_nonfinite_inputs_stay_in_their_token(M, value):
+    d, _ = inputs(M, 6, 272, 256, seed=70)
+    clean = run(d, 2)
+    d["x"][1, 200] = value
+    got = run(d, 2)
+    assert bool(got[0][1].isnan().all())       # the group's scale or its code is no number
+    rest = torch.arange(M, device="cuda") != 1
+    assert torch.equal(got[0][rest], clean[0][rest])
+    assert torch.equal(got[1], clean[1]) and torch.equal(got[2], clean[2])
+
+
 def test_zero_rows_pitched_input_and_guarded_output():
     M, E, H, I, topk = 6, 5, 272, 128, 2
     d, _ = inputs(M, E, H, I, seed=7)
