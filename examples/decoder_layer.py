@@ -24,13 +24,13 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import block_wise_fp8_gb300 as fb  # noqa: E402
 
 BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-SIZES = dict(H=2048, heads=16, kv_heads=4, D=128, E=32, I=512, topk=4, adapters=8, rank=16)
+SIZES = dict(H=2048, heads=16, kv_heads=2, D=128, E=32, I=512, topk=4, adapters=8, rank=16)
 
 
 class Layer:
     """Weights, quantised once, and the buffers of a step of `M` tokens."""
 
-    def __init__(self, M: int, seed: int = 0, H=2048, heads=16, kv_heads=4, D=128, E=32, I=512,
+    def __init__(self, M: int, seed: int = 0, H=2048, heads=16, kv_heads=2, D=128, E=32, I=512,
                  topk=4, adapters=8, rank=16, context=256):
         g = torch.Generator("cuda").manual_seed(seed)
         rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
