@@ -525,8 +525,10 @@ enum { FP8BQ_MOE_SOFTMAX = 0, FP8BQ_MOE_SIGMOID = 1 };
  * topk <= min(E, 16), H and I <= 65536 (ERR_SHAPE), H % 16 == 0, I % 128 == 0
  * (ERR_ALIGN).  Workspace: fp8bq_moe_workspace_bytes(M, E, H, I, topk), zeroed
  * once with fp8bq_workspace_init; one that is large enough serves calls of any
- * sizes.  The launch is cooperative (one CTA an SM;
- * ERR_CUDA where the device cannot hold it). */
+ * sizes.  The launch is cooperative (one CTA an SM; ERR_CUDA where the device
+ * cannot hold it) and its CTAs wait on one another: let calls on different
+ * streams of one device follow each other by events, as calls that share a
+ * workspace have to anyway. */
 FP8BQ_API int fp8bq_moe_layer(const void *x, int64_t ldx, const float *logits, const float *bias,
                               int score, int renormalize, float routed_scale, int64_t topk,
                               const void *w13, const float *s13, const void *w2, const float *s2,

@@ -34,7 +34,8 @@ def group(ids, L):
 
 
 @pytest.mark.parametrize("M,L", [(0, 3), (1, 1), (31, 5), (32, 512), (33, 2), (1000, 7),
-                                 (1025, 512), (16384, 128), (100003, 33)])
+                                 (1025, 512), (16384, 128), (100003, 33),
+                                 (1024, 9), (2048, 1), (2049, 40), (8191, 511), (8193, 300)])
 def test_group_sorts_stably(M, L):
     g = torch.Generator("cuda").manual_seed(M + L)
     ids = torch.randint(-2, L + 2, (M,), generator=g, device="cuda", dtype=I32)
