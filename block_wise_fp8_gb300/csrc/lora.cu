@@ -214,11 +214,15 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
   const int g1 = min(groups, g0 + p.ngroups);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint16_t *bw = p.b + static_cast<int64_t>(t.a) * p.N * p.R + 4 * q;
-  uint4 bs[2][2];
-  uint2 bv[KS][4];
-  // a column group's base and B: not t's, so the first group's are asked for
+  // Column groups whose loads are in flight (64 tokens of 32 adapters, rank 32,
+  // 6144 -> 6144: 13.0 us for both kernels with two, 13.5 with one, 15.2 with
+  // three, which take too many registers, as two do at higher ranks)
+  constexpr int kAhead = KS <= 2 ? 2 : 1;
+  uint4 bsp[kAhead][2][2];
+  uint2 bvp[kAhead][KS][4];
+  // a column group's base and B: not t's, so the first groups' are asked for
   // while the first product still runs
-  auto load = [&](int cg) {
+  auto load = [&](int cg, uint4(&bs)[2][2], uint2(&bv)[KS][4]) {
     const int n0 = cg * 32, nc = n0 + 8 * q;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -239,8 +243,11 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
               bw + static_cast<int64_t>(col) * p.R + ks * 16));
       }
   };
-  int cg = g0 + (by_n ? w : 0);
-  if (cg < g1) load(cg);
+  const int step = by_n ? 4 : 1;
+  const int first = g0 + (by_n ? w : 0);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (first + u * step < g1) load(first + u * step, bsp[u], bvp[u]);
 
   griddep_wait();
   if (rank > 0) {
@@ -280,9 +287,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
   }
   // each lane reads back only what it wrote: no barrier
 
-  for (bool first = true; cg < g1; cg += by_n ? 4 : 1, first = false) {
+  auto product = [&](int cg, uint4(&bs)[2][2], uint2(&bv)[KS][4]) {
     const int nc = cg * 32 + 8 * q;  // this lane's 8 output columns
-    if (!first) load(cg);
     if (rank & 15) {  // columns past the rank are not used as numbers
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -332,7 +338,16 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
         *reinterpret_cast<uint4 *>(p.y + tok[m][r] * p.ldy + nc) =
             make_uint4(o[0], o[1], o[2], o[3]);
       }
-  }
+  };
+#pragma unroll 1
+  for (int cg = first; cg < g1; cg += kAhead * step)
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = cg + u * step;
+      if (at >= g1) break;
+      product(at, bsp[u], bvp[u]);
+      if (at + kAhead * step < g1) load(at + kAhead * step, bsp[u], bvp[u]);
+    }
 }
 
 // Stable counting sort of tokens by adapter in one cluster of C CTAs: each warp
