@@ -30,7 +30,11 @@
 namespace fp8bq {
 namespace {
 
-constexpr int kWarpTokens = 32;  // two 16-row MMA tiles
+// Tokens of one adapter that a CTA takes: two 16-row MMA tiles, the same for each
+// of its warps, which share out K or the columns.  (Tiles of 128, a warp's own 32
+// tokens each, left a warp all of K: 24.7 us for 44 tokens of one adapter of rank
+// 56, 1200 -> 2648, against 11.7.)
+constexpr int kTile = 32;
 constexpr int kLoraThreads = 128;
 
 // D (16x8, FP32) += A (16x16, BF16) B (16x8, BF16)
@@ -44,9 +48,8 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // t = A_a x over one K split, 64 ranks at most (a higher rank takes a second
-// plane of CTAs, which finds x in L2).  A tile of at most 32 tokens has its K blocks
-// dealt to the four warps, whose sums are joined in a fixed order; a longer
-// one has its tokens dealt to them.
+// plane of CTAs, which finds x in L2).  The K blocks are dealt to the four warps,
+// whose sums are joined in a fixed order.
 template <int NT>  // 8-row groups of A: min(R, 64) <= 8 NT
 __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArgs p) {
   __shared__ float red[3][NT * 8][32];
@@ -55,15 +58,11 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int M = static_cast<int>(p.M);
-  const Tile t = find_tile(p.offsets, p.L, M, blockIdx.x, false);
+  const Tile t = find_tile<kTile>(p.offsets, p.L, M, blockIdx.x, false);
   const int r0 = blockIdx.z * (NT * 8);  // first rank of this plane
   const int rank = rank_of(p, t.a) - r0;
   if (t.count == 0 || rank <= 0) return;
-  const bool by_k = t.count <= kWarpTokens;
-  const int tok0 = by_k ? 0 : w * kWarpTokens;
-  const int here = min(t.count - tok0, kWarpTokens);  // tokens of this warp
-  if (!by_k && here <= 0) return;                      // no barrier follows in that form
-  const bool two = here > 16;
+  const bool two = t.count > 16;
 
   const uint16_t *xr[2][2];
 #pragma unroll
@@ -72,8 +71,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
     for (int r = 0; r < 2; ++r) {
       const int row = m * 16 + r * 8 + g;
       xr[m][r] = nullptr;
-      if (row < here) {
-        const int tok = __ldg(p.order + t.start + tok0 + row);
+      if (row < t.count) {
+        const int tok = __ldg(p.order + t.start + row);
         if (tok >= 0 && tok < M) xr[m][r] = p.x + tok * p.ldx + 16 * q;
       }
     }
@@ -96,7 +95,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
   const uint4 zero = make_uint4(0, 0, 0, 0);
   constexpr int kUnroll = NT <= 4 ? 2 : 1;
 #pragma unroll kUnroll
-  for (int kb = kb0 + (by_k ? w : 0); kb < kb1; kb += by_k ? 4 : 1) {
+  for (int kb = kb0 + w; kb < kb1; kb += 4) {
     const int k = kb * 64;
     const bool in = k + 16 * q < p.K;
     uint4 xv[2][2][2], av[NT][2];
@@ -136,33 +135,31 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
     }
   }
 
-  if (by_k) {
-    if (w > 0) {
+  if (w > 0) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) red[w - 1][(m * NT + n) * 4 + i][lane] = acc[m][n][i];
-    }
-    __syncthreads();
-    if (w > 0) return;
-#pragma unroll
-    for (int o = 0; o < 3; ++o)
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] += red[o][(m * NT + n) * 4 + i][lane];
+        for (int i = 0; i < 4; ++i) red[w - 1][(m * NT + n) * 4 + i][lane] = acc[m][n][i];
   }
-  float *out = p.part + (static_cast<int64_t>(blockIdx.y) * p.M + t.start + tok0) * p.R;
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int o = 0; o < 3; ++o)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] += red[o][(m * NT + n) * 4 + i][lane];
+  float *out = p.part + (static_cast<int64_t>(blockIdx.y) * p.M + t.start) * p.R;
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = m * 16 + r * 8 + g;
-      if (row >= here) continue;
+      if (row >= t.count) continue;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int c = r0 + n * 8 + 2 * q;
@@ -173,10 +170,9 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
     }
 }
 
-// y = base + s_a * B_a t.  A warp holds up to 32 tokens' t as MMA operands in
-// its own part of shared memory and walks groups of 32 columns; in a tile of
-// at most 32 tokens the four warps take different groups, else different
-// tokens.  Rows without an adapter come as a tile of rank 0 and are copied.
+// y = base + s_a * B_a t.  The warps lay t out as MMA operands in shared memory,
+// each a part of it, and walk the groups of 32 columns, each every fourth.  Rows
+// without an adapter come as a tile of rank 0 and are copied.
 template <int KS>  // 16-wide steps of the rank: R <= 16 KS
 __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArgs p) {
   extern __shared__ uint4 sm[];
@@ -186,18 +182,15 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
   const int M = static_cast<int>(p.M);
   // the first product's launch waited for everything before it, so what it
   // read (offsets, order, weights) and the base rows are visible here already
-  const Tile t = find_tile(p.offsets, p.L, M, blockIdx.x, p.copy_rest != 0);
-  const bool by_n = t.count <= kWarpTokens;
-  const int tok0 = by_n ? 0 : w * kWarpTokens;
-  const int here = min(t.count - tok0, kWarpTokens);
-  if (here <= 0) {  // nothing to do, but this grid must not end before the first product's
+  const Tile t = find_tile<kTile>(p.offsets, p.L, M, blockIdx.x, p.copy_rest != 0);
+  if (t.count == 0) {  // nothing to do, but this grid must not end before the first product's
     griddep_wait();
     return;
   }
-  const bool two = here > 16;
+  const bool two = t.count > 16;
   const int rank = rank_of(p, t.a);
   const int ks_n = (rank + 15) / 16;
-  uint4 *my = sm + w * (KS * 2 * 2 * 32) + lane;  // [ks][m][hi, lo][lane]
+  uint4 *my = sm + lane;  // [ks][m][hi, lo][lane]
 
   int tok[2][2];
 #pragma unroll
@@ -205,7 +198,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = m * 16 + r * 8 + g;
-      const int v = row < here ? __ldg(p.order + t.start + tok0 + row) : -1;
+      const int v = row < t.count ? __ldg(p.order + t.start + row) : -1;
       tok[m][r] = v < M ? v : -1;
     }
 
@@ -243,49 +236,46 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
               bw + static_cast<int64_t>(col) * p.R + ks * 16));
       }
   };
-  const int step = by_n ? 4 : 1;
-  const int first = g0 + (by_n ? w : 0);
+  constexpr int kStep = kLoraThreads / 32;
+  const int first = g0 + w;
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (first + u * step < g1) load(first + u * step, bsp[u], bvp[u]);
+    if (first + u * kStep < g1) load(first + u * kStep, bsp[u], bvp[u]);
 
   griddep_wait();
   if (rank > 0) {
     const float scale = __ldg(p.scales + t.a);
-    const float *src = p.part + (static_cast<int64_t>(t.start) + tok0) * p.R;
-    for (int ks = 0; ks < ks_n; ++ks) {
-      const int k = ks * 16 + 4 * q;
+    const float *src = p.part + static_cast<int64_t>(t.start) * p.R;
+    for (int i = w; i < ks_n * 2; i += kLoraThreads / 32) {
+      const int ks = i >> 1, m = i & 1, k = ks * 16 + 4 * q;
+      if (m == 1 && !two) continue;
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (m == 1 && !two) break;
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = m * 16 + r * 8 + g;
-          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (row < here && k < p.R) {
-            const float *at = src + static_cast<int64_t>(row) * p.R + k;
+      for (int r = 0; r < 2; ++r) {
+        const int row = m * 16 + r * 8 + g;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (row < t.count && k < p.R) {
+          const float *at = src + static_cast<int64_t>(row) * p.R + k;
 #pragma unroll 8
-            for (int s = 0; s < p.splits; ++s) {
-              const float4 f = __ldcg(reinterpret_cast<const float4 *>(at + s * p.M * p.R));
-              v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-            }
+          for (int s = 0; s < p.splits; ++s) {
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(at + s * p.M * p.R));
+            v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
           }
-          float l[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = k + i < rank ? v[i] * scale : 0.0f;
-            l[i] = low_half(v[i], __uint_as_float(pack_bf16(0.0f, v[i]) & 0xFFFF0000u));
-          }
-          hi[r] = pack_bf16(v[0], v[1]), hi[2 + r] = pack_bf16(v[2], v[3]);
-          lo[r] = pack_bf16(l[0], l[1]), lo[2 + r] = pack_bf16(l[2], l[3]);
         }
-        my[((ks * 2 + m) * 2 + 0) * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        my[((ks * 2 + m) * 2 + 1) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        float l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = k + i < rank ? v[i] * scale : 0.0f;
+          l[i] = low_half(v[i], __uint_as_float(pack_bf16(0.0f, v[i]) & 0xFFFF0000u));
+        }
+        hi[r] = pack_bf16(v[0], v[1]), hi[2 + r] = pack_bf16(v[2], v[3]);
+        lo[r] = pack_bf16(l[0], l[1]), lo[2 + r] = pack_bf16(l[2], l[3]);
       }
+      my[((ks * 2 + m) * 2 + 0) * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      my[((ks * 2 + m) * 2 + 1) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
-  // each lane reads back only what it wrote: no barrier
+  __syncthreads();
 
   auto product = [&](int cg, uint4(&bs)[2][2], uint2(&bv)[KS][4]) {
     const int nc = cg * 32 + 8 * q;  // this lane's 8 output columns
@@ -340,13 +330,13 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
       }
   };
 #pragma unroll 1
-  for (int cg = first; cg < g1; cg += kAhead * step)
+  for (int cg = first; cg < g1; cg += kAhead * kStep)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int at = cg + u * step;
+      const int at = cg + u * kStep;
       if (at >= g1) break;
       product(at, bsp[u], bvp[u]);
-      if (at + kAhead * step < g1) load(at + kAhead * step, bsp[u], bvp[u]);
+      if (at + kAhead * kStep < g1) load(at + kAhead * kStep, bsp[u], bvp[u]);
     }
 }
 
@@ -539,11 +529,7 @@ cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
   const int ks = (a.R + 15) / 16;
   auto expand = [&](auto k) {
     constexpr int KS = decltype(k)::value;
-    constexpr int smem = KS * 2 * 2 * 32 * 16 * 4;
-    if (smem > 48 * 1024) {
-      cudaError_t e = allow_smem<lora_expand_kernel<KS>>(smem);
-      if (e != cudaSuccess) return e;
-    }
+    constexpr int smem = KS * 2 * 2 * 32 * 16;
     return launch_pdl(lora_expand_kernel<KS>, grid, block, smem, st, a);
   };
   if (ks <= 1) return expand(std::integral_constant<int, 1>{});

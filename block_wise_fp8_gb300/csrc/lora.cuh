@@ -8,8 +8,6 @@
 namespace fp8bq {
 namespace {
 
-constexpr int kTile = 128;      // tokens of one adapter that a CTA takes
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -27,9 +25,10 @@ struct Tile {
 };
 
 // The idx-th tile of the segments (rows offsets[a] .. offsets[a+1]-1 of
-// adapter a, cut into tiles of kTile rows; with `rest`, the rows after the
+// adapter a, cut into tiles of ROWS rows; with `rest`, the rows after the
 // last segment as adapter L).  One warp; count 0 when there is no such tile.
 // Bounds outside [0, M] are clamped.
+template <int ROWS>
 __device__ Tile find_tile(const int *offsets, int L, int M, int idx, bool rest) {
   const int lane = threadIdx.x & 31;
   const int segs = L + (rest ? 1 : 0);
@@ -38,7 +37,7 @@ __device__ Tile find_tile(const int *offsets, int L, int M, int idx, bool rest) 
   int n = 0;
   for (int i = 0; i < per; ++i) {
     const int k = lane * per + i;
-    if (k < segs) n += (max(bound(k + 1) - bound(k), 0) + kTile - 1) / kTile;
+    if (k < segs) n += (max(bound(k + 1) - bound(k), 0) + ROWS - 1) / ROWS;
   }
   int upto = n;
 #pragma unroll
@@ -56,9 +55,9 @@ __device__ Tile find_tile(const int *offsets, int L, int M, int idx, bool rest) 
       const int k = lane * per + i;
       if (k >= segs) break;
       const int s = bound(k), len = max(bound(k + 1) - s, 0);
-      const int tiles = (len + kTile - 1) / kTile;
+      const int tiles = (len + ROWS - 1) / ROWS;
       if (left < tiles) {
-        t = {k, s + left * kTile, min(kTile, len - left * kTile)};
+        t = {k, s + left * ROWS, min(ROWS, len - left * ROWS)};
         break;
       }
       left -= tiles;

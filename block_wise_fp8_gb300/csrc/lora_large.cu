@@ -67,6 +67,8 @@ __device__ __forceinline__ void bulk_wait_group_read() {
 // 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
+constexpr int kTile = 128;  // tokens of one adapter that a CTA takes
+
 // ---------------------------------------------------------------- shrink
 
 constexpr int kShrinkStages = 6;
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_large_kernel(co
   const uint32_t tmem = bars.tmem;
   griddep_wait();
   griddep_launch_dependents();
-  const Tile t = find_tile(p.offsets, p.L, M, blockIdx.x, false);
+  const Tile t = find_tile<kTile>(p.offsets, p.L, M, blockIdx.x, false);
   const int rank = rank_of(p, t.a);
   const int kb0 = blockIdx.y * p.kb_split;
   const int steps = t.count > 0 && rank > 0 ? min((p.K + 63) / 64, kb0 + p.kb_split) - kb0 : 0;
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
       const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
       w += blk1 - blk0;
-      const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
+      const Tile t = find_tile<kTile>(p.offsets, p.L, M, tile, p.copy_rest != 0);
       const int rank = rank_of(p, t.a);
       int tok = row < t.count ? __ldg(p.order + t.start + row) : -1;
       if (tok >= M) tok = -1;
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
       const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
       w += blk1 - blk0;
-      const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
+      const Tile t = find_tile<kTile>(p.offsets, p.L, M, tile, p.copy_rest != 0);
       const int rank = rank_of(p, t.a), ks = (rank + 15) / 16;
       q += blk1 - blk0;
       if (rank == 0) continue;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int tile = static_cast<int>(w / nblk), blk0 = static_cast<int>(w - static_cast<int64_t>(tile) * nblk);
       const int blk1 = static_cast<int>(w1 - w < nblk - blk0 ? blk0 + (w1 - w) : nblk);
       w += blk1 - blk0;
-      const Tile t = find_tile(p.offsets, p.L, M, tile, p.copy_rest != 0);
+      const Tile t = find_tile<kTile>(p.offsets, p.L, M, tile, p.copy_rest != 0);
       const int rank = rank_of(p, t.a);
       if (rank == 0) continue;
       const uint16_t *b = p.b + static_cast<int64_t>(t.a) * p.N * p.R;
