@@ -134,7 +134,8 @@ struct LoraArgs {
   int fault;             // fault injection, as GemmArgs::fault_skip_first_load
 };
 constexpr int kLoraTickets = 1024;   // more than the tiles of any call with several splits
-bool lora_is_large(int64_t M, int64_t L);  // whether the form of lora_large.cu runs
+constexpr int kLoraLargeTokens = 128;  // fewer never take the form of lora_large.cu
+bool lora_is_large(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);  // whether it runs
 cudaError_t launch_lora_large(const LoraArgs &a, int num_sms, cudaStream_t st);
 // K splits of the first product (a pure function, so that the workspace's size
 // and the launch agree)

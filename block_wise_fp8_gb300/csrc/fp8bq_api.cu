@@ -262,14 +262,14 @@ struct LoraLayout {
 LoraLayout lora_layout(int64_t M, int64_t R, int64_t K) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   int per;
-  // either form's, since the number of adapters is the call's
+  // either form's, since N and the number of adapters are the call's
   const int direct = lora_splits(M, K, false, &per), large = lora_splits(M, K, true, &per);
   const size_t planes = static_cast<size_t>(direct > large ? direct : large);
   LoraLayout l;
   l.tickets = 256;
   l.part = l.tickets + kLoraTickets * 4;
   l.t = l.part + up(planes * static_cast<size_t>(M) * static_cast<size_t>(R) * 4);
-  l.total = l.t + (lora_is_large(M, 1) ? up(static_cast<size_t>(M) * ((R + 15) / 16 * 16) * 4) : 0);
+  l.total = l.t + (M >= kLoraLargeTokens ? up(static_cast<size_t>(M) * ((R + 15) / 16 * 16) * 4) : 0);
   return l;
 }
 size_t lora_workspace(int64_t M, int64_t R, int64_t K) { return lora_layout(M, R, K).total; }
@@ -1020,7 +1020,7 @@ int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b, con
   p.M = M, p.N = static_cast<int>(N), p.K = static_cast<int>(K);
   p.L = static_cast<int>(L), p.R = static_cast<int>(R);
   p.status = static_cast<uint32_t *>(ws), p.wait_limit_ns = wait_limit_ns();
-  if (lora_is_large(M, L)) p.fault = fault_skip_first_load();  // the other form has no waits
+  if (lora_is_large(M, N, K, L, R)) p.fault = fault_skip_first_load();  // the other form has no waits
   return finish_launch(0, launch_lora_add(p, dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 

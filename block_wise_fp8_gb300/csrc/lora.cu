@@ -16,7 +16,7 @@
 // 128 contiguous bytes of a row.  In the same way the columns of the second
 // product are dealt out so that a lane ends with 8 neighbouring outputs.
 //
-// Measured: 5.8 us for one token and 13.4 us for 64 tokens of 32 adapters of mixed
+// Measured: 5.0 us for one token and 11.7 us for 64 tokens of 32 adapters of mixed
 // rank up to 32, 6144 -> 6144 (17 MB; 2.6 us at HBM's rate).  What is left is
 // latency: two kernels of one pass each, the way from offsets over order to the
 // first row, and the splits' sums, read back by every column block.
@@ -481,12 +481,21 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const int *id
 
 }  // namespace
 
-// Which form runs.  The form for many tokens moves 128 tokens of an adapter at a
-// time and is better where its tiles are full enough: 192 tokens of 4 adapters,
-// 6144 -> 6144, rank 32, take it 16.6 us and the direct form 21.5, 1024 tokens of
-// 4 23.8 and 36.8; but 1024 tokens of 32 adapters, all in the batch, 50 and 27, 256
-// of 32 62 and 15.  At 128 tokens of 4 adapters both take 15 us.
-bool lora_is_large(int64_t M, int64_t L) { return M >= 128 && M >= 48 * L; }
+// Which form runs.  The form for many tokens has HBM's rate but costs about 15 us
+// before it does anything, and it moves 128 tokens of an adapter at a time; the
+// direct form's time goes with the products, M R (K + N).  So the former runs from
+// a certain size of these on, and where its tiles are full enough for the rank (in
+// the direct form a higher rank costs more for the same bytes).  Measured, direct
+// and other, us:  M 1024, 4 adapters, rank 64, 4096 -> 14336 (M R (K + N) = 1.2e9)
+// 31 and 34, M 2048 52 and 42; M 2048, rank 32, 6144 -> 6144 (0.8e9) 27 and 28, M
+// 4096 43 and 40; M 4096, 16 adapters, rank 64, 6144 -> 24576 153 and 107, 32 of
+// them 165 and 141; M 2048 of 32 104 and 98, of 64 130 and 176; rank 32, 2048 ->
+// 12288, M 8192, 16 adapters 97 and 90, 32 of them 100 and 114; rank 128, 4096 ->
+// 4096, M 2048, 32 adapters 60 and 49, M 1536 of 64 59 and 79.
+bool lora_is_large(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  return M >= kLoraLargeTokens && M * R >= 1300000000 / (K + N) && M * R * R >= 320 * 1024 * L &&
+         M >= 32 * L;
+}
 
 // Splits of the first product.  Direct form: enough that each warp has a K block
 // (four a split) up to 8 tokens, fewer above, where there are more tiles and the
@@ -504,7 +513,7 @@ int lora_splits(int64_t M, int64_t K, bool large, int *kb_split) {
 }
 
 cudaError_t launch_lora_add(LoraArgs a, int num_sms, cudaStream_t st) {
-  const bool large = lora_is_large(a.M, a.L);
+  const bool large = lora_is_large(a.M, a.N, a.K, a.L, a.R);
   a.splits = lora_splits(a.M, a.K, large, &a.kb_split);
   a.copy_rest = a.y != a.base;
   if (large) return launch_lora_large(a, num_sms, st);

@@ -19,9 +19,9 @@
 //           filled with zeros by the copy.
 //
 // The direct form reads operands straight into registers, which leaves little in
-// flight: 46 + 140 us at 4096 tokens, 6144 -> 24576, rank 64, where these take 17
-// + 62 us (x at 3.0 TB/s: 32 tiles of tokens in a few splits are too few bytes in
-// flight for more; base and y at 6.6 TB/s, HBM's rate) and 95 us with the two
+// flight: 146 us at 4096 tokens, 6144 -> 24576, rank 64, where these take 17 + 62
+// us (x at 3.0 TB/s: 32 tiles of tokens in a few splits are too few bytes in
+// flight for more; base and y at 6.6 TB/s, HBM's rate) and 94 us with the two
 // launches and the hand-over of t between them.
 #include "lora.cuh"
 

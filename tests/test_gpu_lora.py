@@ -99,16 +99,21 @@ def check(y, ref, bound):
     (33, 1, 64, 528, 104), (64, 32, 16, 512, 1000), (129, 2, 40, 256, 264),
     (300, 3, 128, 400, 72), (517, 5, 72, 320, 328), (1500, 4, 64, 640, 512),
     (700, 200, 16, 128, 64), (256, 1, 8, 64, 8), (1000, 2, 120, 2064, 1160), (9000, 5, 48, 192, 400), (2500, 500, 16, 128, 72),
-    (127, 1, 16, 256, 64), (128, 1, 16, 256, 64), (191, 4, 16, 256, 64), (192, 4, 16, 256, 64)])
+    (127, 1, 16, 256, 64), (128, 1, 16, 256, 64), (191, 4, 16, 256, 64), (192, 4, 16, 256, 64),
+    # enough tokens and work for the form of many tokens
+    (1400, 1, 128, 4112, 4104), (2600, 3, 72, 2064, 5000), (1700, 6, 48, 6000, 10008),
+    (1300, 3, 120, 4096, 4360), (9000, 2, 24, 2064, 4104), (10300, 1, 16, 4112, 4104),
+    (9000, 1, 8, 10256, 8200), (140, 1, 128, 192, 72712), (2000, 20, 64, 4096, 8192)])
 def test_products(M, L, R, K, N):
     d = inputs(M, L, R, K, N, seed=M + R)
     y = run(d)
     check(y, *reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None))
 
 
-@pytest.mark.parametrize("M", [5, 200, 900])
-def test_ranks_hide_what_lies_past_them(M):
-    L, R, K, N = 6, 64, 256, 128
+@pytest.mark.parametrize("M,K,N", [(5, 256, 128), (200, 256, 128), (900, 256, 128),
+                                   (1900, 4096, 6800)])
+def test_ranks_hide_what_lies_past_them(M, K, N):
+    L, R = 6, 64
     d = inputs(M, L, R, K, N, seed=M, low=0)
     ranks = torch.tensor([0, 1, 7, 21, 64, 1000], device="cuda", dtype=I32)
     for i in range(L):
@@ -120,9 +125,10 @@ def test_ranks_hide_what_lies_past_them(M):
     assert torch.equal(y[d["ids"] == 0], d["base"][d["ids"] == 0])
 
 
-@pytest.mark.parametrize("M", [5, 200, 900])
-def test_an_infinite_input_stays_infinite_and_in_its_row(M):
-    L, R, K, N = 2, 16, 256, 128
+@pytest.mark.parametrize("M,R,K,N", [(5, 16, 256, 128), (200, 16, 256, 128), (900, 16, 256, 128),
+                                     (1900, 64, 4096, 6800)])
+def test_an_infinite_input_stays_infinite_and_in_its_row(M, R, K, N):
+    L = 2
     d = inputs(M, L, R, K, N, seed=M, low=0)
     d["a"][:, :, 7] = 0.5
     d["b"][:, ::2, :] = d["b"][:, ::2, :].abs() + 0.25   # same signs: every term is +inf
@@ -137,9 +143,10 @@ def test_an_infinite_input_stays_infinite_and_in_its_row(M):
     assert torch.equal(y[rest], clean[rest])
 
 
-@pytest.mark.parametrize("M", [3, 190, 530])
-def test_in_place_and_pitched(M):
-    L, R, K, N = 3, 16, 144, 80
+@pytest.mark.parametrize("M,R,K,N", [(3, 16, 144, 80), (190, 16, 144, 80), (530, 16, 144, 80),
+                                     (1500, 64, 2064, 12008)])
+def test_in_place_and_pitched(M, R, K, N):
+    L = 3
     d = inputs(M, L, R, K, N, seed=9)
     d["x"] = torch.cat([d["x"], torch.full((M, 24), float("nan"), device="cuda", dtype=BF16)], 1)[:, :K]
     wide = torch.cat([d["base"], torch.full((M, 16), 3.0, device="cuda", dtype=BF16)], 1)
@@ -150,25 +157,25 @@ def test_in_place_and_pitched(M):
     assert bool((wide[:, N:] == 3.0).all())
 
 
-@pytest.mark.parametrize("M", [70, 700])
-def test_no_token_has_an_adapter(M):
-    d = inputs(M, 4, 16, 128, 96, seed=1)
+@pytest.mark.parametrize("M,R,N", [(70, 16, 96), (700, 16, 96), (2000, 64, 12000)])
+def test_no_token_has_an_adapter(M, R, N):
+    d = inputs(M, 4, R, 128, N, seed=1)
     d["ids"].fill_(-1)
     assert torch.equal(run(d), d["base"])
     keep = d["base"].clone()
     assert torch.equal(run(d, y=keep, base=keep), d["base"])
 
 
-@pytest.mark.parametrize("M", [40, 400])
-def test_bounds_and_indices_outside_the_tokens_touch_nothing(M):
-    d = inputs(M, 2, 16, 128, 64, seed=2, low=0)
+@pytest.mark.parametrize("M,R,N", [(40, 16, 64), (400, 16, 64), (1600, 64, 13000)])
+def test_bounds_and_indices_outside_the_tokens_touch_nothing(M, R, N):
+    d = inputs(M, 2, R, 128, N, seed=2, low=0)
     order = torch.arange(M, device="cuda", dtype=I32)
     order[3], order[5] = -4, 4000
-    offsets = torch.tensor([-9, 20, 900], device="cuda", dtype=I32)
+    offsets = torch.tensor([-9, 20, M + 500], device="cuda", dtype=I32)
     ids = torch.where(torch.arange(M, device="cuda") < 20, 0, 1).to(I32)
     ref, bound = reference(d["x"], d["a"], d["b"], d["scales"], ids, d["base"], None)
     y = torch.full_like(d["base"], 5.0)
-    ws = fb.new_workspace(fb.OP_LORA_ADD, M, 16, 128)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, M, R, 128)
     fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
     left = torch.ones(M, dtype=torch.bool, device="cuda")
     left[[3, 5]] = False
@@ -176,13 +183,13 @@ def test_bounds_and_indices_outside_the_tokens_touch_nothing(M):
     assert bool((y[~left] == 5.0).all())
 
 
-@pytest.mark.parametrize("M", [130, 1100])
-def test_repeats_are_identical_and_capture_replays(M):
-    d = inputs(M, 3, 32, 512, 256, seed=5)
+@pytest.mark.parametrize("M,R,N", [(130, 32, 256), (1100, 32, 256), (1800, 64, 11000)])
+def test_repeats_are_identical_and_capture_replays(M, R, N):
+    d = inputs(M, 3, R, 512, N, seed=5)
     first = run(d)
     assert torch.equal(first, run(d))
     order, offsets = group(d["ids"], 3)
-    ws = fb.new_workspace(fb.OP_LORA_ADD, M, 32, 512)
+    ws = fb.new_workspace(fb.OP_LORA_ADD, M, R, 512)
     y = torch.empty_like(first)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -196,7 +203,7 @@ def test_repeats_are_identical_and_capture_replays(M):
 
 def test_one_workspace_serves_calls_of_several_shapes():
     shapes = [(600, 3, 64, 1024, 264), (5, 2, 128, 6144, 64), (2000, 40, 16, 256, 136),
-              (260, 200, 72, 640, 48), (64, 7, 24, 512, 96)]
+              (260, 200, 72, 640, 48), (64, 7, 24, 512, 96), (1500, 3, 64, 6144, 8200)]
     ws = torch.zeros(max(fb.fp8bq_workspace_bytes(fb.OP_LORA_ADD, M, R, K)
                          for M, _, R, K, _ in shapes), dtype=torch.uint8, device="cuda")
     for i, (M, L, R, K, N) in enumerate(shapes + shapes[::-1]):
@@ -230,7 +237,7 @@ def test_no_tokens():
 def test_neighbouring_tokens_go_as_boxes(N):
     """Requests of many tokens in order: whole warps of neighbours, their ends,
     and rows in between that are left alone (pitched y, in place too)."""
-    M, L, R, K = 1000, 3, 32, 192
+    M, L, R, K = 1900, 3, 64, 10800  # enough work for the form of many tokens
     d = inputs(M, L, R, K, N, seed=N)
     d["ids"] = (torch.arange(M, device="cuda") // 237 % (L + 1) - 1).to(I32)
     ref = reference(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], None)
@@ -243,7 +250,9 @@ def test_neighbouring_tokens_go_as_boxes(N):
 
 
 @pytest.mark.parametrize("M,L,R,N,free", [(2100, 3, 16, 9000, 0.5), (1300, 6, 72, 16392, 0.1),
-                                          (5000, 2, 24, 4104, 0.95), (3000, 40, 32, 8200, 0.3)])
+                                          (5000, 2, 24, 4104, 0.95), (3000, 40, 32, 8200, 0.3),
+                                          (2100, 3, 64, 9976, 0.5), (5000, 2, 40, 8200, 0.95),
+                                          (3000, 9, 64, 8200, 0.3), (1300, 2, 128, 8200, 0.1)])
 def test_many_blocks_are_shared_out(M, L, R, N, free):
     """Enough blocks that CTAs take some of them in turn, among them runs of rows
     without an adapter and of adapters of rank 0."""
@@ -266,9 +275,9 @@ CHILD = r"""
 import json, torch
 import block_wise_fp8_gb300 as fb
 from test_gpu_lora import inputs, group, run, check, reference
-d = inputs(700, 2, 32, 2048, 256, seed=1)
+d = inputs(1500, 2, 64, 6144, 8200, seed=1)
 order, offsets = group(d["ids"], 2)
-ws = fb.new_workspace(fb.OP_LORA_ADD, 700, 32, 2048)
+ws = fb.new_workspace(fb.OP_LORA_ADD, 1500, 64, 6144)
 y = torch.empty_like(d["base"])
 fb.fp8bq_lora_add(d["x"], d["a"], d["b"], d["scales"], order, offsets, d["base"], y, ws)
 res = [fb.fp8bq_poll_status(ws)]
