@@ -252,8 +252,10 @@ __device__ void route_tokens(const MoeArgs &a, int t0, int step, short *id, floa
       if (a.bias) {
         // Keys this close may be ordered by binary32 rounding (a few 2^-24 of
         // a sigmoid below 1 and of the sum): such a choice is made in 64 bits.
+        // (A sum near the lowest number has no border below it: the difference is
+        // -inf and its key 0, that of a taken, masked or missing expert.)
         const float v = value_of(best);
-        const uint32_t near = key_of(v - (1e-6f + 4e-7f * fabsf(v)));
+        const uint32_t near = max(key_of(v - (1e-6f + 4e-7f * fabsf(v))), 1u);
         int close = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) close += key[r] >= near ? 1 : 0;

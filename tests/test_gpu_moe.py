@@ -345,3 +345,28 @@ def test_a_wait_that_runs_out_is_reported():
     assert p.returncode == 0, p.stderr[-2000:]
     line = [v for v in p.stdout.splitlines() if v.startswith("RESULT ")][0]
     assert json.loads(line[7:]) == [8, 8]
+
+
+@pytest.mark.parametrize("mask", [torch.finfo(F32).min, -1e30, float("-inf")])
+@pytest.mark.parametrize("E", [33, 96, 130, 500])
+def test_experts_masked_by_their_bias(E, mask):
+    """Fewer experts are free than are chosen: the masked ones follow by their
+    index, each once, or, at -inf, not at all; a masked logit never does."""
+    M, topk = 9, 6
+    d, g = inputs(M, E, 256, 128, seed=E)
+    bias = torch.full((E,), mask, device="cuda")
+    free = [E - 1, 7, E // 2]
+    bias[free] = torch.tensor([0.3, 0.1, 0.2], device="cuda")
+    d["logits"][:, 2] = float("-inf")
+    d["logits"][3, 7] = float("nan")
+    got = run(d, topk, score=fb.MOE_SIGMOID, bias=bias)
+    usable = d["logits"] > float("-inf")
+    key = torch.where(usable, torch.sigmoid(d["logits"].double()) + bias.double(), float("-inf"))
+    order = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :topk]
+    rid = torch.where(key.gather(1, order) > float("-inf"), order, -1)
+    assert torch.equal(got[1].long(), rid)
+    w = torch.where(rid >= 0, torch.sigmoid(d["logits"].double()).gather(1, rid.clamp(min=0)), 0.0)
+    w = w / w.sum(1, keepdim=True)
+    # exp, sum and quotient in binary32, as in check_all
+    assert bool(((got[2].double() - w).abs() <= w * (E + 32) * 2.0 ** -24 + 1e-37).all())
+    check(got[0], *reference(d, rid, w))
