@@ -552,11 +552,10 @@ cudaError_t launch_lora_group(const int *ids, int64_t M, int L, int *order, int 
   const size_t smem = static_cast<size_t>(kGroupThreads / 32) * (L + 1) * sizeof(int);
   auto run = [&](auto c) {
     constexpr int C = decltype(c)::value;
-    if (smem > 48 * 1024) {
-      cudaError_t e = allow_smem<lora_group_kernel<C>>(kGroupThreads / 32 * (kMaxAdapters + 1) *
-                                                       sizeof(int));
-      if (e != cudaSuccess) return e;
-    }
+    // (always: the default limit of 48 KB counts the static arrays too)
+    cudaError_t e = allow_smem<lora_group_kernel<C>>(kGroupThreads / 32 * (kMaxAdapters + 1) *
+                                                     sizeof(int));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

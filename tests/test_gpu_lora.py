@@ -296,3 +296,27 @@ def test_a_wait_that_runs_out_is_reported():
     assert p.returncode == 0, p.stderr[-2000:]
     line = [v for v in p.stdout.splitlines() if v.startswith("RESULT ")][0]
     assert json.loads(line[7:]) == [8]
+
+
+GROUP_CHILD = r"""
+import torch
+from test_gpu_lora import group, group_ref
+M, sizes = {M}, {sizes}
+for L in sizes:
+    g = torch.Generator("cuda").manual_seed(L)
+    ids = torch.randint(-2, L + 2, (M,), generator=g, device="cuda", dtype=torch.int32)
+    order, offsets = group(ids, L)
+    ro, rf = group_ref(ids, L)
+    assert torch.equal(offsets.cpu(), rf) and torch.equal(order.cpu(), ro), L
+"""
+
+
+@pytest.mark.parametrize("M", [64, 1024, 1025, 2000])
+def test_group_of_any_number_of_adapters(M):
+    """The counters' shared memory passes the default limit between L = 349 and
+    384; in a process of its own, where no call with more adapters came before."""
+    code = GROUP_CHILD.format(M=M, sizes=[1, 348, 349, 350, 351, 365, 366, 367, 382, 383, 384, 512])
+    env = dict(os.environ, PYTHONPATH=ROOT + os.pathsep + os.path.join(ROOT, "tests"))
+    p = subprocess.run([sys.executable, "-c", code], env=env, cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
