@@ -284,12 +284,20 @@ __device__ void route_tokens(const MoeArgs &a, int t0, int step, short *id, floa
       for (int r = 0; r < R; ++r)
         if (lane + r * 32 == at) key[r] = 0;
     }
-    float v = 0.0f;
+    float x = 0.0f, v = 0.0f;
     if (got_at >= 0) {
-      const float x = a.bias ? fminf(__ldg(row + got_at), 3.402823466e38f) : value_of(got);
+      x = a.bias ? fminf(__ldg(row + got_at), 3.402823466e38f) : value_of(got);
       v = a.score == 0 ? expf(x - value_of(top)) / denom : sigmoid(x);
     }
-    if (a.renorm) {
+    // Sigmoids near binary32's smallest numbers (e^-87) and below have shares all
+    // the same; they are taken in 64 bits, whose own end is at e^-709.
+    if (a.renorm && a.score != 0 && __any_sync(0xFFFFFFFFu, x < -80.0f)) {
+      const double p = got_at >= 0 ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : 0.0;
+      double s = p;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+      v = s > 0.0 ? static_cast<float>(p / s) : 0.0f;
+    } else if (a.renorm) {
       float s = v;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);

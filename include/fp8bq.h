@@ -505,11 +505,12 @@ enum { FP8BQ_MOE_SOFTMAX = 0, FP8BQ_MOE_SIGMOID = 1 };
  *   route   the topk experts with the largest logits (a tie goes to the lower
  *           index; with `bias`, the largest sigmoid(logit) + bias), weight
  *           w = softmax over all E logits, or sigmoid(logit), of the expert;
- *           renormalize != 0 divides by the sum over the chosen; times
- *           routed_scale.  NaN and -inf logits (and sums with the bias) are
- *           never chosen: a token with fewer usable experts than topk takes
- *           those (id -1 and weight 0 in the places left), one with none gets
- *           y = 0.
+ *           renormalize != 0 divides by the sum over the chosen, however small
+ *           (sigmoids below e^-709, past binary64's range, count as 0: a token
+ *           with no other gets weights and y of 0); times routed_scale.  NaN and
+ *           -inf logits (and sums with the bias) are never chosen: a token with
+ *           fewer usable experts than topk takes those (id -1 and weight 0 in
+ *           the places left), one with none gets y = 0.
  *   x       group-128 codes q = RNE_sat(x / s), s = max(max|x|, 1e-10) * RN(1/448)
  *           in binary32 (fp8bq_quant_act's rule with a product for its division;
  *           the codes stay inside the layer)

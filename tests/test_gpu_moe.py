@@ -370,3 +370,20 @@ def test_experts_masked_by_their_bias(E, mask):
     # exp, sum and quotient in binary32, as in check_all
     assert bool(((got[2].double() - w).abs() <= w * (E + 32) * 2.0 ** -24 + 1e-37).all())
     check(got[0], *reference(d, rid, w))
+
+
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("top", [-20.0, -87.0, -90.0, -200.0, -700.0])
+def test_renormalised_weights_of_very_negative_logits(top, with_bias):
+    """Sigmoids that are small or nothing in binary32 still have shares."""
+    M, E, topk = 5, 12, 4
+    d, g = inputs(M, E, 256, 128, seed=11)
+    d["logits"] = top - 3 * torch.rand(M, E, generator=g, device="cuda")
+    d["logits"][1] = top                       # equal shares
+    d["logits"][2, 4:] -= 60                   # shares of very different size
+    d["logits"][3, ::2] = float("-inf")
+    d["logits"][4, 1:] -= 300                  # one share is all there is
+    bias = torch.randn(E, generator=g, device="cuda") if with_bias else None
+    got = run(d, topk, score=fb.MOE_SIGMOID, renormalize=True, routed_scale=2.5, bias=bias)
+    check_all(d, topk, got, True, True, 2.5, bias)
+    assert bool(((got[2].sum(1) - 2.5).abs() < 1e-5).all())
