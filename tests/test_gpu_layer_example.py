@@ -19,6 +19,7 @@ sys.path.insert(0, os.path.join(ROOT, "examples"))
 
 import block_wise_fp8_gb300 as fb  # noqa: E402
 import decoder_layer  # noqa: E402
+from test_gpu_lora import reference as lora_reference  # noqa: E402
 
 
 @pytest.mark.parametrize("M", [1, 5, 33, 64])
@@ -34,3 +35,34 @@ def test_decoder_layer(M):
     assert float((y.double() - ry).norm() / ry.norm()) < 2.0 ** -2
     first = y.clone()
     assert torch.equal(layer.step(*args)[0], first)
+
+
+@pytest.mark.parametrize("M", [1, 5, 33, 64])
+def test_adapters_within_the_step(M):
+    """What each adapter call of a step adds to its projection is the adapters'
+    product of that step's own rows, within the bound of that call's own tests."""
+    layer = decoder_layer.Layer(M, H=1024, heads=8, kv_heads=2, D=128, E=16, I=256, topk=4,
+                                adapters=4, rank=24, context=31)
+    calls = []
+    add = layer._adapters
+
+    def watched(x, lora, y):
+        x0, y0 = x.clone(), y.clone()
+        add(x, lora, y)
+        calls.append((x0, lora, y0, y.clone()))
+
+    layer._adapters = watched
+    args = decoder_layer.inputs(layer, seed=M, adapters=4)
+    ids = args[3]
+    some = [3, -1, 0, 1, 2][:M]
+    ids[:len(some)] = torch.tensor(some, device="cuda", dtype=ids.dtype)
+    layer.step(*args)
+    assert len(calls) == 2
+    assert torch.equal(calls[0][0], layer.n1) and torch.equal(calls[1][0], layer.attn)
+    for x, (a, b), before, after in calls:
+        want, bound = lora_reference(x, a, b, layer.scales, ids, before, None)
+        assert bool(((after.double() - want).abs() <= bound).all())
+        assert torch.equal(after[ids < 0], before[ids < 0])
+        # the bound is far below what the adapters add
+        added = (want - before.double())[ids >= 0].norm(dim=1)
+        assert bool((bound[ids >= 0].norm(dim=1) < 0.2 * added).all())
