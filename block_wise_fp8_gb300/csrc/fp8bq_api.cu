@@ -307,6 +307,29 @@ int moe_impl(MoeArgs a, const void *x, int64_t ldx, const void *w13, const float
   return finish_launch(0, launch_moe_layer(a, w13, w2, ws, dev, st));
 }
 
+// Whether two of the T x H rows of D values at t * ts + h * hs share a value.
+bool rows_overlap(int64_t T, int64_t H, int64_t D, int64_t ts, int64_t hs) {
+  using wide = __int128;
+  if (T <= 1) ts = 0;
+  if (H <= 1) hs = 0;
+  auto mag = [](int64_t v) { return v < 0 ? -static_cast<wide>(v) : static_cast<wide>(v); };
+  const wide t = mag(ts), h = mag(hs);
+  // the orders that memory has in earnest: heads within tokens, or tokens within heads
+  if ((H <= 1 || h >= D) && (T <= 1 || t >= (H - 1) * h + D)) return false;
+  if ((T <= 1 || t >= D) && (H <= 1 || h >= (T - 1) * t + D)) return false;
+  // others: a row i heads on meets the row of token 0 or of one next to i h / t
+  for (int64_t i = 0; i < H; ++i) {
+    const wide near = t ? i * h / t : 0;
+    for (wide j = near; j <= near + 1; ++j) {
+      if (j >= T || (i == 0 && j == 0)) continue;
+      const wide d = i * h - j * t;
+      if ((d < 0 ? -d : d) < D) return true;
+    }
+    if (t && near >= T && i * h - (T - 1) * t < D) return true;
+  }
+  return false;
+}
+
 int empty_batch(int64_t K, int64_t N) { return (K >= 1 && N >= 1) ? FP8BQ_OK : FP8BQ_ERR_SHAPE; }
 
 int check_parts(const int64_t *parts, int n_parts, int64_t N) {
@@ -960,6 +983,8 @@ int fp8bq_qk_norm_rope(const void *q, int64_t q_ts, int64_t q_hs, int64_t HQ, co
       !aligned(pos, pos_bits / 8))
     return FP8BQ_ERR_ALIGN;
   if ((q_ts | q_hs | k_ts | k_hs | qo_ts | qo_hs | ko_ts | ko_hs) & 7) return FP8BQ_ERR_ALIGN;
+  if (rows_overlap(T, HQ, D, qo_ts, qo_hs) || rows_overlap(T, HK, D, ko_ts, ko_hs))
+    return FP8BQ_ERR_SHAPE;
   DeviceInfo dev;
   RETURN_IF(device_info(&dev));
   RopeArgs a = {};

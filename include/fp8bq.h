@@ -449,7 +449,8 @@ FP8BQ_API int fp8bq_grouped_gemm_masked(const void *q, const float *s_x,
  * `interleaved` is not 0, and values from `rot` on are not rotated.
  * q: BF16, value d of head h of token t at q[t * q_ts + h * q_hs + d] (a slice
  * of the packed QKV rows, for example); k, q_out, k_out likewise.  An output may
- * be its own input (same pointer and strides); no other overlap.  HQ or HK may
+ * be its own input (same pointer and strides); no other overlap, and none among
+ * an output's own heads (ERR_SHAPE).  HQ or HK may
  * be 0 (its pointers NULL).  q_gamma, k_gamma: BF16 [D] or NULL.  table: FP32
  * [P][rot], the cosines of a position's rot/2 angles, then the sines.  pos:
  * DEVICE int32 or int64 [T] (pos_bits 32 or 64); a token whose position lies

@@ -121,3 +121,29 @@ def test_no_tokens():
     e = torch.empty(0, 4, 64, device="cuda", dtype=BF16)
     fb.fp8bq_qk_norm_rope(e, e, None, None, table(4, 64),
                           torch.empty(0, device="cuda", dtype=torch.int64), e, e)
+
+
+def test_outputs_of_any_strides_whose_heads_do_not_overlap():
+    g = torch.Generator("cuda").manual_seed(5)
+    T, H, D = 3, 2, 64
+    # one row for all heads and tokens as input; outputs with heads among the tokens
+    q = torch.randn(1, 1, D, generator=g, device="cuda").to(BF16).expand(T, H, D)
+    tab, pos = table(32, D), torch.arange(T, device="cuda")
+    ref = reference(q, None, tab, pos, 0, False)
+    for ts, hs in ((2 * D, 3 * D), (3 * D, 2 * D), (D, 3 * D), (D + 8, 4 * D), (2 * D, D)):
+        buf = torch.full((10 * D,), 7.0, device="cuda", dtype=BF16)
+        out = buf.as_strided((T, H, D), (ts, hs, 1))
+        fb.fp8bq_qk_norm_rope(q, None, None, None, tab, pos, out, None)
+        check(out, *ref)
+        assert int((buf == 7.0).sum()) == 4 * D    # nothing beside the heads
+    one = torch.empty(1, H, D, device="cuda", dtype=BF16).expand(T, H, D)
+    for out in (one, torch.empty(T, 1, D, device="cuda", dtype=BF16).expand(T, H, D),
+                torch.empty(8 * D, device="cuda", dtype=BF16).as_strided((T, H, D), (D, D, 1))):
+        with pytest.raises(fb.Fp8bqError, match="ERR_SHAPE"):
+            fb.fp8bq_qk_norm_rope(q, None, None, None, tab, pos, out, None)
+        with pytest.raises(fb.Fp8bqError, match="ERR_SHAPE"):
+            fb.fp8bq_qk_norm_rope(q, q, None, None, tab, pos, torch.empty_like(q.contiguous()), out)
+    # one token's expanded token stride means nothing
+    out = torch.empty(1, H, D, device="cuda", dtype=BF16)
+    fb.fp8bq_qk_norm_rope(q[:1], None, None, None, tab, pos[:1], out.as_strided((1, H, D), (0, D, 1)), None)
+    check(out, ref[0][:1], ref[1][:1])

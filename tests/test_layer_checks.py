@@ -208,3 +208,12 @@ def test_moe_experts_abi():
                                       P(A), I(M), I(4), I(256), I(128), P(A), S(1 << 30), P(0))
     assert c(M=0, ids=0) == OK
     assert c(ids=0) == NULL and c(w=0) == NULL and c(ids=A + 2) == ALIGN and c(topk=17) == SHAPE
+
+
+def test_rope_outputs_whose_heads_overlap():
+    """4 query and 2 key heads of 64 values, 3 tokens; what overlaps is refused
+    whatever the order of the strides (inputs may: q's and k's strides go along)."""
+    for kw in (dict(ts=64), dict(ts=0), dict(hs=0), dict(hs=56), dict(ts=248), dict(ts=-248),
+               dict(ts=-64, hs=64), dict(ts=64, hs=184), dict(ts=96, hs=128), dict(T=1, hs=48),
+               dict(HQ=1, HK=1, ts=56), dict(HK=0, k=0, ko=0, hs=0)):
+        assert c_rope(**kw) == SHAPE, kw
