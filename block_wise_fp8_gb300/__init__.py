@@ -658,7 +658,8 @@ def _heads(t, name):
 
 
 def _fit_heads(t, shape, dev):
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or
+            t.get_device() != dev):
         return False
     a, b, one = t.stride()
     return one == 1 and a >= 0 and b >= 0

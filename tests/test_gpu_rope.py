@@ -147,3 +147,17 @@ def test_outputs_of_any_strides_whose_heads_do_not_overlap():
     out = torch.empty(1, H, D, device="cuda", dtype=BF16)
     fb.fp8bq_qk_norm_rope(q[:1], None, None, None, tab, pos[:1], out.as_strided((1, H, D), (0, D, 1)), None)
     check(out, ref[0][:1], ref[1][:1])
+
+
+@pytest.mark.parametrize("name", ["q_gamma", "table", "positions", "q_out", "k_out"])
+@pytest.mark.parametrize("value", [[1.0], None, 5])
+def test_what_is_no_tensor_is_refused(name, value):
+    T, H, D = 3, 2, 64
+    q = torch.ones(T, H, D, device="cuda", dtype=BF16)
+    d = dict(q=q, k=q.clone(), q_gamma=None, k_gamma=None, table=table(8, D),
+             positions=torch.zeros(T, device="cuda", dtype=torch.int32), q_out=q.clone(), k_out=q.clone())
+    if name == "q_gamma" and value is None:
+        return
+    d[name] = value
+    with pytest.raises(ValueError):
+        fb.fp8bq_qk_norm_rope(*d.values())
