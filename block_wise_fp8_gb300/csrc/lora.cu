@@ -16,8 +16,9 @@
 // 128 contiguous bytes of a row.  In the same way the columns of the second
 // product are dealt out so that a lane ends with 8 neighbouring outputs.
 //
-// Measured: 5.0 us for one token and 11.7 us for 64 tokens of 32 adapters of mixed
-// rank up to 32, 6144 -> 6144 (17 MB; 2.6 us at HBM's rate).  What is left is
+// Measured with inputs changing from call to call: 6.2 us for one token and 10.2 us
+// for 64 tokens of 32 adapters of mixed rank up to 32, 6144 -> 6144 (17 MB; 2.6 us
+// at HBM's rate; with one input over and over 5.0 and 11.7).  What is left is
 // latency: two kernels of one pass each, the way from offsets over order to the
 // first row, and the splits' sums, read back by every column block.
 //
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
 // the order is fixed), the counters are scanned key by key, over the warps, then
 // over the CTAs, and each warp writes its stretch.  The bytes are nothing; the
 // barriers and a warp's walk over its tokens are what it takes.  Measured with
-// tokens in random order: 2.3 us for 64 tokens of 32 adapters, 6.3 us for 16384 of
+// one set of tokens in random order, over and over: 2.3 us for 64 tokens of 32 adapters, 6.3 us for 16384 of
 // 128 (23 in one CTA; with a match of the lanes' keys, which goes through the
 // different keys one by one, 9.5 and 48).  Up to 1024 tokens, 32 a warp, a
 // cluster's start costs more than it saves: 3.5 us in one CTA, 4.3 in eight; from
@@ -491,7 +492,10 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const int *id
 // 4096 43 and 40; M 4096, 16 adapters, rank 64, 6144 -> 24576 153 and 107, 32 of
 // them 165 and 141; M 2048 of 32 104 and 98, of 64 130 and 176; rank 32, 2048 ->
 // 12288, M 8192, 16 adapters 97 and 90, 32 of them 100 and 114; rank 128, 4096 ->
-// 4096, M 2048, 32 adapters 60 and 49, M 1536 of 64 59 and 79.
+// 4096, M 2048, 32 adapters 60 and 49, M 1536 of 64 59 and 79.  L is the table's
+// size, all that the host knows, and stands for the adapters of the batch: 4096
+// tokens of four adapters, rank 64, 6144 -> 24576, take 96 us with a table of up
+// to 32, 188 in one of 64, where the direct form runs, and 236 in one of 128.
 bool lora_is_large(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   return M >= kLoraLargeTokens && M * R >= 1300000000 / (K + N) && M * R * R >= 320 * 1024 * L &&
          M >= 32 * L;

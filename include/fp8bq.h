@@ -490,7 +490,7 @@ FP8BQ_API int fp8bq_lora_group(const int32_t *ids, int64_t M, int64_t L, int32_t
  * K % 16 == 0, N % 8 == 0, R % 8 == 0, pitches multiples of 8, pointers 16-byte
  * aligned (ERR_ALIGN); 1 <= R <= 128, 1 <= L <= 512 (ERR_SHAPE).  Workspace:
  * fp8bq_workspace_bytes(FP8BQ_OP_LORA_ADD, M, R, K), zeroed once; one that is
- * large enough serves calls of any shapes.  Two launches. */
+ * large enough serves calls of any shapes, of this function alone.  Two launches. */
 FP8BQ_API int fp8bq_lora_add(const void *x, int64_t ldx, const void *a, const void *b,
                              const float *scales, const int32_t *ranks, const int32_t *order,
                              const int32_t *offsets, const void *base, int64_t ld_base, void *y,
@@ -513,8 +513,9 @@ enum { FP8BQ_MOE_SOFTMAX = 0, FP8BQ_MOE_SIGMOID = 1 };
  *           fewer usable experts than topk takes those (id -1 and weight 0 in
  *           the places left), one with none gets y = 0.
  *   x       group-128 codes q = RNE_sat(x / s), s = max(max|x|, 1e-10) * RN(1/448)
- *           in binary32 (fp8bq_quant_act's rule with a product for its division;
- *           the codes stay inside the layer)
+ *           in binary32 (fp8bq_quant_act's rule with a product for its division,
+ *           so that quotients halfway between two codes may go to the other
+ *           one; the codes stay inside the layer)
  *   g, u    rows 0 .. I-1 and I .. 2I-1 of w13[e] times x, as fp8bq_grouped_gemm
  *           up to its BF16 rounding, which is left out
  *   h       = g / (1 + exp(-g)) * u in FP32, quantised by the same rule
@@ -528,7 +529,8 @@ enum { FP8BQ_MOE_SOFTMAX = 0, FP8BQ_MOE_SIGMOID = 1 };
  * topk <= min(E, 16), H and I <= 65536 (ERR_SHAPE), H % 16 == 0, I % 128 == 0
  * (ERR_ALIGN).  Workspace: fp8bq_moe_workspace_bytes(M, E, H, I, topk), zeroed
  * once with fp8bq_workspace_init; one that is large enough serves calls of any
- * sizes.  The launch is cooperative (one CTA an SM; ERR_CUDA where the device
+ * sizes, of these two functions alone (another call's sums would stand where
+ * the counters are).  The launch is cooperative (one CTA an SM; ERR_CUDA where the device
  * cannot hold it) and its CTAs wait on one another: let calls on different
  * streams of one device follow each other by events, as calls that share a
  * workspace have to anyway. */
