@@ -32,6 +32,9 @@ __all__ = [
     "OP_LORA_ADD", "fp8bq_qk_norm_rope", "fp8bq_lora_group", "fp8bq_lora_add",
     "MOE_SOFTMAX", "MOE_SIGMOID", "MOE_MAX_TOKENS", "fp8bq_moe_layer", "fp8bq_moe_experts",
     "fp8bq_moe_workspace_bytes", "new_moe_workspace",
+    "OP_PROMPT_ATTENTION", "fp8bq_prompt_attention", "fp8bq_kv4_append", "fp8bq_kv4_read",
+    "fp8bq_kv4_attention", "fp8bq_kv4_evict", "fp8bq_kv4_workspace_bytes", "new_kv4_workspace",
+    "new_kv4_cache",
     "library_path",
     "fp8bq_version", "fp8bq_status_string", "fp8bq_last_cuda_error",
     "fp8bq_workspace_bytes", "fp8bq_workspace_init", "fp8bq_poll_status",
@@ -47,7 +50,7 @@ __all__ = [
 SCALE_ROW_MAJOR, SCALE_COL_MAJOR = 0, 1
 (OP_GEMM, OP_LINEAR, OP_MX_GEMM, OP_MX_LINEAR, OP_STATIC_GEMM,
  OP_STATIC_LINEAR, OP_CHANNEL_GEMM, OP_CHANNEL_LINEAR, OP_UE8M0_GEMM,
- OP_UE8M0_LINEAR, OP_GROUPED_GEMM, OP_LORA_ADD) = range(12)
+ OP_UE8M0_LINEAR, OP_GROUPED_GEMM, OP_LORA_ADD, OP_PROMPT_ATTENTION) = range(13)
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1               # router scores of fp8bq_moe_layer
 MOE_MAX_TOKENS = 64
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024      # FP8BQ_NOALLOC_SCRATCH_BYTES
@@ -126,6 +129,12 @@ def _load():
         "fp8bq_qk_norm_rope": (I32, [P] * 10 + [F32] + [P] * 4 + [I32, I32] + [P] * 9),
         "fp8bq_lora_group": (I32, [P] * 6),
         "fp8bq_lora_add": (I32, [P] * 20),
+        "fp8bq_prompt_attention": (I32, [P] * 11 + [F32] + [P] * 10),
+        "fp8bq_kv4_append": (I32, [P] * 7 + [I32] + [P] * 4 + [F32, F32] + [P] * 4),
+        "fp8bq_kv4_read": (I32, [P] * 4 + [I32, F32, F32] + [P] * 10),
+        "fp8bq_kv4_attention": (I32, [P] * 9 + [F32] * 3 + [P] * 12),
+        "fp8bq_kv4_evict": (I32, [P] * 17),
+        "fp8bq_kv4_workspace_bytes": (SZ, [I64] * 6 + [I32]),
         "fp8bq_moe_workspace_bytes": (SZ, [I64, I64, I64, I64, I64]),
         "fp8bq_moe_layer": (I32, [P, I64, P, P, I32, I32, F32, I64, P, P, P, P, P, P, P, I64, I64,
                                   I64, I64, P, SZ, P]),
@@ -846,6 +855,171 @@ def fp8bq_moe_experts(x, ids, weights, w13, s13, w2, s2, y, ws, stream=None):
         s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr(), M, E, H, I, ws.data_ptr(),
         _nbytes(ws), _call_stream(stream, dev))
     _check(status, "fp8bq_moe_experts")
+
+
+# ---------------------------------------------------------------- attention and its cache
+
+def _check_heads(what, dev, stream, heads, contig, optional=None):
+    """`heads`: (name, tensor, shape), `contig`: (name, tensor, dtypes, shape) each;
+    `optional`: one more of `contig`, whose tensor may be None."""
+    more = contig if optional is None or optional[1] is None else (*contig, optional)
+    if stream is None and dev >= 0 and all(_fit_heads(t, s, dev) for _, t, s in heads) and \
+            _fits(dev, [c[1:] for c in more]):
+        return
+    _validate(what, [_Spec(n, t, _BF16, s, kind="heads") for n, t, s in heads] +
+              [_Spec(*c) for c in more], stream)
+
+
+def fp8bq_prompt_attention(q, k, v, offsets, y, ws, scale=None, stream=None):
+    """Causal attention over whole prompts: q [T, HQ, D], k and v [T, HK, D] (any
+    token and head strides: slices of the packed QKV rows), sequences packed one
+    after the other with their bounds in offsets int32 [S + 1], into y [T, HQ, D].
+    scale: 1 / sqrt(D) unless given.  Workspace: new_workspace(OP_PROMPT_ATTENTION,
+    T, HQ, D), one for any sizes."""
+    T, HQ, D = _heads(q, "q")
+    HK = _heads(k, "k")[1]
+    S = _len(offsets) - 1
+    if S < 0:
+        raise ValueError("offsets must be a 1-D tensor of S + 1 elements")
+    dev = _device(q)
+    _check_heads("fp8bq_prompt_attention", dev, stream, (
+        ("q", q, (T, HQ, D)), ("k", k, (T, HK, D)), ("v", v, (T, HK, D)), ("y", y, (T, HQ, D))),
+        (("offsets", offsets, _I32, (S + 1,)), ("ws", ws, _U8, (_len(ws),))))
+    qt, qh, _ = q.stride()
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    yt, yh, _ = y.stride()
+    status = _lib.fp8bq_prompt_attention(
+        q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, offsets.data_ptr(), S,
+        D ** -0.5 if scale is None else scale, y.data_ptr(), yt, yh, T, HQ, HK, D, ws.data_ptr(),
+        _nbytes(ws), _call_stream(stream, dev))
+    _check(status, "fp8bq_prompt_attention")
+
+
+def _cache_sizes(cache, D):
+    """(pages, heads, tokens a page) of a cache [pages, HK, page * 9 * D / 8] of uint8."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be a 3-D tensor [pages, heads, page bytes]")
+    pages, HK, size = cache.shape
+    page, odd = divmod(size * 8, 9 * D) if D > 0 else (0, 1)
+    if odd or page not in (16, 32, 64, 128):
+        raise ValueError(f"cache: {size} bytes are no page of 16, 32, 64 or 128 tokens of heads "
+                         f"of {D}")
+    return pages, HK, page
+
+
+def new_kv4_cache(pages: int, heads: int, page: int, D: int, device="cuda"):
+    """An empty 4-bit cache: uint8 [pages, heads, page * 9 * D / 8], zeroed."""
+    if page not in (16, 32, 64, 128) or D not in (64, 128, 256):
+        raise ValueError("page must be 16, 32, 64 or 128, D 64, 128 or 256")
+    return torch.zeros(pages, heads, page * 9 * D // 8, dtype=torch.uint8, device=device)
+
+
+def _rows_check(what, k, v, slots, cache, weights, stream):
+    T, HK, D = _heads(k, "k")
+    pages, heads, page = _cache_sizes(cache, D)
+    if heads != HK:
+        raise ValueError(f"{what}: the cache has {heads} heads, k has {HK}")
+    dev = _device(k)
+    _check_heads(what, dev, stream, (("k", k, (T, HK, D)), ("v", v, (T, HK, D))),
+                 (("slots", slots, _POS, (T,)), ("cache", cache, _U8, tuple(cache.shape))),
+                 ("weights", weights, _F32, (pages, HK, page)))
+    return T, HK, D, pages, page, dev, 64 if slots.dtype is torch.int64 else 32
+
+
+def fp8bq_kv4_append(k, v, slots, cache, weights=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                     stream=None):
+    """Writes rows k, v [T, HK, D] into the slots (page * page size + place, int32 or
+    int64 [T]; one outside the cache is left out) of a 4-bit cache; `weights` [pages,
+    HK, page size], if given, is zeroed there."""
+    T, HK, D, pages, page, dev, bits = _rows_check("fp8bq_kv4_append", k, v, slots, cache, weights,
+                                                   stream)
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    status = _lib.fp8bq_kv4_append(
+        k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), bits, cache.data_ptr(),
+        pages, page, _opt_ptr(weights), k_scale, v_scale, T, HK, D, _call_stream(stream, dev))
+    _check(status, "fp8bq_kv4_append")
+
+
+def fp8bq_kv4_read(cache, slots, k, v, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Reads slots of a 4-bit cache into rows k, v [T, HK, D]; rows of slots outside
+    the cache are left as they are."""
+    T, HK, D, pages, page, dev, bits = _rows_check("fp8bq_kv4_read", k, v, slots, cache, None,
+                                                   stream)
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    status = _lib.fp8bq_kv4_read(
+        cache.data_ptr(), pages, page, slots.data_ptr(), bits, k_scale, v_scale, k.data_ptr(), kt,
+        kh, v.data_ptr(), vt, vh, T, HK, D, _call_stream(stream, dev))
+    _check(status, "fp8bq_kv4_read")
+
+
+def fp8bq_kv4_workspace_bytes(B: int, Tq: int, HQ: int, HK: int, D: int, max_len: int,
+                              weights: bool = False) -> int:
+    return _lib.fp8bq_kv4_workspace_bytes(B, Tq, HQ, HK, D, max_len, weights)
+
+
+def new_kv4_workspace(B: int, Tq: int, HQ: int, HK: int, D: int, max_len: int,
+                      weights: bool = False, device="cuda", stream=None):
+    """A zero-initialised workspace for fp8bq_kv4_attention at these sizes (max_len: the
+    block table's width times the page size)."""
+    ws = torch.empty(fp8bq_kv4_workspace_bytes(B, Tq, HQ, HK, D, max_len, weights),
+                     dtype=torch.uint8, device=device)
+    fp8bq_workspace_init(ws, stream)
+    return ws
+
+
+def fp8bq_kv4_attention(q, cache, table, lens, y, ws, weights=None, scale=None,
+                        k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Attention of the last Tq tokens of each of B sequences over their pages of a
+    4-bit cache: q and y [B * Tq, HQ, D], block table int32 [B, width], lens int32 [B]
+    (the new tokens included).  weights FP32 [pages, HK, page size], if given, grows
+    by the softmax weight that each cached token gets.  scale: 1 / sqrt(D) unless
+    given.  Workspace: new_kv4_workspace."""
+    N, HQ, D = _heads(q, "q")
+    pages, HK, page = _cache_sizes(cache, D)
+    B, width = _mat(table, "table")
+    if N % B if B else N:
+        raise ValueError(f"fp8bq_kv4_attention: q has {N} rows for {B} sequences")
+    dev = _device(q)
+    _check_heads("fp8bq_kv4_attention", dev, stream, (("q", q, (N, HQ, D)), ("y", y, (N, HQ, D))),
+                 (("cache", cache, _U8, (pages, HK, page * 9 * D // 8)),
+                  ("table", table, _I32, (B, width)), ("lens", lens, _I32, (B,)),
+                  ("ws", ws, _U8, (_len(ws),))), ("weights", weights, _F32, (pages, HK, page)))
+    if N == 0:
+        return
+    qt, qh, _ = q.stride()
+    yt, yh, _ = y.stride()
+    status = _lib.fp8bq_kv4_attention(
+        q.data_ptr(), qt, qh, cache.data_ptr(), pages, page, table.data_ptr(), width,
+        lens.data_ptr(), D ** -0.5 if scale is None else scale, k_scale, v_scale,
+        _opt_ptr(weights), y.data_ptr(), yt, yh, B, N // B, HQ, HK, D, ws.data_ptr(), _nbytes(ws),
+        _call_stream(stream, dev))
+    _check(status, "fp8bq_kv4_attention")
+
+
+def fp8bq_kv4_evict(cache, table, lens, weights, new_table, new_lens, kept, recent: int, D: int,
+                    stream=None):
+    """Keeps kept.shape[2] of each sequence's tokens for every head: the last `recent`
+    and those of the largest weights, copied in order to the pages of new_table int32
+    [B, width'] (pages that nothing else uses).  new_lens int32 [B], kept int32
+    [B, HK, budget]: the tokens' places before, then -1.  D: the heads' size."""
+    pages, HK, page = _cache_sizes(cache, D)
+    B, width = _mat(table, "table")
+    new_width = _mat(new_table, "new_table")[1]
+    budget = _heads(kept, "kept")[2]
+    dev = _device(cache)
+    _check_heads("fp8bq_kv4_evict", dev, stream, (), (
+        ("cache", cache, _U8, (pages, HK, page * 9 * D // 8)), ("table", table, _I32, (B, width)),
+        ("lens", lens, _I32, (B,)), ("weights", weights, _F32, (pages, HK, page)),
+        ("new_table", new_table, _I32, (B, new_width)), ("new_lens", new_lens, _I32, (B,)),
+        ("kept", kept, _I32, (B, HK, budget))))
+    status = _lib.fp8bq_kv4_evict(
+        cache.data_ptr(), pages, page, table.data_ptr(), width, lens.data_ptr(),
+        weights.data_ptr(), new_table.data_ptr(), new_width, new_lens.data_ptr(), kept.data_ptr(),
+        budget, recent, B, HK, D, _call_stream(stream, dev))
+    _check(status, "fp8bq_kv4_evict")
 
 
 # ---------------------------------------------------------------- residual add + RMSNorm

@@ -176,6 +176,81 @@ size_t moe_workspace(int64_t M, int64_t E, int64_t H, int64_t I, int64_t topk);
 cudaError_t launch_moe_layer(MoeArgs a, const void *w13, const void *w2, void *ws,
                              const DeviceInfo &dev, cudaStream_t st);
 
+// The 4-bit paged cache (kv4.cuh, kv4_cache.cu, kv4_attention.cu)
+struct Kv4AppendArgs {
+  const uint16_t *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;
+  const void *slots;  // [T] int32 or int64: page * page size + place
+  uint8_t *cache;
+  float *weights;     // [pages][HK][page size], or nullptr
+  int64_t T, pages;
+  int HK, D, page_log2, slots64;
+  float k_inv, v_inv;  // RN(1 / scale)
+};
+struct Kv4ReadArgs {
+  const uint8_t *cache;
+  const void *slots;
+  uint16_t *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;
+  int64_t T, pages;
+  int HK, D, page_log2, slots64;
+  float k_scale, v_scale;
+};
+struct Kv4EvictArgs {
+  uint8_t *cache;
+  float *weights;
+  const int *table, *lens, *new_table;  // [B][width], [B], [B][new_width]
+  int *new_lens, *kept;                 // [B], [B][HK][budget]
+  int64_t pages, width, new_width;
+  int B, HK, D, page_log2, budget, recent, max_len;
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs &a, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4ReadArgs &a, cudaStream_t st);
+cudaError_t launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st);
+
+constexpr int kKv4MaxBatch = 1024;
+constexpr int kKv4MaxRows = 128;      // query rows of one key/value head
+constexpr int kKv4MaxItems = 65536;   // sequences x heads x row blocks
+struct Kv4AttnArgs {
+  const uint16_t *q;
+  uint16_t *y;
+  int64_t q_ts, q_hs, y_ts, y_hs;
+  const uint8_t *cache;
+  const int *table, *lens;
+  float *weights;
+  int64_t pages, width;
+  int B, Tq, HK, G, D, page_log2, max_len;
+  float scale_log2;  // softmax scale * log2(e) * k_scale
+  float v_scale;
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+  int fault;          // fault injection, as GemmArgs::fault_skip_first_load
+  // set by the launcher: the workspace's parts
+  uint32_t *tickets;  // [kKv4MaxItems] CTAs that have left their part of an item
+  float *part;        // unfinished items' sums
+  float *stats;       // [B * HK * rows] maximum and sum (with weights)
+  float *logits;      // [B * HK * rows][max_len] (with weights)
+};
+size_t kv4_workspace(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t max_len,
+                     bool weights);
+cudaError_t launch_kv4_attention(Kv4AttnArgs a, void *ws, int num_sms, cudaStream_t st);
+
+// Causal attention over whole prompts (prompt_attention.cu)
+constexpr int kMaxPrompts = 1024;
+constexpr int64_t kMaxPromptTokens = int64_t(1) << 19;
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *y;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, y_ts, y_hs;
+  const int *offsets;  // [S + 1]
+  int T, S, HQ, HK, D;
+  float scale_log2;    // softmax scale * log2(e)
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+  int fault;           // fault injection, as GemmArgs::fault_skip_first_load
+};
+cudaError_t launch_prompt_attention(const PromptArgs &a, int num_sms, cudaStream_t st);
+
 // ---------------------------------------------------------------- GEMM
 
 // kModeChannel: one FP32 scale per token (activation row) and per output

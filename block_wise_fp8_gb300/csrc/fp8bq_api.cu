@@ -330,6 +330,43 @@ bool rows_overlap(int64_t T, int64_t H, int64_t D, int64_t ts, int64_t hs) {
   return false;
 }
 
+// 4-bit cache: tokens a page, as a power of two; -1 for a size that is none
+int page_log2(int64_t page) {
+  return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1;
+}
+
+bool positive(float v) { return v > 0.0f && v <= 3.4028235e38f; }
+
+int check_kv4_sizes(int64_t pages, int64_t page, int64_t HK, int64_t D) {
+  if (pages < 1 || pages > (int64_t(1) << 31) - 1 || HK < 1 || HK > 1024) return FP8BQ_ERR_SHAPE;
+  if (page_log2(page) < 0 || (D != 64 && D != 128 && D != 256)) return FP8BQ_ERR_UNSUPPORTED;
+  return FP8BQ_OK;
+}
+
+// rows of keys and values beside the cache (append and read); T > 0
+int check_kv4_rows(const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                   int64_t v_hs, const void *slots, int slot_bits, const void *cache, int64_t T,
+                   int64_t HK, int64_t D) {
+  if (!k || !v || !slots || !cache) return FP8BQ_ERR_NULL;
+  if (T * HK > ((int64_t(1) << 31) - 1) / (D / 8) * 256) return FP8BQ_ERR_SHAPE;  // the grid
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, slot_bits / 8) ||
+      ((k_ts | k_hs | v_ts | v_hs) & 7))
+    return FP8BQ_ERR_ALIGN;
+  return FP8BQ_OK;
+}
+
+// sizes of the attention over the cache
+int check_kv4_attention(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t max_len) {
+  if (B < 0 || B > kKv4MaxBatch || Tq < 1 || HK < 1 || HK > 1024 || HQ < 1 || HQ % HK ||
+      max_len < 0 || max_len > (int64_t(1) << 28))
+    return FP8BQ_ERR_SHAPE;
+  if (D != 64 && D != 128 && D != 256) return FP8BQ_ERR_UNSUPPORTED;
+  const int64_t G = HQ / HK;
+  if (Tq > kKv4MaxRows || G > kKv4MaxRows || G * Tq > kKv4MaxRows) return FP8BQ_ERR_UNSUPPORTED;
+  if (B * HK * ((G * Tq + 7) / 8) > kKv4MaxItems || B * HK > 65535) return FP8BQ_ERR_SHAPE;
+  return FP8BQ_OK;
+}
+
 int empty_batch(int64_t K, int64_t N) { return (K >= 1 && N >= 1) ? FP8BQ_OK : FP8BQ_ERR_SHAPE; }
 
 int check_parts(const int64_t *parts, int n_parts, int64_t N) {
@@ -401,8 +438,9 @@ const char *fp8bq_status_string(int s) {
 int fp8bq_last_cuda_error(void) { return g_last_cuda_error; }
 
 size_t fp8bq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
-  if (op < FP8BQ_OP_GEMM || op > FP8BQ_OP_LORA_ADD || M < 0 || N < 1 || K < 1) return 256;
+  if (op < FP8BQ_OP_GEMM || op > FP8BQ_OP_PROMPT_ATTENTION || M < 0 || N < 1 || K < 1) return 256;
   if (op == FP8BQ_OP_LORA_ADD) return lora_workspace(M, N, K);
+  if (op == FP8BQ_OP_PROMPT_ATTENTION) return 256;  // the status word
   return workspace_layout(op, M, N, K).total;
 }
 
@@ -959,6 +997,163 @@ int fp8bq_grouped_gemm_masked(const void *q, const float *s_x, int s_layout, con
   RETURN_IF(device_info(&dev));
   return gemm_grouped_impl(q, s_x, s_layout, w, s_w, nullptr, masked_m, E, max_m, y, M, N, K,
                            ws, static_cast<cudaStream_t>(stream), dev);
+}
+
+// ------------------------------------------------------------------ attention and its cache
+
+int fp8bq_prompt_attention(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts,
+                           int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
+                           const int32_t *offsets, int64_t S, float scale, void *y, int64_t y_ts,
+                           int64_t y_hs, int64_t T, int64_t HQ, int64_t HK, int64_t D, void *ws,
+                           size_t ws_bytes, void *stream) {
+  if (T < 0 || T > kMaxPromptTokens || S < 0 || S > kMaxPrompts || HK < 1 || HQ < 1 || HQ > 1024 ||
+      HQ % HK || !positive(scale) || !positive(scale * 1.4426950408889634f))
+    return FP8BQ_ERR_SHAPE;
+  if (D < 16 || D > 128 || HQ / HK > 128) return FP8BQ_ERR_UNSUPPORTED;
+  if (D % 16) return FP8BQ_ERR_ALIGN;
+  if (T == 0 || S == 0) return FP8BQ_OK;
+  if (!q || !k || !v || !offsets || !y) return FP8BQ_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(y, 16) ||
+      !aligned(offsets, 4) || ((q_ts | q_hs | k_ts | k_hs | v_ts | v_hs | y_ts | y_hs) & 7))
+    return FP8BQ_ERR_ALIGN;
+  // rows of a tensor map: strides of their own (a size of one has none)
+  constexpr int64_t kMaxStride = int64_t(1) << 38;
+  const int64_t inputs[6][2] = {{T, q_ts}, {HQ, q_hs}, {T, k_ts}, {HK, k_hs}, {T, v_ts}, {HK, v_hs}};
+  for (const auto &s : inputs)
+    if (s[0] > 1 && (s[1] < 1 || s[1] > kMaxStride)) return FP8BQ_ERR_SHAPE;
+  if (rows_overlap(T, HQ, D, y_ts, y_hs)) return FP8BQ_ERR_SHAPE;
+  if (!ws || ws_bytes < 256) return FP8BQ_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  PromptArgs a = {};
+  a.q = static_cast<const uint16_t *>(q), a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v), a.y = static_cast<uint16_t *>(y);
+  a.q_ts = q_ts, a.q_hs = q_hs, a.k_ts = k_ts, a.k_hs = k_hs;
+  a.v_ts = v_ts, a.v_hs = v_hs, a.y_ts = y_ts, a.y_hs = y_hs;
+  a.offsets = offsets, a.T = static_cast<int>(T), a.S = static_cast<int>(S);
+  a.HQ = static_cast<int>(HQ), a.HK = static_cast<int>(HK), a.D = static_cast<int>(D);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.status = static_cast<uint32_t *>(ws), a.wait_limit_ns = wait_limit_ns();
+  a.fault = fault_skip_first_load();
+  return finish_launch(0, launch_prompt_attention(a, dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_kv4_append(const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                     int64_t v_hs, const void *slots, int slot_bits, void *cache, int64_t pages,
+                     int64_t page, float *weights, float k_scale, float v_scale, int64_t T,
+                     int64_t HK, int64_t D, void *stream) {
+  if (T < 0 || T > (int64_t(1) << 31) - 1 || !positive(k_scale) || !positive(v_scale))
+    return FP8BQ_ERR_SHAPE;
+  RETURN_IF(check_kv4_sizes(pages, page, HK, D));
+  if (slot_bits != 32 && slot_bits != 64) return FP8BQ_ERR_UNSUPPORTED;
+  if (T == 0) return FP8BQ_OK;
+  RETURN_IF(check_kv4_rows(k, k_ts, k_hs, v, v_ts, v_hs, slots, slot_bits, cache, T, HK, D));
+  if (!aligned(weights, 4)) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  Kv4AppendArgs a = {};
+  a.k = static_cast<const uint16_t *>(k), a.v = static_cast<const uint16_t *>(v);
+  a.k_ts = k_ts, a.k_hs = k_hs, a.v_ts = v_ts, a.v_hs = v_hs;
+  a.slots = slots, a.slots64 = slot_bits == 64;
+  a.cache = static_cast<uint8_t *>(cache), a.weights = weights;
+  a.T = T, a.pages = pages, a.HK = static_cast<int>(HK), a.D = static_cast<int>(D);
+  a.page_log2 = page_log2(page), a.k_inv = 1.0f / k_scale, a.v_inv = 1.0f / v_scale;
+  return finish_launch(0, launch_kv4_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, const void *slots, int slot_bits,
+                   float k_scale, float v_scale, void *k, int64_t k_ts, int64_t k_hs, void *v,
+                   int64_t v_ts, int64_t v_hs, int64_t T, int64_t HK, int64_t D, void *stream) {
+  if (T < 0 || T > (int64_t(1) << 31) - 1 || !positive(k_scale) || !positive(v_scale))
+    return FP8BQ_ERR_SHAPE;
+  RETURN_IF(check_kv4_sizes(pages, page, HK, D));
+  if (slot_bits != 32 && slot_bits != 64) return FP8BQ_ERR_UNSUPPORTED;
+  if (T == 0) return FP8BQ_OK;
+  RETURN_IF(check_kv4_rows(k, k_ts, k_hs, v, v_ts, v_hs, slots, slot_bits, cache, T, HK, D));
+  if (rows_overlap(T, HK, D, k_ts, k_hs) || rows_overlap(T, HK, D, v_ts, v_hs)) return FP8BQ_ERR_SHAPE;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  Kv4ReadArgs a = {};
+  a.cache = static_cast<const uint8_t *>(cache);
+  a.slots = slots, a.slots64 = slot_bits == 64;
+  a.k = static_cast<uint16_t *>(k), a.v = static_cast<uint16_t *>(v);
+  a.k_ts = k_ts, a.k_hs = k_hs, a.v_ts = v_ts, a.v_hs = v_hs;
+  a.T = T, a.pages = pages, a.HK = static_cast<int>(HK), a.D = static_cast<int>(D);
+  a.page_log2 = page_log2(page), a.k_scale = k_scale, a.v_scale = v_scale;
+  return finish_launch(0, launch_kv4_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8bq_kv4_workspace_bytes(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D,
+                                 int64_t max_len, int weights) {
+  if (check_kv4_attention(B, Tq, HQ, HK, D, max_len) != FP8BQ_OK) return 256;
+  return kv4_workspace(B, Tq, HQ, HK, D, max_len, weights != 0);
+}
+
+int fp8bq_kv4_attention(const void *q, int64_t q_ts, int64_t q_hs, const void *cache, int64_t pages,
+                        int64_t page, const int32_t *table, int64_t width, const int32_t *lens,
+                        float scale, float k_scale, float v_scale, float *weights, void *y,
+                        int64_t y_ts, int64_t y_hs, int64_t B, int64_t Tq, int64_t HQ, int64_t HK,
+                        int64_t D, void *ws, size_t ws_bytes, void *stream) {
+  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+  if (width < 0 || width > (int64_t(1) << 28) || !positive(scale) || !positive(k_scale) ||
+      !positive(v_scale) || !positive(scale_log2))
+    return FP8BQ_ERR_SHAPE;
+  RETURN_IF(check_kv4_sizes(pages, page, HK, D));
+  const int64_t max_len = width * page;
+  RETURN_IF(check_kv4_attention(B, Tq, HQ, HK, D, max_len));
+  if (B == 0) return FP8BQ_OK;
+  if (!q || !cache || (width > 0 && !table) || !lens || !y) return FP8BQ_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(y, 16) || !aligned(table, 4) ||
+      !aligned(lens, 4) || !aligned(weights, 4) || ((q_ts | q_hs | y_ts | y_hs) & 7))
+    return FP8BQ_ERR_ALIGN;
+  if (rows_overlap(B * Tq, HQ, D, y_ts, y_hs)) return FP8BQ_ERR_SHAPE;
+  if (!ws || ws_bytes < kv4_workspace(B, Tq, HQ, HK, D, max_len, weights != nullptr))
+    return FP8BQ_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return FP8BQ_ERR_ALIGN;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  Kv4AttnArgs a = {};
+  a.q = static_cast<const uint16_t *>(q), a.y = static_cast<uint16_t *>(y);
+  a.q_ts = q_ts, a.q_hs = q_hs, a.y_ts = y_ts, a.y_hs = y_hs;
+  a.cache = static_cast<const uint8_t *>(cache);
+  a.table = table, a.lens = lens, a.weights = weights;
+  a.pages = pages, a.width = width, a.B = static_cast<int>(B), a.Tq = static_cast<int>(Tq);
+  a.HK = static_cast<int>(HK), a.G = static_cast<int>(HQ / HK), a.D = static_cast<int>(D);
+  a.page_log2 = page_log2(page), a.max_len = static_cast<int>(max_len);
+  a.scale_log2 = scale_log2, a.v_scale = v_scale;
+  a.wait_limit_ns = wait_limit_ns(), a.fault = fault_skip_first_load();
+  return finish_launch(0, launch_kv4_attention(a, ws, dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bq_kv4_evict(void *cache, int64_t pages, int64_t page, const int32_t *table, int64_t width,
+                    const int32_t *lens, float *weights, const int32_t *new_table,
+                    int64_t new_width, int32_t *new_lens, int32_t *kept, int64_t budget,
+                    int64_t recent, int64_t B, int64_t HK, int64_t D, void *stream) {
+  RETURN_IF(check_kv4_sizes(pages, page, HK, D));
+  constexpr int64_t kMax = int64_t(1) << 28;
+  if (B < 0 || B > kKv4MaxBatch || width < 0 || width > kMax || width * page > kMax || budget < 1 ||
+      budget > kMax || recent < 0 || recent > budget || new_width > kMax ||
+      new_width < (budget + page - 1) / page ||
+      B * HK * budget > ((int64_t(1) << 31) - 1) / (D / 16) * 256)
+    return FP8BQ_ERR_SHAPE;
+  if (B == 0) return FP8BQ_OK;
+  if (!cache || (width > 0 && !table) || !lens || !weights || !new_table || !new_lens || !kept)
+    return FP8BQ_ERR_NULL;
+  if (!aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(weights, 4) ||
+      !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
+    return FP8BQ_ERR_ALIGN;
+  if (new_lens == lens) return FP8BQ_ERR_SHAPE;
+  DeviceInfo dev;
+  RETURN_IF(device_info(&dev));
+  Kv4EvictArgs a = {};
+  a.cache = static_cast<uint8_t *>(cache), a.weights = weights;
+  a.table = table, a.lens = lens, a.new_table = new_table, a.new_lens = new_lens, a.kept = kept;
+  a.pages = pages, a.width = width, a.new_width = new_width;
+  a.B = static_cast<int>(B), a.HK = static_cast<int>(HK), a.D = static_cast<int>(D);
+  a.page_log2 = page_log2(page), a.budget = static_cast<int>(budget);
+  a.recent = static_cast<int>(recent), a.max_len = static_cast<int>(width * page);
+  return finish_launch(0, launch_kv4_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ beside the linears

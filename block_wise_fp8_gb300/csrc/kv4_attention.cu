@@ -1,0 +1,709 @@
+// kv4_attention.cu -- attention of a few new tokens of every sequence over its
+// pages of the 4-bit cache (kv4.cuh has the layout).
+//
+// Per sequence, query token i, head h and its key/value head:
+//   s_j = scale * g_k * q . k_j,  p_j = exp(s_j - max s) / sum exp(s - max s),
+//   y = g_v * sum_j p_j v_j       over the cached tokens j that query i may see.
+// The query rows of one key/value head (G heads x Tq tokens) share every key and
+// value that is read, so they go through one pass over the pages: 9D/8 bytes a token
+// and head, which is what bounds the kernel where contexts are long.
+//
+// Products by mma.sync m16n8k16 in FP16, whose fragments the codes are unpacked into
+// from shared memory: the cache's rows are the wide side (16 tokens, or 16 of the D
+// values), the query rows the narrow one (8).  code * scale is exact in FP16.  A
+// query row is scaled by a power of two so that its largest value lies in [2^14,
+// 2^15); what FP16 then drops lies 2^-39 below that.  p is rounded to FP16 (half a
+// step: 2^-11 of a p, 2^-25 of the largest); sums, maxima and the statistics are FP32.
+//
+// The order of the D values is free in the first product and that of the tokens in
+// the second, so a lane takes D/4 neighbouring values of a key row, and D/8 of a
+// value row, each lane's from one or two groups, with wide loads free of conflicts.
+#include "kv4.cuh"
+
+namespace fp8bq {
+namespace {
+
+constexpr int kTile = 128;      // tokens a stage holds
+constexpr int kWarps = 4;       // consumer warps, 32 tokens of a tile each
+constexpr int kThreads = kWarps * 32 + 32;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int D>
+constexpr int kv4_stages() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+
+template <int D, int NB>
+struct Sizes {
+  static constexpr int kRows = 8 * NB;                  // query rows of an item
+  static constexpr int kStages = kv4_stages<D>();
+  static constexpr int kStageBytes = kTile * 9 * D / 8;
+  static constexpr int kPart = kRows * (D + 2);         // floats of a CTA's part of an item
+  static constexpr int kJoinBytes = kWarps * kPart * 4;
+  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + (kKv4MaxBatch + 2) * 4 + 256;
+  static constexpr int kCtas = NB == 1 && D <= 128 ? 3 : D == 256 && NB == 2 ? 1 : 2;  // an SM
+};
+
+// Where a CTA is in the flattened list of tiles: sequence, item of it, tile.
+struct Place {
+  int b, item, tile, tiles;  // tiles: of each of the sequence's items
+};
+
+struct Bars {
+  uint64_t full[4], empty[4];
+  uint32_t abort, never, ticket, pad;
+  uint32_t pages[4];  // which pages of a stage's tile are there
+};
+
+// The tiles of the batch: sequence b has len/128 (up) of them for each of its HK *
+// blocks items; first[b] counts those of one item before b.  Every CTA takes an
+// equal run of the whole list, so that ragged batches fill the device evenly.
+struct Plan {
+  const int *first;  // [B + 1]
+  int B, items;      // items a sequence: HK * blocks
+  __device__ int64_t total() const { return static_cast<int64_t>(first[B]) * items; }
+  // fewer CTAs than the grid has take part where there are fewer tiles
+  __device__ int64_t ctas() const { return min(max(total(), int64_t(1)), static_cast<int64_t>(gridDim.x)); }
+  __device__ int64_t start(int64_t cta) const { return total() * min(cta, ctas()) / ctas(); }
+  __device__ int cta_of(int64_t tile) const { return static_cast<int>(((tile + 1) * ctas() - 1) / total()); }
+  __device__ Place at(int64_t f) const {
+    int lo = 0, hi = B;  // the last b with first[b] * items <= f that has tiles
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (static_cast<int64_t>(first[mid]) * items <= f) lo = mid; else hi = mid;
+    }
+    Place p;
+    p.b = lo;
+    p.tiles = first[lo + 1] - first[lo];
+    const int64_t in = f - static_cast<int64_t>(first[lo]) * items;
+    p.item = static_cast<int>(in / p.tiles);
+    p.tile = static_cast<int>(in - static_cast<int64_t>(p.item) * p.tiles);
+    return p;
+  }
+  __device__ void next(Place &p) const {
+    if (++p.tile < p.tiles) return;
+    p.tile = 0;
+    if (++p.item < items) return;
+    p.item = 0;
+    do {
+      ++p.b;
+    } while (p.b < B && first[p.b + 1] == first[p.b]);
+    if (p.b < B) p.tiles = first[p.b + 1] - first[p.b];
+  }
+};
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_kernel(const Kv4AttnArgs a) {
+  using S = Sizes<D, NB>;
+  constexpr int kRows = S::kRows, kStages = S::kStages;
+  constexpr int kKeyWords = D / 32;       // 32-bit words of codes a lane takes of a key row
+  constexpr int kTiles = D / 16;          // products of 16 values of the D
+  constexpr int kValueWords = D / 64;     // words of codes a lane takes of a value row
+  extern __shared__ __align__(128) uint8_t smem[];
+  float *join = reinterpret_cast<float *>(smem + kStages * S::kStageBytes);
+  int *first = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(join) + S::kJoinBytes);
+  __shared__ Bars bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile uint32_t *abort = &bars.abort;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], kWarps);
+    bars.abort = bars.never = 0;
+    fence_mbar_init();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+  const int P = 1 << a.page_log2;
+  const int R = a.G * a.Tq, blocks = (R + kRows - 1) / kRows;
+  const Kv4Page pg = kv4_page(P, D);
+  auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), a.max_len); };
+  for (int b = tid; b < a.B; b += kThreads) first[b + 1] = (length(b) + kTile - 1) / kTile;
+  if (tid == 0) first[0] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int v = b0 + lane < a.B ? first[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += u;
+      }
+      v += run;
+      if (b0 + lane < a.B) first[b0 + lane + 1] = v;
+      run = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+  }
+  __syncthreads();
+  const Plan plan = {first, a.B, a.HK * blocks};
+  const int64_t f0 = plan.start(blockIdx.x), f1 = plan.start(static_cast<int64_t>(blockIdx.x) + 1);
+
+  if (warp == kWarps) {
+    // ---- copies: a tile's pages, each one run of bytes, into the stage
+    Place p = f0 < f1 ? plan.at(f0) : Place{};
+    const int per_tile = kTile >> a.page_log2;
+    auto look_up = [&]() -> int {  // this lane's page of tile p, -1 where there is none
+      const int at = (p.tile << (7 - a.page_log2)) + lane;
+      if (lane >= per_tile || (at << a.page_log2) >= length(p.b)) return -1;
+      const int page = __ldg(a.table + static_cast<int64_t>(p.b) * a.width + at);
+      return page < a.pages ? page : -1;
+    };
+    int page = f0 < f1 ? look_up() : -1;
+    int st = 0, ph = 1;
+    int64_t f = f0;
+    for (; f < f1; ++f) {
+      const int head = p.item / blocks;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars.empty[st], ph, abort, a.wait_limit_ns))) break;
+      const bool on = page >= 0;
+      const uint32_t there = __ballot_sync(0xFFFFFFFFu, on);
+      if (lane == 0) {
+        bars.pages[st] = there;
+        mbar_arrive_expect_tx(&bars.full[st], __popc(there) * pg.bytes);
+      }
+      __syncwarp();
+      if (on && !(a.fault && blockIdx.x == 0 && f == f0))
+        bulk_load_1d(smem + st * S::kStageBytes + lane * pg.bytes,
+                     a.cache + (static_cast<int64_t>(page) * a.HK + head) * pg.bytes, pg.bytes,
+                     &bars.full[st]);
+      if (++st == kStages) st = 0, ph ^= 1;
+      if (f + 1 < f1) {
+        plan.next(p);
+        page = look_up();
+      }
+    }
+    if (*abort) {  // copies in flight land before the memory is given up
+      for (int64_t k = f - kStages < f0 ? f0 : f - kStages; k < f; ++k)
+        mbar_wait(&bars.full[(k - f0) % kStages], (k - f0) / kStages & 1, &bars.never, a.wait_limit_ns);
+    }
+  } else {
+    const int g = lane >> 2, t = lane & 3;
+    // tokens of a block of 16 as the products' rows take them
+    const int key_row = (g >> 1) + (g & 1) * 4;
+    uint32_t qf[kTiles][NB][2];   // the query rows, a value pair a register
+    float qs[NB][2];              // log2 units a product, of this lane's two columns
+    float mx[NB][2], sum[NB][2];
+    float o[kTiles][NB][4];
+    int ends[NB][2];              // tokens that the column's query may see
+    int st = 0, ph = 0;
+    Place p = f0 < f1 ? plan.at(f0) : Place{};
+    int len = 0, row0 = 0, head = 0;
+    for (int64_t f = f0; f < f1; ++f) {
+      if (f == f0 || p.tile == 0) {
+        // ---- a new item: its query rows
+        len = length(p.b);
+        head = p.item / blocks;
+        row0 = (p.item - head * blocks) * kRows;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int row = row0 + nb * 8 + g;
+          uint4 raw[D / 32];
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+          if (row < R) {
+            const int i = row / a.G;
+            const uint16_t *q = a.q + (static_cast<int64_t>(p.b) * a.Tq + i) * a.q_ts +
+                                static_cast<int64_t>(head * a.G + row - i * a.G) * a.q_hs + t * (D / 4);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) raw[k] = __ldg(reinterpret_cast<const uint4 *>(q) + k);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
+                                         __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu)));
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          // the row's power of two: its largest value to [2^14, 2^15)
+          const int e = top >> 7;
+          const int up = e == 255 ? 0 : 14 + 127 - max(e, 24);
+          const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale_log2;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            qs[nb][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + c) * 4);
+            const int r = row0 + nb * 8 + 2 * t + c;
+            ends[nb][c] = r < R ? len - (a.Tq - 1 - r / a.G) : len;
+            mx[nb][c] = -INFINITY, sum[nb][c] = 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              qf[i * 2 + j / 2][nb][j & 1] = pack_f16(__uint_as_float(w[j] << 16) * by,
+                                                      __uint_as_float(w[j] & 0xFFFF0000u) * by);
+          }
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[j][nb][c] = 0.0f;
+        }
+      }
+      // (after a wait that gave up the walk goes on, over whatever the memory holds,
+      // so that no warp leaves the others at a barrier)
+      mbar_wait(&bars.full[st], ph, abort, a.wait_limit_ns);
+      const uint8_t *stage = smem + st * S::kStageBytes;
+      const int tok0 = p.tile * kTile + warp * 32;
+      const uint32_t there = __shfl_sync(0xFFFFFFFFu, bars.pages[st], 0);
+      const int per_tile = kTile >> a.page_log2;
+      // every token of the warp's 32 seen by every row, and its pages there
+      const int seen_by_all = len - (a.Tq - 1);
+      const bool whole = tok0 + 32 <= seen_by_all && there == (1u << per_tile) - 1u;
+      auto block_of = [&](int mb, int &in) {  // page of the warp's 16-token block, place in it
+        const int at = warp * 32 + mb * 16;
+        in = at & (P - 1);
+        return stage + (at >> a.page_log2) * pg.bytes;
+      };
+      if (whole || tok0 < len) {
+        float s[2][NB][4];
+        // ---- scores of 2 x 16 tokens
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+          int in;
+          const uint8_t *page = block_of(mb, in);
+          uint32_t w[2][kKeyWords];
+          uint32_t sc[2][D / 64];  // a group's scale in both halves
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = in + key_row + r * 8;
+            const uint8_t *codes = page + row * (D / 2) + t * (D / 8);
+            if constexpr (D == 64) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(codes);
+              w[r][0] = v.x, w[r][1] = v.y;
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 128; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(codes)[i];
+                w[r][i * 4] = v.x, w[r][i * 4 + 1] = v.y, w[r][i * 4 + 2] = v.z, w[r][i * 4 + 3] = v.w;
+              }
+            }
+            const uint8_t *scales = page + pg.k_scales + row * (D / 16) + t * (D / 64);
+            if constexpr (D == 64) {
+              sc[r][0] = both_low(e4m3x2_to_f16(*scales));
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 128; ++i) {
+                const uint32_t two = e4m3x2_to_f16(reinterpret_cast<const uint16_t *>(scales)[i]);
+                sc[r][2 * i] = both_low(two), sc[r][2 * i + 1] = both_high(two);
+              }
+            }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[mb][nb][c] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kKeyWords; ++i) {
+            uint32_t lo[4], hi[4];
+            e2m1x8_to_f16(w[0][i], lo);
+            e2m1x8_to_f16(w[1][i], hi);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t f[4] = {hmul2(lo[2 * k], sc[0][i / 2]), hmul2(hi[2 * k], sc[1][i / 2]),
+                                     hmul2(lo[2 * k + 1], sc[0][i / 2]), hmul2(hi[2 * k + 1], sc[1][i / 2])};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_f16(s[mb][nb], f, qf[2 * i + k][nb][0], qf[2 * i + k][nb][1]);
+            }
+          }
+        }
+        // ---- log2 units; what a row may not see goes to -inf
+        if (whole) {
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) s[mb][nb][c] *= qs[nb][c & 1];
+        } else {
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb) {
+            const bool here = there >> ((warp * 32 + mb * 16) >> a.page_log2) & 1u;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int tok = tok0 + mb * 16 + key_row + (c >> 1) * 8;
+                s[mb][nb][c] = here && tok < ends[nb][c & 1] ? s[mb][nb][c] * qs[nb][c & 1] : -INFINITY;
+              }
+          }
+        }
+        if (a.logits) {
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int r = row0 + nb * 8 + 2 * t + (c & 1);
+                const int tok = tok0 + mb * 16 + key_row + (c >> 1) * 8;
+                if (r < R && tok < a.max_len)
+                  a.logits[((static_cast<int64_t>(p.b) * a.HK + head) * R + r) * a.max_len + tok] = s[mb][nb][c];
+              }
+        }
+        // ---- the running maximum; what was summed before follows it
+        bool grew = false;
+        float fix[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = fmaxf(fmaxf(s[0][nb][c], s[0][nb][c + 2]), fmaxf(s[1][nb][c], s[1][nb][c + 2]));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            m = fmaxf(m, mx[nb][c]);
+            fix[nb][c] = m > mx[nb][c] ? ex2(mx[nb][c] - m) : 1.0f;
+            grew |= m > mx[nb][c];
+            mx[nb][c] = m;
+          }
+        if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            sum[nb][0] *= fix[nb][0], sum[nb][1] *= fix[nb][1];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[j][nb][c] *= fix[nb][c & 1];
+          }
+        }
+        // ---- p, and its fragments for the second product: rows become columns
+        uint32_t pf[2][NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float m0 = mx[nb][0] == -INFINITY ? 0.0f : mx[nb][0];
+          const float m1 = mx[nb][1] == -INFINITY ? 0.0f : mx[nb][1];
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb) {
+            const float p0 = ex2(s[mb][nb][0] - m0), p1 = ex2(s[mb][nb][1] - m1);
+            const float p2 = ex2(s[mb][nb][2] - m0), p3 = ex2(s[mb][nb][3] - m1);
+            sum[nb][0] += p0 + p2, sum[nb][1] += p1 + p3;
+            pf[mb][nb][0] = transpose8x8(pack_f16(p0, p1));
+            pf[mb][nb][1] = transpose8x8(pack_f16(p2, p3));
+          }
+        }
+        // ---- p times the values
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+          int in;
+          const uint8_t *page = block_of(mb, in);
+          uint32_t w[4][kValueWords];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the products' order
+          uint32_t sb[4];              // their scale bytes (two groups for D == 256)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = in + t + r * 4;
+            const uint8_t *codes = page + pg.v_codes + row * (D / 2) + g * (D / 16);
+            if constexpr (D == 64) {
+              w[r][0] = *reinterpret_cast<const uint32_t *>(codes);
+            } else if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(codes);
+              w[r][0] = v.x, w[r][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4 *>(codes);
+              w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+            }
+            const uint8_t *scales = page + pg.v_scales + row * (D / 16);
+            if constexpr (D == 256) sb[r] = *reinterpret_cast<const uint16_t *>(scales + 2 * g);
+            else sb[r] = scales[D == 128 ? g : g >> 1];
+          }
+          if (!whole) {
+            // values of tokens that no row may see count as 0 whatever their bytes
+            // hold; a NaN that some rows see goes to those rows alone
+            const bool here = there >> ((warp * 32 + mb * 16) >> a.page_log2) & 1u;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int tok = tok0 + mb * 16 + t + r * 4;
+              if (!here || tok >= len) sb[r] = 0;
+              constexpr int kGroups = D == 256 ? 2 : 1;  // groups of this lane's values
+#pragma unroll
+              for (int k = 0; k < kGroups; ++k) {
+                const uint32_t one = sb[r] >> (8 * k) & 0xFFu;
+                const bool bad = (one & 0x7Fu) == kE4m3Nan && tok >= seen_by_all;
+                if (bad) sb[r] &= ~(0xFFu << (8 * k));
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, bad);
+                if (who == 0) continue;
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {  // the lanes of the same values, other tokens
+                  if (!(who >> (g * 4 + tt) & 1u)) continue;
+                  const int other = tok0 + mb * 16 + tt + r * 4;
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                      if (other < ends[nb][c])
+#pragma unroll
+                        for (int j = k * (kTiles / kGroups); j < (k + 1) * (kTiles / kGroups); ++j)
+                          o[j][nb][c] = o[j][nb][c + 2] = NAN;
+                }
+              }
+            }
+          }
+          constexpr int kScales = D == 256 ? 2 : 1;
+          uint32_t sv[2][kScales];  // scales of tokens 2t, 2t+1 | 2t+8, 2t+9
+#pragma unroll
+          for (int k = 0; k < kScales; ++k) {
+            sv[0][k] = e4m3x2_to_f16((sb[0] >> (8 * k) & 0xFFu) | (sb[1] >> (8 * k) & 0xFFu) << 8);
+            sv[1][k] = e4m3x2_to_f16((sb[2] >> (8 * k) & 0xFFu) | (sb[3] >> (8 * k) & 0xFFu) << 8);
+          }
+#pragma unroll
+          for (int i = 0; i < kValueWords; ++i) {
+            // the codes of two tokens side by side: even values, odd values
+            uint32_t ev[2][4], od[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t x = w[2 * k][i], y = w[2 * k + 1][i];
+              e2m1x8_to_f16((x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), ev[k]);
+              e2m1x8_to_f16((x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[k]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int group = D == 256 ? i / 2 : 0;
+              const uint32_t f[4] = {hmul2(ev[0][j], sv[0][group]), hmul2(od[0][j], sv[0][group]),
+                                     hmul2(ev[1][j], sv[1][group]), hmul2(od[1][j], sv[1][group])};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_f16(o[i * 4 + j][nb], f, pf[mb][nb][0], pf[mb][nb][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.empty[st]);
+      if (++st == kStages) st = 0, ph ^= 1;
+
+      // ---- the item's end, or the run's: the warps' sums together
+      const bool ends_here = p.tile + 1 == p.tiles;
+      if (ends_here || f + 1 == f1) {
+        const bool begun_here = f - p.tile >= f0;
+        const bool alone = begun_here && ends_here;  // no other CTA has a part of it
+        float *mine = join + warp * S::kPart;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float l = sum[nb][c];
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+            const int row = nb * 8 + 2 * t + c;
+            if (g == 0) mine[kRows * D + row * 2] = mx[nb][c], mine[kRows * D + row * 2 + 1] = l;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+              *reinterpret_cast<float2 *>(mine + row * D + g * (D / 8) + 2 * j) =
+                  make_float2(o[j][nb][c], o[j][nb][c + 2]);
+          }
+        named_bar_sync(1, kWarps * 32);
+        const int64_t item = static_cast<int64_t>(p.b) * plan.items + p.item;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (begun_here ? 1 : 0);
+        // a thread has 4 neighbouring values of a row
+        auto finish = [&](float4 v, int row, int d, float m, float l) {
+          const int r = row0 + row;
+          if (r >= R) return;
+          const int i = r / a.G;
+          const float by = l == 0.0f ? 0.0f : a.v_scale / l;
+          uint16_t *y = a.y + (static_cast<int64_t>(p.b) * a.Tq + i) * a.y_ts +
+                        static_cast<int64_t>(head * a.G + r - i * a.G) * a.y_hs + d;
+          uint2 out;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.x) : "f"(v.y * by), "f"(v.x * by));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.y) : "f"(v.w * by), "f"(v.z * by));
+          *reinterpret_cast<uint2 *>(y) = out;
+          if (a.stats && d == 0)
+            *reinterpret_cast<float2 *>(a.stats + ((static_cast<int64_t>(p.b) * a.HK + head) * R + r) * 2) =
+                make_float2(m, l);
+        };
+        for (int e = tid; e < kRows * D / 4; e += kWarps * 32) {
+          const int row = e / (D / 4), d = e % (D / 4) * 4;
+          float m = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join[w * S::kPart + kRows * D + row * 2]);
+          float4 v = make_float4(0, 0, 0, 0);
+          float l = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            // (a part with nothing seen holds zeros, or the NaN that a row was given)
+            const float mw = join[w * S::kPart + kRows * D + row * 2];
+            const float by = mw == -INFINITY ? (m == -INFINITY ? 1.0f : 0.0f) : ex2(mw - m);
+            const float4 x = *reinterpret_cast<const float4 *>(join + w * S::kPart + row * D + d);
+            v.x += x.x * by, v.y += x.y * by, v.z += x.z * by, v.w += x.w * by;
+            l += join[w * S::kPart + kRows * D + row * 2 + 1] * by;
+          }
+          if (alone) {
+            finish(v, row, d, m, l);
+          } else {
+            float *to = a.part + slot * S::kPart;
+            *reinterpret_cast<float4 *>(to + row * D + d) = v;
+            if (d == 0) to[kRows * D + row * 2] = m, to[kRows * D + row * 2 + 1] = l;
+          }
+        }
+        if (!alone) {
+          // the last CTA to leave its part sums all of them, in the order of the tokens
+          const int64_t s0 = static_cast<int64_t>(first[p.b]) * plan.items + static_cast<int64_t>(p.item) * p.tiles;
+          const int c0 = plan.cta_of(s0), c1 = plan.cta_of(s0 + p.tiles - 1);
+          __threadfence();
+          named_bar_sync(1, kWarps * 32);
+          if (tid == 0) {
+            const uint32_t seen = atom_add_acq_rel_gpu(a.tickets + item, 1u);
+            bars.ticket = seen;
+            if (seen == static_cast<uint32_t>(c1 - c0)) a.tickets[item] = 0u;
+          }
+          named_bar_sync(1, kWarps * 32);
+          if (bars.ticket == static_cast<uint32_t>(c1 - c0)) {
+            __threadfence();
+            // the item begins in the second slot of its first CTA, and goes on in the
+            // first one of each of the others
+            auto at = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * S::kPart; };
+            for (int e = tid; e < kRows * D / 4; e += kWarps * 32) {
+              const int row = e / (D / 4), d = e % (D / 4) * 4;
+              float m = -INFINITY;
+              for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(at(c) + kRows * D + row * 2));
+              float4 v = make_float4(0, 0, 0, 0);
+              float l = 0.0f;
+              for (int c = c0; c <= c1; ++c) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(at(c) + kRows * D + row * 2));
+                const float by = ml.x == -INFINITY ? (m == -INFINITY ? 1.0f : 0.0f) : ex2(ml.x - m);
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(at(c) + row * D + d));
+                v.x += x.x * by, v.y += x.y * by, v.z += x.z * by, v.w += x.w * by;
+                l += ml.y * by;
+              }
+              finish(v, row, d, m, l);
+            }
+          }
+        }
+        named_bar_sync(1, kWarps * 32);  // before the shared sums are written again
+      }
+      if (f + 1 < f1) plan.next(p);
+    }
+    // ---- sequences without a cached token: zeros
+    const int64_t rows = static_cast<int64_t>(a.Tq) * a.HK * a.G;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      if (first[b + 1] != first[b]) continue;
+      for (int64_t e = tid; e < rows * (D / 4); e += kWarps * 32) {
+        const int64_t row = e / (D / 4), i = row / (a.HK * a.G), h = row - i * (a.HK * a.G);
+        *reinterpret_cast<uint2 *>(a.y + (static_cast<int64_t>(b) * a.Tq + i) * a.y_ts + h * a.y_hs +
+                                   e % (D / 4) * 4) = make_uint2(0, 0);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *abort) atomicMax(a.status, kStatusTimeout);
+}
+
+// ---------------------------------------------------------------- the weights
+
+// weights[page][head][place] += sum over the query rows of exp2(s - max) / sum, from
+// the scores that the attention left: a thread has one cached token.  A thread is
+// the only one to add to its place, unless sequences share a page.
+constexpr int kWeightThreads = 256;
+__global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4AttnArgs a) {
+  __shared__ float2 stat[kKv4MaxRows];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int R = a.G * a.Tq, h = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
+  const int len = min(max(__ldg(a.lens + b), 0), a.max_len);
+  if (blockIdx.x * kWeightThreads >= len) return;
+  const int64_t bh = static_cast<int64_t>(b) * a.HK + h;
+  for (int r = threadIdx.x; r < R; r += kWeightThreads) {
+    const float2 ml = *reinterpret_cast<const float2 *>(a.stats + (bh * R + r) * 2);
+    // a row that sees nothing adds nothing
+    stat[r] = make_float2(ml.x, ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
+  }
+  __syncthreads();
+  const int tok = blockIdx.x * kWeightThreads + threadIdx.x;
+  if (tok >= len) return;
+  const int page = __ldg(a.table + static_cast<int64_t>(b) * a.width + (tok >> a.page_log2));
+  if (page < 0 || page >= a.pages) return;
+  const float *s = a.logits + bh * R * a.max_len + tok;
+  float w = 0.0f;
+  for (int r = 0; r < R; ++r) {
+    const float v = s[static_cast<int64_t>(r) * a.max_len];
+    if (v != -INFINITY) w += ex2(v - stat[r].x) * stat[r].y;
+  }
+  atomicAdd(a.weights + ((static_cast<int64_t>(page) * a.HK + h) << a.page_log2) + (tok & ((1 << a.page_log2) - 1)), w);
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int kMaxCtas = 3 * 160;  // more than three on each of a GB300's SMs
+
+struct Layout {
+  size_t tickets, part, stats, logits, total;
+};
+Layout layout(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t max_len, bool weights) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  Layout l;
+  // the tickets' place and size are the same for all sizes, so that one workspace
+  // serves calls of several
+  l.tickets = 256;
+  l.part = l.tickets + kKv4MaxItems * 4;
+  l.stats = l.part + up(static_cast<size_t>(2) * kMaxCtas * 16 * (D + 2) * 4);
+  const size_t rows = static_cast<size_t>(B) * HQ * Tq;
+  l.logits = l.stats + (weights ? up(rows * 8) : 0);
+  l.total = l.logits + (weights ? up(rows * static_cast<size_t>(max_len) * 4) : 0);
+  return l;
+}
+
+}  // namespace
+
+size_t kv4_workspace(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t max_len,
+                     bool weights) {
+  return layout(B, Tq, HQ, HK, D, max_len, weights).total;
+}
+
+cudaError_t launch_kv4_attention(Kv4AttnArgs a, void *ws, int num_sms, cudaStream_t st) {
+  const Layout l = layout(a.B, a.Tq, static_cast<int64_t>(a.HK) * a.G, a.HK, a.D, a.max_len, a.weights != nullptr);
+  uint8_t *at = static_cast<uint8_t *>(ws);
+  a.status = static_cast<uint32_t *>(ws);
+  a.tickets = reinterpret_cast<uint32_t *>(at + l.tickets);
+  a.part = reinterpret_cast<float *>(at + l.part);
+  if (a.weights) {
+    a.stats = reinterpret_cast<float *>(at + l.stats);
+    a.logits = reinterpret_cast<float *>(at + l.logits);
+  }
+  const int R = a.G * a.Tq;
+  auto run = [&](auto d, auto n) {
+    constexpr int D = decltype(d)::value, NB = decltype(n)::value;
+    using S = Sizes<D, NB>;
+    cudaError_t e = allow_smem<kv4_attention_kernel<D, NB>>(S::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>(a.B) * a.HK * ((R + S::kRows - 1) / S::kRows) *
+                          ((a.max_len + kTile - 1) / kTile);
+    const int64_t most = static_cast<int64_t>(num_sms) * S::kCtas;
+    const int64_t grid = tiles < most ? (tiles < 1 ? 1 : tiles) : most;
+    return launch_pdl(kv4_attention_kernel<D, NB>,
+                      dim3(static_cast<unsigned>(grid < kMaxCtas ? grid : kMaxCtas)), dim3(kThreads),
+                      S::kSmem, st, a);
+  };
+  auto by_rows = [&](auto d) {
+    return R <= 8 ? run(d, std::integral_constant<int, 1>{}) : run(d, std::integral_constant<int, 2>{});
+  };
+  cudaError_t e = a.D == 64    ? by_rows(std::integral_constant<int, 64>{})
+                  : a.D == 128 ? by_rows(std::integral_constant<int, 128>{})
+                               : by_rows(std::integral_constant<int, 256>{});
+  if (e != cudaSuccess || !a.weights || a.max_len == 0) return e;
+  return launch_pdl(kv4_weights_kernel,
+                    dim3((a.max_len + kWeightThreads - 1) / kWeightThreads, a.B * a.HK),
+                    dim3(kWeightThreads), 0, st, a);
+}
+
+}  // namespace fp8bq

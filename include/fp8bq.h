@@ -24,8 +24,9 @@
  *   and the grouped (MoE) block GEMM over experts' weights [E, N, K]
  *   ("SGLang 源码完全拆解(十九)", §MoE:专家权重多一个维度).  Beside the linear
  *   stand a whole mixture-of-experts layer for a few tokens, low-rank adapters
- *   of many requests, and the norm of query and key heads with the rotary
- *   embedding.
+ *   of many requests, the norm of query and key heads with the rotary
+ *   embedding, and the attention between them and the output projection: over
+ *   whole prompts, and over a paged cache of keys and values in 4 bits.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -65,8 +66,8 @@
  *    the environment, read once.  After a timeout the outputs are undefined
  *    and the workspace must be zeroed again (fp8bq_workspace_init).  For
  *    tests, FP8BQ_FAULT_INJECT=skip_first_load:<n> (read once) makes the next
- *    n GEMM launches (and MoE layers, and adapter calls in their form for many
- *    tokens) skip one tile copy so that their waits run out.
+ *    n GEMM launches (and MoE layers, adapter calls in their form for many
+ *    tokens, and attention calls) skip one tile copy so that their waits run out.
  *  - No C++ exception crosses this interface.
  */
 #ifndef FP8BQ_H
@@ -111,7 +112,8 @@ enum {
   FP8BQ_OP_UE8M0_GEMM = 8,
   FP8BQ_OP_UE8M0_LINEAR = 9,
   FP8BQ_OP_GROUPED_GEMM = 10, /* both grouped forms; M = rows of A and Y in all */
-  FP8BQ_OP_LORA_ADD = 11      /* fp8bq_lora_add; N = the adapters' rank R */
+  FP8BQ_OP_LORA_ADD = 11,     /* fp8bq_lora_add; N = the adapters' rank R */
+  FP8BQ_OP_PROMPT_ATTENTION = 12 /* fp8bq_prompt_attention, any sizes */
 };
 
 /* ---------------------------------------------------------------- utility
@@ -552,6 +554,117 @@ FP8BQ_API int fp8bq_moe_experts(const void *x, int64_t ldx, const int32_t *ids,
 /* Workspace bytes of both forms (256 for sizes that they refuse). */
 FP8BQ_API size_t fp8bq_moe_workspace_bytes(int64_t M, int64_t E, int64_t H, int64_t I,
                                            int64_t topk);
+
+/* ------------------------------------------------ attention and its cache
+ * Between the query/key norm and the output projection.  Heads: query head h
+ * belongs to key/value head h / (HQ / HK); HQ is a multiple of HK.  All tensors
+ * of heads are BF16, value d of head h of token t at [t * ts + h * hs + d], with
+ * pointers 16-byte aligned and strides multiples of 8 (ERR_ALIGN).  scale (the
+ * softmax's, 1/sqrt(D) as a rule), k_scale and v_scale are positive and finite
+ * (ERR_SHAPE). */
+
+/* Causal attention over whole prompts, S sequences packed one after the other:
+ * rows offsets[s] .. offsets[s+1]-1 belong to sequence s, and for its token i
+ *   y_i = sum_{j <= i} softmax_j(scale * q_i . k_j) v_j
+ * with FP32 scores, maximum, sum and products' sums; the weights enter the second
+ * product as BF16 (half a step: 2^-8 of a weight, as far as y's own rounding).
+ * Keys and values that a token does not see have no part in its row, whatever they
+ * hold (infinities and NaN among them).
+ * q: [T, HQ, D]; k, v: [T, HK, D]; y: [T, HQ, D], which may be q itself (same pointer
+ * and strides); no other overlap, and none among y's own heads (ERR_SHAPE).  Strides
+ * of the inputs at least 1 (ERR_SHAPE; one of a single token or head does not
+ * matter).  offsets: DEVICE int32 [S+1], non-decreasing; bounds outside [0, T] are
+ * clamped, rows outside every sequence are not written, and sequences that overlap
+ * (decreasing offsets) leave their rows unspecified.
+ * 16 <= D <= 128 and HQ / HK <= 128 (ERR_UNSUPPORTED), D % 16 == 0 (ERR_ALIGN),
+ * T <= 2^19, S <= 1024, HQ <= 1024 (ERR_SHAPE).  Workspace:
+ * fp8bq_workspace_bytes(FP8BQ_OP_PROMPT_ATTENTION, ...), for the status word.
+ * One launch. */
+FP8BQ_API int fp8bq_prompt_attention(const void *q, int64_t q_ts, int64_t q_hs, const void *k,
+                                     int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                                     int64_t v_hs, const int32_t *offsets, int64_t S, float scale,
+                                     void *y, int64_t y_ts, int64_t y_hs, int64_t T, int64_t HQ,
+                                     int64_t HK, int64_t D, void *ws, size_t ws_bytes,
+                                     void *stream);
+
+/* The 4-bit paged cache: uint8 [pages][HK][page * 9 * D / 8], 16-byte aligned, D
+ * = 64, 128 or 256, page (tokens a page) = 16, 32, 64 or 128 (ERR_UNSUPPORTED).  A
+ * page of a head holds, one after the other, its tokens' key codes [page][D/2], key
+ * scales [page][D/16], value codes [page][D/2] and value scales [page][D/16].  A code
+ * is E2M1 (values 0 0.5 1 1.5 2 3 4 6 and their negatives), value 2i of a row in the
+ * low half of its byte i; a scale is E4M3, one for 16 values; a value is code * scale
+ * * k_scale (v_scale for values).
+ * A slot is page index * page + place.  A block table int32 [B, width] names the
+ * pages of each sequence in order; lens int32 [B] its cached tokens, clamped to
+ * [0, width * page].  A page index outside [0, pages) means that its tokens are not
+ * there: nothing is read or written for them, and no query sees them.
+ * `weights`, where given, is FP32 [pages][HK][page]: the softmax weight that each
+ * cached token has received so far. */
+
+/* Writes token t's key and value rows into slot slots[t] (DEVICE int32 or int64 [T],
+ * slot_bits 32 or 64; a slot outside [0, pages * page) is left out, which is how a
+ * padded batch marks its padding).  Per group of 16 values, x' = x * RN(1 / k_scale):
+ *   s = max(E4M3(min(max|x'| / 6, 448)), 2^-9), code = E2M1(x' / s)
+ * with a binary32 division for the scale, nearest even, and the code of the exact
+ * quotient, ties to the even code, beyond 6 to 6 (infinities too); a NaN makes the
+ * group's scale NaN.  weights (may be NULL): zeroed for the slots written.  Two rows
+ * for one slot leave it unspecified. */
+FP8BQ_API int fp8bq_kv4_append(const void *k, int64_t k_ts, int64_t k_hs, const void *v,
+                               int64_t v_ts, int64_t v_hs, const void *slots, int slot_bits,
+                               void *cache, int64_t pages, int64_t page, float *weights,
+                               float k_scale, float v_scale, int64_t T, int64_t HK, int64_t D,
+                               void *stream);
+
+/* Reads slots back into rows [T, HK, D] (what a prompt behind a cached prefix starts
+ * with), exact up to one BF16 rounding of the product with k_scale or v_scale (none
+ * for powers of two); rows of slots outside the cache are left as they are. */
+FP8BQ_API int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, const void *slots,
+                             int slot_bits, float k_scale, float v_scale, void *k, int64_t k_ts,
+                             int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, int64_t T,
+                             int64_t HK, int64_t D, void *stream);
+
+/* Attention of Tq new tokens of each of B sequences over their cached tokens, the new
+ * ones among them (append them first): query i of sequence b, row b * Tq + i of q and
+ * y ([B * Tq, HQ, D]), sees the first lens[b] - (Tq - 1 - i) tokens,
+ *   y = sum_j softmax_j(scale * q . k_j) v_j;
+ * a query that sees none gets zeros.  FP32 scores, maxima and sums; the weights enter
+ * the second product in FP16 (half a step: 2^-11 of a weight, 2^-25 of the row's
+ * largest).  What the cache holds behind a sequence's end, or in pages that are not
+ * there, has no part in y, whatever it is.
+ * weights (may be NULL): each seen token's entry of its page and head grows by the sum
+ * of its softmax weights over the head's HQ / HK * Tq query rows (where sequences
+ * share a page, in no fixed order; everything else is the same from call to call).
+ * HQ / HK * Tq <= 128 (ERR_UNSUPPORTED); B <= 1024, B * HK <= 65535,
+ * B * HK * ceil(HQ / HK * Tq / 8) <= 65536, width * page <= 2^28 (ERR_SHAPE).
+ * Workspace: fp8bq_kv4_workspace_bytes(B, Tq, HQ, HK, D, width * page, weights !=
+ * NULL), zeroed once; one that is large enough serves calls of any sizes, of this
+ * function alone.  One launch, two with weights. */
+FP8BQ_API int fp8bq_kv4_attention(const void *q, int64_t q_ts, int64_t q_hs, const void *cache,
+                                  int64_t pages, int64_t page, const int32_t *table, int64_t width,
+                                  const int32_t *lens, float scale, float k_scale, float v_scale,
+                                  float *weights, void *y, int64_t y_ts, int64_t y_hs, int64_t B,
+                                  int64_t Tq, int64_t HQ, int64_t HK, int64_t D, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* Workspace bytes of fp8bq_kv4_attention (256 for sizes that it refuses). */
+FP8BQ_API size_t fp8bq_kv4_workspace_bytes(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D,
+                                           int64_t max_len, int weights);
+
+/* Keeps `budget` of each sequence's cached tokens, for every key/value head its own:
+ * the last `recent` ones, and of those before them the budget - recent with the largest
+ * weights (ties to the earlier token; NaN below everything).  They are copied, codes,
+ * scales and weights, in their order to the pages that new_table int32 [B, new_width]
+ * names, which must not be pages that a sequence of the call still reads.  A sequence of
+ * no more than `budget` tokens is copied whole.  new_lens: int32 [B] = min(len, budget)
+ * (not lens itself: ERR_SHAPE); kept: int32 [B, HK, budget], the tokens' places before,
+ * ascending, then -1.  A token whose old or new page is not there is not copied.
+ * 0 <= recent <= budget, budget >= 1, new_width * page >= budget, B <= 1024
+ * (ERR_SHAPE).  Two launches. */
+FP8BQ_API int fp8bq_kv4_evict(void *cache, int64_t pages, int64_t page, const int32_t *table,
+                              int64_t width, const int32_t *lens, float *weights,
+                              const int32_t *new_table, int64_t new_width, int32_t *new_lens,
+                              int32_t *kept, int64_t budget, int64_t recent, int64_t B, int64_t HK,
+                              int64_t D, void *stream);
 
 /* ------------------------------------------------ weight / calibration set-up */
 
