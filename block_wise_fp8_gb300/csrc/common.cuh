@@ -360,6 +360,11 @@ struct LaunchShape {
   int tail_kps;
 };
 
+// BF16 heads [T, H, D] (strides ts and hs elements, multiples of 8) with a box of
+// 64 values x box_heads x box_tokens and 128-byte swizzling; values from D on and
+// heads and tokens outside read as zeros.
+bool make_heads_map(CUtensorMap *m, const void *base, int64_t T, int64_t H, int64_t D, int64_t ts,
+                    int64_t hs, int box_tokens, int box_heads);
 // K-major E4M3 matrix [rows, K] (pitch K bytes) as a TMA map with a
 // [box_rows x 128 B] box and 128-byte swizzling.
 bool make_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows);

@@ -74,6 +74,22 @@ bool make_bf16_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_heads_map(CUtensorMap *m, const void *base, int64_t T, int64_t H, int64_t D, int64_t ts,
+                    int64_t hs, int box_tokens, int box_heads) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                        static_cast<cuuint64_t>(T)};
+  // a single head's or token's stride is never used
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(H > 1 ? hs : D) * 2,
+                           static_cast<cuuint64_t>(T > 1 ? ts : D) * 2};
+  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Small cache of encoded tensor maps keyed by (base, rows, K, box rows): repeated
 // calls on the same tensors (every forward of a layer) skip the host-side encode.
 bool cached_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K,

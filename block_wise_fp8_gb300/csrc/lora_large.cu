@@ -28,21 +28,6 @@
 namespace fp8bq {
 namespace {
 
-// Instruction descriptor, kind::f16: D = F32 (bits 4-5 = 1), A and B BF16 (bits
-// 7-9, 10-12 = 1), both K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
-__device__ __forceinline__ uint32_t idesc_bf16(uint32_t M, uint32_t N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // 16 bytes global -> shared, of which the first `bytes` (0 .. 16) are read and
 // the rest are zeros.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, uint32_t bytes) {

@@ -3,67 +3,482 @@
 //
 // Per sequence (rows offsets[s] .. offsets[s+1]-1), token i and head h:
 //   s_j = scale * q_i . k_j for j <= i,  y_i = sum_j softmax(s)_j v_j
-// with the maximum, the sum and the products' sums in FP32.
+// in one pass over the keys with the running maximum and sum of the softmax.
+//
+// Bound by the tensor cores: 4 D operations a pair of query row and key.  A unit of
+// work is a key/value head of 2 x 128 query rows: floor(128 / G) tokens x G heads
+// each (G = HQ / HK), so that the rows of short sequences fill the tiles, and all
+// heads of a group share the keys and values that are read.  Per tile of 128 keys
+//   S = Q K^T    both operands in shared memory (TMA, 128-byte swizzle), S in TMEM
+//   P = exp2(S - max), BF16, written over S's own columns
+//   O += P V     P from TMEM, V as TMA left it (N-major), O in TMEM
+// The two row tiles alternate: while the tensor cores work for one, the other's
+// four warps (a thread a row) compute its P.  TMEM is full: 2 x (128 S + 128 O).
+// O is rescaled only when a row's maximum has grown by more than 2^8 since its last
+// reference (p <= 2^8 until then; the row's sum is held to the same reference).
+// P is rounded to BF16 (half a step, 2^-8 of a p): kind::f16 takes both operands in
+// one type, and V is BF16.
 #include "common.cuh"
 #include "ptx.cuh"
 
 namespace fp8bq {
 namespace {
 
-// A warp a query row; a lane has four neighbouring values of D.
-__global__ void __launch_bounds__(128) prompt_attention_kernel(const PromptArgs a) {
+constexpr int kKeys = 128;                 // keys a tile
+constexpr int kThreads = 384;              // 2 x 4 softmax warps, MMA warp, copy warp, 2 idle
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
+// registers: a softmax thread holds a row's 128 scores, which the third warpgroup
+// makes room for (384 x 168 at launch)
+constexpr int kHighRegs = 224, kLowRegs = 56;
+constexpr int kHalf = 128 * 128;           // bytes of 128 rows x 64 values
+constexpr float kGrowth = 8.0f;            // log2: a maximum within it keeps its reference
+
+template <int DP>
+struct Cfg {
+  static constexpr int kHalves = DP / 64;
+  static constexpr int kTileBytes = kHalves * kHalf;  // 128 rows of Q, K or V
+  static constexpr int kStages = DP == 128 ? 4 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;  // 1024: alignment
+};
+
+struct Unit {
+  int start;   // the sequence's first row
+  int len;     // its tokens
+  int t0;      // the unit's first token
+  int head;    // key/value head
+  int tiles;   // key tiles; 0: no more units
+  int bad;     // a value that is not finite lies among the last tiles' values
+};
+
+struct Shared {
+  uint64_t q_full[2], q_empty;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t v_clean[2], u_full[2], u_empty[2], done;
+  uint32_t abort, never, tmem, pad;
+  Unit unit[2];
+  int bound[kMaxPrompts + 1];
+  int blocks[kMaxPrompts];
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Units in the order of their work, the longest first: block l of every sequence
+// that has more than l blocks, for l from the top; a block's key/value heads are
+// neighbours.  Runs on one warp.
+struct Units {
+  const int *blocks;
+  int S, top, HK;
+  int64_t total;
+  __device__ int64_t above(int level, int lane) const {  // blocks at `level` and above
+    int n = 0;
+    for (int s = lane; s < S; s += 32) n += max(blocks[s] - level, 0);
+    return __reduce_add_sync(0xFFFFFFFFu, n);
+  }
+  __device__ void find(int64_t u, int lane, int &seq, int &block, int &head) const {
+    const int rank = static_cast<int>(u / HK);
+    head = static_cast<int>(u - static_cast<int64_t>(rank) * HK);
+    int lo = 0, hi = top;  // the last level with above(level) > rank
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (above(mid, lane) > rank) lo = mid; else hi = mid;
+    }
+    block = lo;
+    int k = rank - static_cast<int>(above(lo + 1, lane));  // the k-th sequence with that block
+    seq = 0;
+    for (int s0 = 0; s0 < S; s0 += 32) {
+      uint32_t has = __ballot_sync(0xFFFFFFFFu, s0 + lane < S && blocks[s0 + lane] > lo);
+      const int n = __popc(has);
+      if (k < n) {
+        for (; k > 0; --k) has &= has - 1;
+        seq = s0 + __ffs(has) - 1;
+        break;
+      }
+      k -= n;
+    }
+  }
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                        const __grid_constant__ CUtensorMap vm, const PromptArgs a) {
+  using C = Cfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint8_t *ring = smem + 2 * C::kTileBytes;
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile uint32_t *abort = &sh.abort;
+  const uint64_t limit = a.wait_limit_ns;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.s_full[i], 1), mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_free[i], 4);
+      mbar_init(&sh.u_full[i], 1), mbar_init(&sh.u_empty[i], 9);
+      mbar_init(&sh.v_clean[i], 8);
+    }
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 1);
+    mbar_init(&sh.q_empty, 1), mbar_init(&sh.done, 1);
+    sh.abort = sh.never = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == kCopyWarp && lane == 0) tma_prefetch_desc(&qm), tma_prefetch_desc(&km), tma_prefetch_desc(&vm);
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(a.T) * a.HQ) return;
-  const int h = static_cast<int>(row % a.HQ), tok = static_cast<int>(row / a.HQ);
-  auto bound = [&](int s) { return min(max(__ldg(a.offsets + s), 0), a.T); };
-  int lo = 0, hi = a.S;  // the last s with offsets[s] <= tok
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (bound(mid) <= tok) lo = mid; else hi = mid;
-  }
-  const int start = bound(lo), end = bound(lo + 1);
-  if (tok < start || tok >= end) return;
-  const bool on = lane * 4 < a.D;
-  auto load = [&](const uint16_t *p, float (&f)[4]) {
-    uint2 v = make_uint2(0, 0);
-    if (on) v = __ldg(reinterpret_cast<const uint2 *>(p + lane * 4));
-    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-  };
-  float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-  load(a.q + tok * a.q_ts + h * a.q_hs, q);
-  const int hk = h / (a.HQ / a.HK);
-  for (int j = start; j <= tok; ++j) {
-    float k[4], v[4];
-    load(a.k + j * a.k_ts + hk * a.k_hs, k);
-    load(a.v + j * a.v_ts + hk * a.v_hs, v);
-    float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+  const int G = a.HQ / a.HK, half_tokens = 128 / G, unit_tokens = 2 * half_tokens;
+  for (int s = tid; s <= a.S; s += kThreads) sh.bound[s] = min(max(__ldg(a.offsets + s), 0), a.T);
+  __syncthreads();
+  for (int s = tid; s < a.S; s += kThreads)
+    sh.blocks[s] = (max(sh.bound[s + 1] - sh.bound[s], 0) + unit_tokens - 1) / unit_tokens;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  if (warp < 8) setmaxnreg_inc<kHighRegs>();
+  else setmaxnreg_dec<kLowRegs>();
+
+  if (warp == kCopyWarp) {
+    // ---- copies, and the units for everybody
+    Units units = {sh.blocks, a.S, 0, a.HK, 0};
+    int top = 0;
+    for (int s = lane; s < a.S; s += 32) top = max(top, sh.blocks[s]);
+    units.top = __reduce_max_sync(0xFFFFFFFFu, top);
+    units.total = units.above(0, lane) * a.HK;
+    const int64_t grid = gridDim.x, cta = blockIdx.x;
+    const uint32_t q_bytes = C::kHalves * half_tokens * G * 128;
+    int64_t c = 0;  // copies into the ring so far
+    bool ok = true;
+    int k = 0;
+    auto ring_copy = [&](const CUtensorMap *map, int head, int row, bool skip) {
+      const int st = static_cast<int>(c % C::kStages);
+      if (!mbar_wait(&sh.kv_empty[st], (c / C::kStages & 1) ^ 1, abort, limit)) return false;
+      mbar_arrive_expect_tx(&sh.kv_full[st], C::kTileBytes);
+      ++c;
+      if (skip) return true;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), by = exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * by + p;
+      for (int h = 0; h < C::kHalves; ++h)
+        tma_load_3d(ring + st * C::kTileBytes + h * kHalf, map, &sh.kv_full[st], h * 64, head, row);
+      return true;
+    };
+    for (;; ++k) {
+      // rounds in turn from the left and from the right: equal sums
+      const int64_t u = k * grid + (k & 1 ? grid - 1 - cta : cta);
+      Unit un = {0, 0, 0, 0, 0, 0};
+      if (u < units.total) {
+        int seq, block;
+        units.find(u, lane, seq, block, un.head);
+        un.start = sh.bound[seq];
+        un.len = sh.bound[seq + 1] - un.start;
+        un.t0 = block * unit_tokens;
+        un.tiles = (min(un.len, un.t0 + unit_tokens) + kKeys - 1) / kKeys;
+      }
+      if (lane == 0) {
+        ok = mbar_wait(&sh.u_empty[k & 1], (k >> 1 & 1) ^ 1, abort, limit);
+        if (ok) {
+          sh.unit[k & 1] = un;
+          mbar_arrive(&sh.u_full[k & 1]);
+        }
+        if (ok && un.tiles > 0) {
+          ok = ring_copy(&km, un.head, un.start, a.fault && cta == 0 && k == 0) &&
+               mbar_wait(&sh.q_empty, (k & 1) ^ 1, abort, limit);
+          for (int i = 0; i < 2 && ok; ++i) {
+            mbar_arrive_expect_tx(&sh.q_full[i], q_bytes);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * by + p * v[i];
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_3d(smem + i * C::kTileBytes + h * kHalf, &qm, &sh.q_full[i], h * 64,
+                          un.head * G, un.start + un.t0 + i * half_tokens);
+          }
+          ok = ok && ring_copy(&vm, un.head, un.start, false);
+          for (int j = 1; j < un.tiles && ok; ++j)
+            ok = ring_copy(&km, un.head, un.start + j * kKeys, false) &&
+                 ring_copy(&vm, un.head, un.start + j * kKeys, false);
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok || un.tiles == 0) break;
+    }
+    if (lane == 0 && *abort) {  // copies in flight land before the memory is given up
+      for (int64_t i = c < C::kStages ? 0 : c - C::kStages; i < c; ++i)
+        mbar_wait(&sh.kv_full[i % C::kStages], i / C::kStages & 1, &sh.never, limit);
+      for (int i = 0; i < 2 && k > 0; ++i) mbar_wait(&sh.q_full[i], (k - 1) & 1, &sh.never, limit);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ---- products: S of both row tiles, then P V and the next S of each in turn
+    if (lane == 0) {
+      const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
+      const int steps = a.D / 16;
+      int64_t c = 0;
+      uint32_t pph[2] = {0, 0}, looked = 0;  // tiles whose values were looked through
+      bool ok = true;
+      auto scores = [&](int i, int st) {
+        const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + i * C::kTileBytes));
+        const uint64_t kd = sdesc_kmajor_sw128(smem_u32(ring + st * C::kTileBytes));
+        for (int s = 0; s < steps; ++s) {
+          const uint64_t off = (s >> 2) * (kHalf / 16) + (s & 3) * 2;
+          umma_bf16(tmem + i * 128, qd + off, kd + off, s_desc, s > 0);
+        }
+        umma_commit(&sh.s_full[i]);
+      };
+      auto wait_kv = [&](int64_t n) {
+        return mbar_wait(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit);
+      };
+      for (int k = 0;; ++k) {
+        ok = mbar_wait(&sh.u_full[k & 1], k >> 1 & 1, abort, limit);
+        if (!ok) break;
+        const int tiles = sh.unit[k & 1].tiles, special = sh.unit[k & 1].t0 / kKeys;
+        mbar_arrive(&sh.u_empty[k & 1]);
+        if (tiles == 0) break;
+        ok = wait_kv(c);
+        for (int i = 0; i < 2 && ok; ++i) {
+          ok = mbar_wait(&sh.q_full[i], k & 1, abort, limit);
+          if (!ok) break;
+          tc_fence_after();
+          scores(i, static_cast<int>(c % C::kStages));
+        }
+        if (!ok) break;
+        umma_commit(&sh.kv_empty[c % C::kStages]);
+        if (tiles == 1) umma_commit(&sh.q_empty);
+        ++c;
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int vs = static_cast<int>(c % C::kStages);
+          const bool more = j + 1 < tiles;
+          const int ks = static_cast<int>((c + 1) % C::kStages);
+          ok = wait_kv(c);
+          if (ok && j >= special) {
+            ok = mbar_wait(&sh.v_clean[looked & 1], looked >> 1 & 1, abort, limit);
+            ++looked;
+          }
+          for (int i = 0; i < 2 && ok; ++i) {
+            ok = mbar_wait(&sh.p_ready[i], pph[i], abort, limit);
+            pph[i] ^= 1;
+            if (ok && j == 0) ok = mbar_wait(&sh.o_free[i], (k & 1) ^ 1, abort, limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = sdesc_nmajor_sw128(smem_u32(ring + vs * C::kTileBytes), kHalf);
+            for (int s = 0; s < kKeys / 16; ++s)
+              umma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + s * 8, vd + s * (2048 / 16), o_desc,
+                           j > 0 || s > 0);
+            umma_commit(&sh.o_done[i]);
+            if (i == 1) umma_commit(&sh.kv_empty[vs]);
+            if (more) {
+              if (i == 0) ok = wait_kv(c + 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(i, ks);
+              if (i == 1) umma_commit(&sh.kv_empty[ks]);
+              if (i == 1 && j + 2 == tiles) umma_commit(&sh.q_empty);
+            }
+          }
+          c += more ? 2 : 1;
+        }
+        if (!ok) break;
+      }
+      umma_commit(&sh.done);
+      mbar_wait(&sh.done, 0, &sh.never, limit);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- softmax: a thread a row of tile i
+    const int i = warp >> 2, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
+    const int tok_in = row / G, head_in = row - tok_in * G;
+    const float sc = a.scale_log2;
+    int64_t c = 0;
+    uint32_t sph = 0, oph = 0, looked = 0;
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.u_full[k & 1], k >> 1 & 1, abort, limit));
+      if (!ok) break;
+      Unit un = sh.unit[k & 1];
+      if (un.tiles == 0) break;
+      const int tok = un.t0 + i * half_tokens + tok_in;
+      const int special = un.t0 / kKeys;
+      float ref = -INFINITY, sum = 0.0f;
+      for (int j = 0; j < un.tiles && ok; ++j) {
+        if (j >= special) {
+          // values of these tokens are hidden from some rows: where one is not finite
+          // 0 times it would spoil them, so it is taken out here and added to the
+          // rows that see it at the end
+          const int64_t n = c + 2 * j + 1;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit));
+          if (!ok) break;
+          uint4 *v = reinterpret_cast<uint4 *>(ring + (n % C::kStages) * C::kTileBytes) + tid;
+          bool wrote = false;
+#pragma unroll
+          for (int w = 0; w < C::kTileBytes / 16 / 256; ++w) {
+            const uint4 x = v[w * 256];
+            auto flags = [](uint32_t y) { return ((y & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+            if ((flags(x.x) | flags(x.y) | flags(x.z) | flags(x.w)) == 0) continue;
+            auto clean = [&](uint32_t y) {
+              const uint32_t f = flags(y);
+              return y & ~((f >> 31) * 0xFFFF0000u) & ~((f >> 15 & 1u) * 0xFFFFu);
+            };
+            v[w * 256] = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+            wrote = true;
+          }
+          if (wrote) sh.unit[k & 1].bad = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          // (two barriers in turn: one tile's four warps may be a tile ahead)
+          if (lane == 0) mbar_arrive(&sh.v_clean[looked & 1]);
+          ++looked;
+        }
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.s_full[i], sph, abort, limit));
+        sph ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, s + q * 32);
+        tmem_ld_wait();
+        const int seen = tok - j * kKeys + 1;  // keys of the tile that the row sees
+        if (__any_sync(0xFFFFFFFFu, seen < kKeys)) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x)
+            if (x >= seen) s[x] = 0xFF800000u;  // -inf
+        }
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < 128; ++x) m[x & 3] = fmaxf(m[x & 3], __uint_as_float(s[x]));
+        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        const bool grow = (top - ref) * sc > kGrowth;
+        if (j == 0) {
+          ref = top;
+        } else if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float by = grow ? ex2((ref - top) * sc) : 1.0f;
+          if (grow) ref = top;
+          sum *= by;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_done[i], oph ^ 1, abort, limit));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(o_at + q * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+            tmem_st32(o_at + q * 32, o);
+          }
+        }
+        oph ^= 1;
+        const float neg = ref == -INFINITY ? 0.0f : -ref * sc;
+        float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float p0 = ex2(__fmaf_rn(__uint_as_float(s[q * 64 + 2 * x]), sc, neg));
+            const float p1 = ex2(__fmaf_rn(__uint_as_float(s[q * 64 + 2 * x + 1]), sc, neg));
+            l[x & 1] += p0, l[2 + (x & 1)] += p1;
+            p[x] = pack_bf16(p0, p1);
+          }
+          tmem_st32(s_at + q * 32, p);
+        }
+        sum += (l[0] + l[1]) + (l[2] + l[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[i]);
+      }
+      if (!ok) break;
+      c += 2 * un.tiles;
+      // ---- the unit's end
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_done[i], oph ^ 1, abort, limit));
+      if (!ok) break;
+      tc_fence_after();
+      const bool bad = *reinterpret_cast<volatile int *>(&sh.unit[k & 1].bad) != 0;
+      const bool live = tok_in < half_tokens && tok < un.len;
+      const float by = 1.0f / sum;
+      uint16_t *y = a.y + static_cast<int64_t>(un.start + tok) * a.y_ts +
+                    static_cast<int64_t>(un.head * G + head_in) * a.y_hs;
+#pragma unroll 1
+      for (int q = 0; q < DP / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(o_at + q * 32, o);
+        tmem_ld_wait();
+        if (!live) continue;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+        if (bad)
+          for (int t = special * kKeys; t <= tok; ++t) {
+            const uint16_t *v = a.v + static_cast<int64_t>(un.start + t) * a.v_ts +
+                                static_cast<int64_t>(un.head) * a.v_hs + q * 32;
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (q * 32 + x < a.D) {
+                const uint32_t bits = v[x];
+                if ((bits & 0x7F80u) == 0x7F80u)
+                  o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(bits << 16));
+              }
+          }
+#pragma unroll
+        for (int x = 0; x < 32; x += 8)
+          if (q * 32 + x < a.D) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              w[z] = pack_bf16(__uint_as_float(o[x + 2 * z]), __uint_as_float(o[x + 2 * z + 1]));
+            *reinterpret_cast<uint4 *>(y + q * 32 + x) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.o_free[i]), mbar_arrive(&sh.u_empty[k & 1]);
+    }
   }
-  if (!on) return;
-  uint2 out;
-  const float by = 1.0f / l;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.x) : "f"(o[1] * by), "f"(o[0] * by));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.y) : "f"(o[3] * by), "f"(o[2] * by));
-  *reinterpret_cast<uint2 *>(a.y + tok * a.y_ts + h * a.y_hs + lane * 4) = out;
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) atomicMax(a.status, kStatusTimeout);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, int num_sms, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.T) * a.HQ;
-  return launch_pdl(prompt_attention_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
-                    st, a);
+  const int G = a.HQ / a.HK, half_tokens = 128 / G;
+  CUtensorMap qm, km, vm;
+  if (!make_heads_map(&qm, a.q, a.T, a.HQ, a.D, a.q_ts, a.q_hs, half_tokens, G) ||
+      !make_heads_map(&km, a.k, a.T, a.HK, a.D, a.k_ts, a.k_hs, kKeys, 1) ||
+      !make_heads_map(&vm, a.v, a.T, a.HK, a.D, a.v_ts, a.v_hs, kKeys, 1))
+    return cudaErrorInvalidValue;
+  // units at most: every sequence may end inside one
+  const int64_t blocks = (a.T + 2 * half_tokens - 1) / (2 * half_tokens) + a.S;
+  const int64_t most = blocks * a.HK;
+  const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
+  auto run = [&](auto d) {
+    constexpr int DP = decltype(d)::value;
+    cudaError_t e = allow_smem<prompt_attention_kernel<DP>>(Cfg<DP>::kSmem);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc waits for registers that the block was launched with: no launch
+    // unless the compiled count covers the split
+    static const int regs = [] {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, prompt_attention_kernel<DP>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs * kThreads < 256 * kHighRegs + 128 * kLowRegs) return cudaErrorInvalidConfiguration;
+    return launch_pdl(prompt_attention_kernel<DP>, dim3(grid), dim3(kThreads), Cfg<DP>::kSmem, st, qm,
+                      km, vm, a);
+  };
+  return a.D <= 64 ? run(std::integral_constant<int, 64>{}) : run(std::integral_constant<int, 128>{});
 }
 
 }  // namespace fp8bq
