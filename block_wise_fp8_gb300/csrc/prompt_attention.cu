@@ -149,11 +149,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  if (warp < 8) setmaxnreg_inc<kHighRegs>();
-  else setmaxnreg_dec<kLowRegs>();
 
   if (warp == kCopyWarp) {
     // ---- copies, and the units for everybody
+    setmaxnreg_dec<kLowRegs>();
     Units units = {sh.blocks, a.S, 0, a.HK, 0};
     int top = 0;
     for (int s = lane; s < a.S; s += 32) top = max(top, sh.blocks[s]);
@@ -220,6 +219,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---- products: S of both row tiles, then P V and the next S of each in turn
+    setmaxnreg_dec<kLowRegs>();
     if (lane == 0) {
       const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
       const int steps = a.D / 16;
@@ -295,6 +295,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: a thread a row of tile i
+    setmaxnreg_inc<kHighRegs>();
     const int i = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
@@ -444,6 +445,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free[i]), mbar_arrive(&sh.u_empty[k & 1]);
     }
+  } else {
+    setmaxnreg_dec<kLowRegs>();
   }
   tc_fence_before();
   __syncthreads();
