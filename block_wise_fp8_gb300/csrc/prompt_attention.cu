@@ -51,7 +51,7 @@ struct Unit {
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
   uint64_t v_clean[2], u_full[2], u_empty[2], done;
@@ -69,6 +69,31 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// pairs of FP32 values in one 64-bit register, two operations an instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -126,10 +151,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       mbar_init(&sh.s_full[i], 1), mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_free[i], 4);
       mbar_init(&sh.u_full[i], 1), mbar_init(&sh.u_empty[i], 9);
-      mbar_init(&sh.v_clean[i], 8);
+      mbar_init(&sh.v_clean[i], 8), mbar_init(&sh.q_empty[i], 1);
     }
     for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 1);
-    mbar_init(&sh.q_empty, 1), mbar_init(&sh.done, 1);
+    mbar_init(&sh.done, 1);
     sh.abort = sh.never = 0;
     fence_mbar_init();
   }
@@ -193,9 +218,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           mbar_arrive(&sh.u_full[k & 1]);
         }
         if (ok && un.tiles > 0) {
-          ok = ring_copy(&km, un.head, un.start, a.fault && cta == 0 && k == 0) &&
-               mbar_wait(&sh.q_empty, (k & 1) ^ 1, abort, limit);
+          ok = ring_copy(&km, un.head, un.start, a.fault && cta == 0 && k == 0);
           for (int i = 0; i < 2 && ok; ++i) {
+            ok = mbar_wait(&sh.q_empty[i], (k & 1) ^ 1, abort, limit);
+            if (!ok) break;
             mbar_arrive_expect_tx(&sh.q_full[i], q_bytes);
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
@@ -218,77 +244,85 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    // ---- products: S of both row tiles, then P V and the next S of each in turn
+    // ---- products: S of both row tiles, then P V and the next S of each in turn.
+    // The whole warp walks, so that addresses stay in uniform registers; one lane of
+    // it issues.
     setmaxnreg_dec<kLowRegs>();
-    if (lane == 0) {
-      const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
-      const int steps = a.D / 16;
-      int64_t c = 0;
-      uint32_t pph[2] = {0, 0}, looked = 0;  // tiles whose values were looked through
-      bool ok = true;
-      auto scores = [&](int i, int st) {
-        const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + i * C::kTileBytes));
-        const uint64_t kd = sdesc_kmajor_sw128(smem_u32(ring + st * C::kTileBytes));
-        for (int s = 0; s < steps; ++s) {
-          const uint64_t off = (s >> 2) * (kHalf / 16) + (s & 3) * 2;
-          umma_bf16(tmem + i * 128, qd + off, kd + off, s_desc, s > 0);
+    const uint32_t lead = lane == 0;
+    const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
+    const uint64_t q_base = sdesc_kmajor_sw128(smem_u32(smem));
+    const uint64_t k_base = sdesc_kmajor_sw128(smem_u32(ring));
+    const uint64_t v_base = sdesc_nmajor_sw128(smem_u32(ring), kHalf);
+    const int steps = a.D / 16;
+    uint32_t pph[2] = {0, 0}, looked = 0;  // tiles whose values were looked through
+    int st = 0;
+    uint32_t ring_ph = 0;  // the ring's place and round
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, limit));
+    };
+    auto scores = [&](int i, int s_) {
+      const uint64_t qd = q_base + i * (C::kTileBytes / 16), kd = k_base + s_ * (C::kTileBytes / 16);
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s) {
+        const uint64_t off = (s >> 2) * (kHalf / 16) + (s & 3) * 2;
+        if (s < steps) umma_bf16_if(lead, tmem + i * 128, qd + off, kd + off, s_desc, s > 0);
+      }
+      umma_commit_if(lead, &sh.s_full[i]);
+    };
+    for (int k = 0; ok; ++k) {
+      ok = wait(&sh.u_full[k & 1], k >> 1 & 1);
+      if (!ok) break;
+      const int tiles = __shfl_sync(0xFFFFFFFFu, sh.unit[k & 1].tiles, 0);
+      const int special = __shfl_sync(0xFFFFFFFFu, sh.unit[k & 1].t0, 0) / kKeys;
+      __syncwarp();
+      if (lead) mbar_arrive(&sh.u_empty[k & 1]);
+      if (tiles == 0) break;
+      ok = wait(&sh.kv_full[st], ring_ph);
+      for (int i = 0; i < 2 && ok; ++i) {
+        ok = wait(&sh.q_full[i], k & 1);
+        tc_fence_after();
+        if (ok) scores(i, st);
+      }
+      if (!ok) break;
+      umma_commit_if(lead, &sh.kv_empty[st]);
+      if (tiles == 1) umma_commit_if(lead, &sh.q_empty[0]), umma_commit_if(lead, &sh.q_empty[1]);
+      if (++st == C::kStages) st = 0, ring_ph ^= 1;
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int vs = st;
+        const bool more = j + 1 < tiles;
+        ok = wait(&sh.kv_full[vs], ring_ph);
+        if (++st == C::kStages) st = 0, ring_ph ^= 1;
+        if (ok && j >= special) {
+          ok = wait(&sh.v_clean[looked & 1], looked >> 1 & 1);
+          ++looked;
         }
-        umma_commit(&sh.s_full[i]);
-      };
-      auto wait_kv = [&](int64_t n) {
-        return mbar_wait(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit);
-      };
-      for (int k = 0;; ++k) {
-        ok = mbar_wait(&sh.u_full[k & 1], k >> 1 & 1, abort, limit);
-        if (!ok) break;
-        const int tiles = sh.unit[k & 1].tiles, special = sh.unit[k & 1].t0 / kKeys;
-        mbar_arrive(&sh.u_empty[k & 1]);
-        if (tiles == 0) break;
-        ok = wait_kv(c);
-        for (int i = 0; i < 2 && ok; ++i) {
-          ok = mbar_wait(&sh.q_full[i], k & 1, abort, limit);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ok = ok && wait(&sh.p_ready[i], pph[i]);
+          pph[i] ^= 1;
+          if (ok && j == 0) ok = wait(&sh.o_free[i], (k & 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
-          scores(i, static_cast<int>(c % C::kStages));
-        }
-        if (!ok) break;
-        umma_commit(&sh.kv_empty[c % C::kStages]);
-        if (tiles == 1) umma_commit(&sh.q_empty);
-        ++c;
-        for (int j = 0; j < tiles && ok; ++j) {
-          const int vs = static_cast<int>(c % C::kStages);
-          const bool more = j + 1 < tiles;
-          const int ks = static_cast<int>((c + 1) % C::kStages);
-          ok = wait_kv(c);
-          if (ok && j >= special) {
-            ok = mbar_wait(&sh.v_clean[looked & 1], looked >> 1 & 1, abort, limit);
-            ++looked;
-          }
-          for (int i = 0; i < 2 && ok; ++i) {
-            ok = mbar_wait(&sh.p_ready[i], pph[i], abort, limit);
-            pph[i] ^= 1;
-            if (ok && j == 0) ok = mbar_wait(&sh.o_free[i], (k & 1) ^ 1, abort, limit);
+          const uint64_t vd = v_base + vs * (C::kTileBytes / 16);
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            umma_bf16_ta_if(lead, tmem + 256 + i * 128, tmem + i * 128 + s * 8, vd + s * (2048 / 16),
+                            o_desc, j > 0 || s > 0);
+          umma_commit_if(lead, &sh.o_done[i]);
+          if (i == 1) umma_commit_if(lead, &sh.kv_empty[vs]);
+          if (more) {
+            if (i == 0) ok = wait(&sh.kv_full[st], ring_ph);
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = sdesc_nmajor_sw128(smem_u32(ring + vs * C::kTileBytes), kHalf);
-            for (int s = 0; s < kKeys / 16; ++s)
-              umma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + s * 8, vd + s * (2048 / 16), o_desc,
-                           j > 0 || s > 0);
-            umma_commit(&sh.o_done[i]);
-            if (i == 1) umma_commit(&sh.kv_empty[vs]);
-            if (more) {
-              if (i == 0) ok = wait_kv(c + 1);
-              if (!ok) break;
-              tc_fence_after();
-              scores(i, ks);
-              if (i == 1) umma_commit(&sh.kv_empty[ks]);
-              if (i == 1 && j + 2 == tiles) umma_commit(&sh.q_empty);
-            }
+            scores(i, st);
+            if (j + 2 == tiles) umma_commit_if(lead, &sh.q_empty[i]);
+            if (i == 1) umma_commit_if(lead, &sh.kv_empty[st]);
           }
-          c += more ? 2 : 1;
         }
-        if (!ok) break;
+        if (more && ++st == C::kStages) st = 0, ring_ph ^= 1;
       }
+    }
+    if (lead) {
       umma_commit(&sh.done);
       mbar_wait(&sh.done, 0, &sh.never, limit);
     }
@@ -357,8 +391,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
         }
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 128; ++x) m[x & 3] = fmaxf(m[x & 3], __uint_as_float(s[x]));
-        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        for (int x = 0; x < 128; x += 2)
+          m[x >> 1 & 3] = max3(m[x >> 1 & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+        const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]);
         const bool grow = (top - ref) * sc > kGrowth;
         if (j == 0) {
           ref = top;
@@ -381,20 +416,25 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
         }
         oph ^= 1;
         const float neg = ref == -INFINITY ? 0.0f : -ref * sc;
-        float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t sc2 = pair(sc, sc), neg2 = pair(neg, neg);
+        uint64_t l[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t p[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            const float p0 = ex2(__fmaf_rn(__uint_as_float(s[q * 64 + 2 * x]), sc, neg));
-            const float p1 = ex2(__fmaf_rn(__uint_as_float(s[q * 64 + 2 * x + 1]), sc, neg));
-            l[x & 1] += p0, l[2 + (x & 1)] += p1;
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(s[q * 64 + 2 * x]), __uint_as_float(s[q * 64 + 2 * x + 1])),
+                        sc2, neg2), p0, p1);
+            p0 = ex2(p0), p1 = ex2(p1);
+            l[x & 1] = add2(l[x & 1], pair(p0, p1));
             p[x] = pack_bf16(p0, p1);
           }
           tmem_st32(s_at + q * 32, p);
         }
-        sum += (l[0] + l[1]) + (l[2] + l[3]);
+        float l0, l1;
+        unpair(add2(l[0], l[1]), l0, l1);
+        sum += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
