@@ -363,7 +363,9 @@ int check_kv4_attention(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D
   if (D != 64 && D != 128 && D != 256) return FP8BQ_ERR_UNSUPPORTED;
   const int64_t G = HQ / HK;
   if (Tq > kKv4MaxRows || G > kKv4MaxRows || G * Tq > kKv4MaxRows) return FP8BQ_ERR_UNSUPPORTED;
-  if (B * HK * ((G * Tq + 7) / 8) > kKv4MaxItems || B * HK > 65535) return FP8BQ_ERR_SHAPE;
+  const int64_t items = B * HK * ((G * Tq + 7) / 8);
+  if (items > kKv4MaxItems || B * HK > 65535 || items * ((max_len + 63) / 64) > (int64_t(1) << 30))
+    return FP8BQ_ERR_SHAPE;
   return FP8BQ_OK;
 }
 

@@ -23,8 +23,7 @@
 namespace fp8bq {
 namespace {
 
-constexpr int kTile = 128;      // tokens a stage holds
-constexpr int kWarps = 4;       // consumer warps, 32 tokens of a tile each
+constexpr int kWarps = 4;       // consumer warps
 constexpr int kThreads = kWarps * 32 + 32;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -53,17 +52,18 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-template <int D>
-constexpr int kv4_stages() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
-
 template <int D, int NB>
 struct Sizes {
-  static constexpr int kRows = 8 * NB;                  // query rows of an item
-  static constexpr int kStages = kv4_stages<D>();
-  static constexpr int kStageBytes = kTile * 9 * D / 8;
-  static constexpr int kPart = kRows * (D + 2);         // floats of a CTA's part of an item
-  static constexpr int kJoinBytes = kWarps * kPart * 4;
-  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + (kKv4MaxBatch + 2) * 4 + 256;
+  static constexpr int kRows = 8 * NB;             // query rows of an item
+  static constexpr int kMB = 2;                    // blocks of 16 tokens, a warp's of a tile
+  static constexpr int kTile = kWarps * 16 * kMB;  // tokens a stage holds
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kKvBytes = kTile * 9 * D / 8;
+  static constexpr int kStageBytes = kKvBytes + kRows * D * 2;  // and an item's query rows
+  static constexpr int kPart = kRows * (D + 2);    // floats of a CTA's part of an item
+  // three quarters of every warp's sums, and all rows' maxima and sums
+  static constexpr int kJoinBytes = 3 * kRows * D * 4 + kWarps * kRows * 8;
+  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes;  // and (B + 1) * 4
   static constexpr int kCtas = NB == 1 && D <= 128 ? 3 : D == 256 && NB == 2 ? 1 : 2;  // an SM
 };
 
@@ -74,33 +74,44 @@ struct Place {
 
 struct Bars {
   uint64_t full[4], empty[4];
-  uint32_t abort, never, ticket, pad;
+  uint32_t abort, never, ticket[2];
   uint32_t pages[4];  // which pages of a stage's tile are there
 };
 
-// The tiles of the batch: sequence b has len/128 (up) of them for each of its HK *
+// The tiles of the batch: sequence b has those of its length for each of its HK *
 // blocks items; first[b] counts those of one item before b.  Every CTA takes an
-// equal run of the whole list, so that ragged batches fill the device evenly.
+// equal run of the whole list (the first `more` of them one tile more), so that
+// ragged batches fill the device evenly.
 struct Plan {
   const int *first;  // [B + 1]
   int B, items;      // items a sequence: HK * blocks
-  __device__ int64_t total() const { return static_cast<int64_t>(first[B]) * items; }
-  // fewer CTAs than the grid has take part where there are fewer tiles
-  __device__ int64_t ctas() const { return min(max(total(), int64_t(1)), static_cast<int64_t>(gridDim.x)); }
-  __device__ int64_t start(int64_t cta) const { return total() * min(cta, ctas()) / ctas(); }
-  __device__ int cta_of(int64_t tile) const { return static_cast<int>(((tile + 1) * ctas() - 1) / total()); }
-  __device__ Place at(int64_t f) const {
+  int each, more;    // tiles a CTA, and CTAs with one more
+  __device__ Plan(const int *f, int B_, int items_) : first(f), B(B_), items(items_) {
+    const int total = f[B_] * items_;
+    // fewer CTAs than the grid has take part where there are fewer tiles
+    const int ctas = min(max(total, 1), static_cast<int>(gridDim.x));
+    each = total / ctas;
+    more = total - each * ctas;
+    if (total == 0) each = 0;
+  }
+  __device__ int total() const { return first[B] * items; }
+  __device__ int start(int cta) const { return min(total(), cta * each + min(cta, more)); }
+  __device__ int cta_of(int tile) const {
+    const int longer = more * (each + 1);
+    return tile < longer ? tile / (each + 1) : more + (tile - longer) / each;
+  }
+  __device__ Place at(int f) const {
     int lo = 0, hi = B;  // the last b with first[b] * items <= f that has tiles
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (static_cast<int64_t>(first[mid]) * items <= f) lo = mid; else hi = mid;
+      if (first[mid] * items <= f) lo = mid; else hi = mid;
     }
     Place p;
     p.b = lo;
     p.tiles = first[lo + 1] - first[lo];
-    const int64_t in = f - static_cast<int64_t>(first[lo]) * items;
-    p.item = static_cast<int>(in / p.tiles);
-    p.tile = static_cast<int>(in - static_cast<int64_t>(p.item) * p.tiles);
+    const int in = f - first[lo] * items;
+    p.item = in / p.tiles;
+    p.tile = in - p.item * p.tiles;
     return p;
   }
   __device__ void next(Place &p) const {
@@ -118,13 +129,15 @@ struct Plan {
 template <int D, int NB>
 __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_kernel(const Kv4AttnArgs a) {
   using S = Sizes<D, NB>;
-  constexpr int kRows = S::kRows, kStages = S::kStages;
+  constexpr int kRows = S::kRows, kStages = S::kStages, kMB = S::kMB, kTile = S::kTile;
   constexpr int kKeyWords = D / 32;       // 32-bit words of codes a lane takes of a key row
   constexpr int kTiles = D / 16;          // products of 16 values of the D
   constexpr int kValueWords = D / 64;     // words of codes a lane takes of a value row
+  constexpr int kQuarter = kTiles / kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  float *join = reinterpret_cast<float *>(smem + kStages * S::kStageBytes);
-  int *first = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(join) + S::kJoinBytes);
+  float4 *join = reinterpret_cast<float4 *>(smem + kStages * S::kStageBytes);
+  float2 *join_stat = reinterpret_cast<float2 *>(join + 3 * kRows * D / 4);
+  int *first = reinterpret_cast<int *>(smem + S::kSmem);
   __shared__ Bars bars;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile uint32_t *abort = &bars.abort;
@@ -157,32 +170,43 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     }
   }
   __syncthreads();
-  const Plan plan = {first, a.B, a.HK * blocks};
-  const int64_t f0 = plan.start(blockIdx.x), f1 = plan.start(static_cast<int64_t>(blockIdx.x) + 1);
+  const Plan plan(first, a.B, a.HK * blocks);
+  const int f0 = plan.start(blockIdx.x), f1 = plan.start(blockIdx.x + 1);
 
   if (warp == kWarps) {
-    // ---- copies: a tile's pages, each one run of bytes, into the stage
+    // ---- copies: a tile's pages, each one run of bytes, into the stage, and with an
+    // item's first tile its query rows
     Place p = f0 < f1 ? plan.at(f0) : Place{};
     const int per_tile = kTile >> a.page_log2;
     auto look_up = [&]() -> int {  // this lane's page of tile p, -1 where there is none
-      const int at = (p.tile << (7 - a.page_log2)) + lane;
+      const int at = p.tile * per_tile + lane;
       if (lane >= per_tile || (at << a.page_log2) >= length(p.b)) return -1;
       const int page = __ldg(a.table + static_cast<int64_t>(p.b) * a.width + at);
       return page < a.pages ? page : -1;
     };
     int page = f0 < f1 ? look_up() : -1;
     int st = 0, ph = 1;
-    int64_t f = f0;
+    int f = f0;
     for (; f < f1; ++f) {
-      const int head = p.item / blocks;
+      const int head = p.item / blocks, row = (p.item - head * blocks) * kRows + lane;
+      const bool q_too = f == f0 || p.tile == 0;
+      const bool q_on = q_too && lane < kRows && row < R;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars.empty[st], ph, abort, a.wait_limit_ns))) break;
       const bool on = page >= 0;
       const uint32_t there = __ballot_sync(0xFFFFFFFFu, on);
       if (lane == 0) {
         bars.pages[st] = there;
-        mbar_arrive_expect_tx(&bars.full[st], __popc(there) * pg.bytes);
+        const int rows = q_too ? min(kRows, R - row) : 0;  // (row: the item's first)
+        mbar_arrive_expect_tx(&bars.full[st], __popc(there) * pg.bytes + rows * D * 2);
       }
       __syncwarp();
+      if (q_on) {
+        const int i = row / a.G;
+        bulk_load_1d(smem + st * S::kStageBytes + S::kKvBytes + lane * D * 2,
+                     a.q + (static_cast<int64_t>(p.b) * a.Tq + i) * a.q_ts +
+                         static_cast<int64_t>(head * a.G + row - i * a.G) * a.q_hs,
+                     D * 2, &bars.full[st]);
+      }
       if (on && !(a.fault && blockIdx.x == 0 && f == f0))
         bulk_load_1d(smem + st * S::kStageBytes + lane * pg.bytes,
                      a.cache + (static_cast<int64_t>(page) * a.HK + head) * pg.bytes, pg.bytes,
@@ -194,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
       }
     }
     if (*abort) {  // copies in flight land before the memory is given up
-      for (int64_t k = f - kStages < f0 ? f0 : f - kStages; k < f; ++k)
+      for (int k = max(f - kStages, f0); k < f; ++k)
         mbar_wait(&bars.full[(k - f0) % kStages], (k - f0) / kStages & 1, &bars.never, a.wait_limit_ns);
     }
   } else {
@@ -209,7 +233,34 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     int st = 0, ph = 0;
     Place p = f0 < f1 ? plan.at(f0) : Place{};
     int len = 0, row0 = 0, head = 0;
-    for (int64_t f = f0; f < f1; ++f) {
+    Place early = p, late = p;    // items with parts elsewhere: before this run, behind it
+    bool has_early = false, has_late = false;
+    // what a part with maximum m counts under the maximum of all (one with nothing seen
+    // holds zeros, or the NaN that a row was given)
+    auto factor = [](float m, float all) { return m == -INFINITY ? (all == -INFINITY ? 1.0f : 0.0f) : ex2(m - all); };
+    // product j of query rows nb * 8 + 2t, + 1 of an item: two values of each
+    auto finish = [&](int b, int hd, int r0, int nb, int j, float4 v, const float (&m)[2], const float (&l)[2]) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = r0 + nb * 8 + 2 * t + c;
+        if (r >= R) continue;
+        const int i = r / a.G;
+        const float by = l[c] == 0.0f ? 0.0f : a.v_scale / l[c];
+        uint32_t out;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"((c ? v.w : v.z) * by), "f"((c ? v.y : v.x) * by));
+        *reinterpret_cast<uint32_t *>(a.y + (static_cast<int64_t>(b) * a.Tq + i) * a.y_ts +
+                                      static_cast<int64_t>(hd * a.G + r - i * a.G) * a.y_hs +
+                                      g * (D / 8) + 2 * j) = out;
+        if (a.stats && j == 0 && g == 0)
+          *reinterpret_cast<float2 *>(a.stats + ((static_cast<int64_t>(b) * a.HK + hd) * R + r) * 2) =
+              make_float2(m[c], l[c]);
+      }
+    };
+    for (int f = f0; f < f1; ++f) {
+      // (after a wait that gave up the walk goes on, over whatever the memory holds,
+      // so that no warp leaves the others at a barrier)
+      mbar_wait(&bars.full[st], ph, abort, a.wait_limit_ns);
+      const uint8_t *stage = smem + st * S::kStageBytes;
       if (f == f0 || p.tile == 0) {
         // ---- a new item: its query rows
         len = length(p.b);
@@ -223,11 +274,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
           if (row < R) {
-            const int i = row / a.G;
-            const uint16_t *q = a.q + (static_cast<int64_t>(p.b) * a.Tq + i) * a.q_ts +
-                                static_cast<int64_t>(head * a.G + row - i * a.G) * a.q_hs + t * (D / 4);
+            const uint4 *q = reinterpret_cast<const uint4 *>(stage + S::kKvBytes + (nb * 8 + g) * D * 2 + t * (D / 2));
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) raw[k] = __ldg(reinterpret_cast<const uint4 *>(q) + k);
+            for (int k = 0; k < D / 32; ++k) raw[k] = q[k];
           }
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
@@ -262,26 +311,22 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
             for (int c = 0; c < 4; ++c) o[j][nb][c] = 0.0f;
         }
       }
-      // (after a wait that gave up the walk goes on, over whatever the memory holds,
-      // so that no warp leaves the others at a barrier)
-      mbar_wait(&bars.full[st], ph, abort, a.wait_limit_ns);
-      const uint8_t *stage = smem + st * S::kStageBytes;
-      const int tok0 = p.tile * kTile + warp * 32;
+      const int tok0 = p.tile * kTile + warp * (16 * kMB);
       const uint32_t there = __shfl_sync(0xFFFFFFFFu, bars.pages[st], 0);
       const int per_tile = kTile >> a.page_log2;
-      // every token of the warp's 32 seen by every row, and its pages there
+      // every token of the warp's seen by every row, and the pages there
       const int seen_by_all = len - (a.Tq - 1);
-      const bool whole = tok0 + 32 <= seen_by_all && there == (1u << per_tile) - 1u;
+      const bool whole = tok0 + 16 * kMB <= seen_by_all && there == (1u << per_tile) - 1u;
       auto block_of = [&](int mb, int &in) {  // page of the warp's 16-token block, place in it
-        const int at = warp * 32 + mb * 16;
+        const int at = (warp * kMB + mb) * 16;
         in = at & (P - 1);
         return stage + (at >> a.page_log2) * pg.bytes;
       };
       if (whole || tok0 < len) {
-        float s[2][NB][4];
-        // ---- scores of 2 x 16 tokens
+        float s[kMB][NB][4];
+        // ---- scores
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
+        for (int mb = 0; mb < kMB; ++mb) {
           int in;
           const uint8_t *page = block_of(mb, in);
           uint32_t w[2][kKeyWords];
@@ -332,15 +377,15 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         // ---- log2 units; what a row may not see goes to -inf
         if (whole) {
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+          for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int c = 0; c < 4; ++c) s[mb][nb][c] *= qs[nb][c & 1];
         } else {
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb) {
-            const bool here = there >> ((warp * 32 + mb * 16) >> a.page_log2) & 1u;
+          for (int mb = 0; mb < kMB; ++mb) {
+            const bool here = there >> ((warp * kMB + mb) * 16 >> a.page_log2) & 1u;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -352,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         }
         if (a.logits) {
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+          for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -370,7 +415,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = fmaxf(fmaxf(s[0][nb][c], s[0][nb][c + 2]), fmaxf(s[1][nb][c], s[1][nb][c + 2]));
+            float m = fmaxf(s[0][nb][c], s[0][nb][c + 2]);
+#pragma unroll
+            for (int mb = 1; mb < kMB; ++mb) m = fmaxf(m, fmaxf(s[mb][nb][c], s[mb][nb][c + 2]));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
@@ -390,13 +437,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
           }
         }
         // ---- p, and its fragments for the second product: rows become columns
-        uint32_t pf[2][NB][2];
+        uint32_t pf[kMB][NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const float m0 = mx[nb][0] == -INFINITY ? 0.0f : mx[nb][0];
           const float m1 = mx[nb][1] == -INFINITY ? 0.0f : mx[nb][1];
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb) {
+          for (int mb = 0; mb < kMB; ++mb) {
             const float p0 = ex2(s[mb][nb][0] - m0), p1 = ex2(s[mb][nb][1] - m1);
             const float p2 = ex2(s[mb][nb][2] - m0), p3 = ex2(s[mb][nb][3] - m1);
             sum[nb][0] += p0 + p2, sum[nb][1] += p1 + p3;
@@ -406,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         }
         // ---- p times the values
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
+        for (int mb = 0; mb < kMB; ++mb) {
           int in;
           const uint8_t *page = block_of(mb, in);
           uint32_t w[4][kValueWords];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the products' order
@@ -431,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
           if (!whole) {
             // values of tokens that no row may see count as 0 whatever their bytes
             // hold; a NaN that some rows see goes to those rows alone
-            const bool here = there >> ((warp * 32 + mb * 16) >> a.page_log2) & 1u;
+            const bool here = there >> ((warp * kMB + mb) * 16 >> a.page_log2) & 1u;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int tok = tok0 + mb * 16 + t + r * 4;
@@ -492,107 +539,134 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
       if (lane == 0) mbar_arrive(&bars.empty[st]);
       if (++st == kStages) st = 0, ph ^= 1;
 
-      // ---- the item's end, or the run's: the warps' sums together
+      // ---- the item's end, or the run's: the warps' sums together.  Every warp has
+      // sums of the same values in the same places, and ends up with a quarter of them.
       const bool ends_here = p.tile + 1 == p.tiles;
       if (ends_here || f + 1 == f1) {
         const bool begun_here = f - p.tile >= f0;
-        const bool alone = begun_here && ends_here;  // no other CTA has a part of it
-        float *mine = join + warp * S::kPart;
+        named_bar_sync(1, kWarps * 32);  // what the memory held before has been read
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float l = sum[nb][c];
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            const int row = nb * 8 + 2 * t + c;
-            if (g == 0) mine[kRows * D + row * 2] = mx[nb][c], mine[kRows * D + row * 2 + 1] = l;
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j)
-              *reinterpret_cast<float2 *>(mine + row * D + g * (D / 8) + 2 * j) =
-                  make_float2(o[j][nb][c], o[j][nb][c + 2]);
+            if (g == 0) join_stat[warp * kRows + nb * 8 + 2 * t + c] = make_float2(mx[nb][c], l);
           }
-        named_bar_sync(1, kWarps * 32);
-        const int64_t item = static_cast<int64_t>(p.b) * plan.items + p.item;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (begun_here ? 1 : 0);
-        // a thread has 4 neighbouring values of a row
-        auto finish = [&](float4 v, int row, int d, float m, float l) {
-          const int r = row0 + row;
-          if (r >= R) return;
-          const int i = r / a.G;
-          const float by = l == 0.0f ? 0.0f : a.v_scale / l;
-          uint16_t *y = a.y + (static_cast<int64_t>(p.b) * a.Tq + i) * a.y_ts +
-                        static_cast<int64_t>(head * a.G + r - i * a.G) * a.y_hs + d;
-          uint2 out;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.x) : "f"(v.y * by), "f"(v.x * by));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.y) : "f"(v.w * by), "f"(v.z * by));
-          *reinterpret_cast<uint2 *>(y) = out;
-          if (a.stats && d == 0)
-            *reinterpret_cast<float2 *>(a.stats + ((static_cast<int64_t>(p.b) * a.HK + head) * R + r) * 2) =
-                make_float2(m, l);
-        };
-        for (int e = tid; e < kRows * D / 4; e += kWarps * 32) {
-          const int row = e / (D / 4), d = e % (D / 4) * 4;
-          float m = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join[w * S::kPart + kRows * D + row * 2]);
-          float4 v = make_float4(0, 0, 0, 0);
-          float l = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            // (a part with nothing seen holds zeros, or the NaN that a row was given)
-            const float mw = join[w * S::kPart + kRows * D + row * 2];
-            const float by = mw == -INFINITY ? (m == -INFINITY ? 1.0f : 0.0f) : ex2(mw - m);
-            const float4 x = *reinterpret_cast<const float4 *>(join + w * S::kPart + row * D + d);
-            v.x += x.x * by, v.y += x.y * by, v.z += x.z * by, v.w += x.w * by;
-            l += join[w * S::kPart + kRows * D + row * 2 + 1] * by;
-          }
-          if (alone) {
-            finish(v, row, d, m, l);
-          } else {
-            float *to = a.part + slot * S::kPart;
-            *reinterpret_cast<float4 *>(to + row * D + d) = v;
-            if (d == 0) to[kRows * D + row * 2] = m, to[kRows * D + row * 2 + 1] = l;
+          for (int j = 0; j < kTiles; ++j) {
+            const int to = j / kQuarter, from = warp - (warp > to);  // place among the other three
+            if (to != warp)
+              join[((j * NB + nb) * 3 + from) * 32 + lane] =
+                  make_float4(o[j][nb][0], o[j][nb][1], o[j][nb][2], o[j][nb][3]);
           }
         }
-        if (!alone) {
-          // the last CTA to leave its part sums all of them, in the order of the tokens
-          const int64_t s0 = static_cast<int64_t>(first[p.b]) * plan.items + static_cast<int64_t>(p.item) * p.tiles;
-          const int c0 = plan.cta_of(s0), c1 = plan.cta_of(s0 + p.tiles - 1);
-          __threadfence();
-          named_bar_sync(1, kWarps * 32);
-          if (tid == 0) {
-            const uint32_t seen = atom_add_acq_rel_gpu(a.tickets + item, 1u);
-            bars.ticket = seen;
-            if (seen == static_cast<uint32_t>(c1 - c0)) a.tickets[item] = 0u;
+        named_bar_sync(1, kWarps * 32);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float m[2], l[2], by[kWarps][2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float2 st[kWarps];
+            m[c] = -INFINITY, l[c] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              st[w] = join_stat[w * kRows + nb * 8 + 2 * t + c];
+              m[c] = fmaxf(m[c], st[w].x);
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              by[w][c] = factor(st[w].x, m[c]);
+              l[c] += st[w].y * by[w][c];
+            }
           }
-          named_bar_sync(1, kWarps * 32);
-          if (bars.ticket == static_cast<uint32_t>(c1 - c0)) {
-            __threadfence();
-            // the item begins in the second slot of its first CTA, and goes on in the
-            // first one of each of the others
-            auto at = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * S::kPart; };
-            for (int e = tid; e < kRows * D / 4; e += kWarps * 32) {
-              const int row = e / (D / 4), d = e % (D / 4) * 4;
-              float m = -INFINITY;
-              for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(at(c) + kRows * D + row * 2));
-              float4 v = make_float4(0, 0, 0, 0);
-              float l = 0.0f;
-              for (int c = c0; c <= c1; ++c) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(at(c) + kRows * D + row * 2));
-                const float by = ml.x == -INFINITY ? (m == -INFINITY ? 1.0f : 0.0f) : ex2(ml.x - m);
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(at(c) + row * D + d));
-                v.x += x.x * by, v.y += x.y * by, v.z += x.z * by, v.w += x.w * by;
-                l += ml.y * by;
+#pragma unroll
+          for (int k = 0; k < kQuarter; ++k) {
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {  // the warps in order, whoever sums
+              float4 x;
+              if (w == warp) {
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q)
+                  if (q == warp)
+                    x = make_float4(o[q * kQuarter + k][nb][0], o[q * kQuarter + k][nb][1],
+                                    o[q * kQuarter + k][nb][2], o[q * kQuarter + k][nb][3]);
+              } else {
+                x = join[(((warp * kQuarter + k) * NB + nb) * 3 + w - (w > warp)) * 32 + lane];
               }
-              finish(v, row, d, m, l);
+              v.x += x.x * by[w][0], v.y += x.y * by[w][1], v.z += x.z * by[w][0], v.w += x.w * by[w][1];
+            }
+            if (begun_here && ends_here) {  // no other CTA has a part of it
+              finish(p.b, head, row0, nb, warp * kQuarter + k, v, m, l);
+            } else {
+              float *to = a.part + (2 * static_cast<int64_t>(blockIdx.x) + begun_here) * S::kPart;
+              reinterpret_cast<float4 *>(to)[((warp * kQuarter + k) * NB + nb) * 32 + lane] = v;
+              if (k == 0 && warp == 0 && g == 0)
+                *reinterpret_cast<float4 *>(to + kRows * D + (nb * 8 + 2 * t) * 2) =
+                    make_float4(m[0], l[0], m[1], l[1]);
             }
           }
         }
-        named_bar_sync(1, kWarps * 32);  // before the shared sums are written again
+        if (!(begun_here && ends_here)) {
+          named_bar_sync(1, kWarps * 32);
+          if (tid == 0)  // (the addition releases what the barrier has gathered)
+            bars.ticket[begun_here] = atom_add_acq_rel_gpu(a.tickets + p.b * plan.items + p.item, 1u);
+          if (begun_here) late = p, has_late = true;
+          else early = p, has_early = true;
+        }
       }
       if (f + 1 < f1) plan.next(p);
+    }
+    // ---- items that other CTAs have parts of: the last to leave its part sums all of
+    // them, in the order of the tokens
+    if (has_early || has_late) {
+      named_bar_sync(1, kWarps * 32);
+#pragma unroll 1
+      for (int n = 0; n < 2; ++n) {
+        if (!(n ? has_late : has_early)) continue;
+        const Place &e = n ? late : early;
+        const int s0 = first[e.b] * plan.items + e.item * e.tiles;
+        const int c0 = plan.cta_of(s0), c1 = plan.cta_of(s0 + e.tiles - 1);
+        if (bars.ticket[n] != static_cast<uint32_t>(c1 - c0)) continue;
+        if (tid == 0) a.tickets[e.b * plan.items + e.item] = 0u;
+        __threadfence();
+        const int hd = e.item / blocks, r0 = (e.item - hd * blocks) * kRows;
+        // the item begins in the second slot of its first CTA, and goes on in the first
+        // one of each of the others
+        auto at = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * S::kPart; };
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          auto stat = [&](int c) {
+            return __ldcg(reinterpret_cast<const float4 *>(at(c) + kRows * D + (nb * 8 + 2 * t) * 2));
+          };
+          float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) {
+            const float4 s = stat(c);
+            m[0] = fmaxf(m[0], s.x), m[1] = fmaxf(m[1], s.z);
+          }
+          float4 v[kQuarter];
+#pragma unroll
+          for (int k = 0; k < kQuarter; ++k) v[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) {
+            const float4 s = stat(c);
+            const float f0_ = factor(s.x, m[0]), f1_ = factor(s.z, m[1]);
+            l[0] += s.y * f0_, l[1] += s.w * f1_;
+#pragma unroll
+            for (int k = 0; k < kQuarter; ++k) {
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(at(c)) +
+                                      ((warp * kQuarter + k) * NB + nb) * 32 + lane);
+              v[k].x += x.x * f0_, v[k].y += x.y * f1_, v[k].z += x.z * f0_, v[k].w += x.w * f1_;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kQuarter; ++k) finish(e.b, hd, r0, nb, warp * kQuarter + k, v[k], m, l);
+        }
+      }
     }
     // ---- sequences without a cached token: zeros
     const int64_t rows = static_cast<int64_t>(a.Tq) * a.HK * a.G;
@@ -684,15 +758,15 @@ cudaError_t launch_kv4_attention(Kv4AttnArgs a, void *ws, int num_sms, cudaStrea
   auto run = [&](auto d, auto n) {
     constexpr int D = decltype(d)::value, NB = decltype(n)::value;
     using S = Sizes<D, NB>;
-    cudaError_t e = allow_smem<kv4_attention_kernel<D, NB>>(S::kSmem);
+    cudaError_t e = allow_smem<kv4_attention_kernel<D, NB>>(S::kSmem + (kKv4MaxBatch + 1) * 4);
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(a.B) * a.HK * ((R + S::kRows - 1) / S::kRows) *
-                          ((a.max_len + kTile - 1) / kTile);
+                          ((a.max_len + S::kTile - 1) / S::kTile);
     const int64_t most = static_cast<int64_t>(num_sms) * S::kCtas;
     const int64_t grid = tiles < most ? (tiles < 1 ? 1 : tiles) : most;
     return launch_pdl(kv4_attention_kernel<D, NB>,
                       dim3(static_cast<unsigned>(grid < kMaxCtas ? grid : kMaxCtas)), dim3(kThreads),
-                      S::kSmem, st, a);
+                      S::kSmem + (a.B + 1) * 4, st, a);
   };
   auto by_rows = [&](auto d) {
     return R <= 8 ? run(d, std::integral_constant<int, 1>{}) : run(d, std::integral_constant<int, 2>{});

@@ -635,7 +635,8 @@ FP8BQ_API int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, con
  * of its softmax weights over the head's HQ / HK * Tq query rows (where sequences
  * share a page, in no fixed order; everything else is the same from call to call).
  * HQ / HK * Tq <= 128 (ERR_UNSUPPORTED); B <= 1024, B * HK <= 65535,
- * B * HK * ceil(HQ / HK * Tq / 8) <= 65536, width * page <= 2^28 (ERR_SHAPE).
+ * n = B * HK * ceil(HQ / HK * Tq / 8) <= 65536, width * page <= 2^28 and n times its
+ * blocks of 64 tokens <= 2^30 (ERR_SHAPE).
  * Workspace: fp8bq_kv4_workspace_bytes(B, Tq, HQ, HK, D, width * page, weights !=
  * NULL), zeroed once; one that is large enough serves calls of any sizes, of this
  * function alone.  One launch, two with weights. */
