@@ -345,10 +345,8 @@ int check_kv4_sizes(int64_t pages, int64_t page, int64_t HK, int64_t D) {
 
 // rows of keys and values beside the cache (append and read); T > 0
 int check_kv4_rows(const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
-                   int64_t v_hs, const void *slots, int slot_bits, const void *cache, int64_t T,
-                   int64_t HK, int64_t D) {
+                   int64_t v_hs, const void *slots, int slot_bits, const void *cache) {
   if (!k || !v || !slots || !cache) return FP8BQ_ERR_NULL;
-  if (T * HK > ((int64_t(1) << 31) - 1) / (D / 8) * 256) return FP8BQ_ERR_SHAPE;  // the grid
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, slot_bits / 8) ||
       ((k_ts | k_hs | v_ts | v_hs) & 7))
     return FP8BQ_ERR_ALIGN;
@@ -1050,7 +1048,7 @@ int fp8bq_kv4_append(const void *k, int64_t k_ts, int64_t k_hs, const void *v, i
   RETURN_IF(check_kv4_sizes(pages, page, HK, D));
   if (slot_bits != 32 && slot_bits != 64) return FP8BQ_ERR_UNSUPPORTED;
   if (T == 0) return FP8BQ_OK;
-  RETURN_IF(check_kv4_rows(k, k_ts, k_hs, v, v_ts, v_hs, slots, slot_bits, cache, T, HK, D));
+  RETURN_IF(check_kv4_rows(k, k_ts, k_hs, v, v_ts, v_hs, slots, slot_bits, cache));
   if (!aligned(weights, 4)) return FP8BQ_ERR_ALIGN;
   DeviceInfo dev;
   RETURN_IF(device_info(&dev));
@@ -1072,7 +1070,7 @@ int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, const void *s
   RETURN_IF(check_kv4_sizes(pages, page, HK, D));
   if (slot_bits != 32 && slot_bits != 64) return FP8BQ_ERR_UNSUPPORTED;
   if (T == 0) return FP8BQ_OK;
-  RETURN_IF(check_kv4_rows(k, k_ts, k_hs, v, v_ts, v_hs, slots, slot_bits, cache, T, HK, D));
+  RETURN_IF(check_kv4_rows(k, k_ts, k_hs, v, v_ts, v_hs, slots, slot_bits, cache));
   if (rows_overlap(T, HK, D, k_ts, k_hs) || rows_overlap(T, HK, D, v_ts, v_hs)) return FP8BQ_ERR_SHAPE;
   DeviceInfo dev;
   RETURN_IF(device_info(&dev));
@@ -1136,8 +1134,7 @@ int fp8bq_kv4_evict(void *cache, int64_t pages, int64_t page, const int32_t *tab
   constexpr int64_t kMax = int64_t(1) << 28;
   if (B < 0 || B > kKv4MaxBatch || width < 0 || width > kMax || width * page > kMax || budget < 1 ||
       budget > kMax || recent < 0 || recent > budget || new_width > kMax ||
-      new_width < (budget + page - 1) / page ||
-      B * HK * budget > ((int64_t(1) << 31) - 1) / (D / 16) * 256)
+      new_width < (budget + page - 1) / page)
     return FP8BQ_ERR_SHAPE;
   if (B == 0) return FP8BQ_OK;
   if (!cache || (width > 0 && !table) || !lens || !weights || !new_table || !new_lens || !kept)

@@ -27,7 +27,7 @@ constexpr int kWarps = 4;       // consumer warps
 constexpr int kThreads = kWarps * 32 + 32;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -45,6 +45,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+constexpr float kGrowth = 8.0f;  // log2: how far a score may pass a row's reference
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -67,7 +69,8 @@ struct Sizes {
   static constexpr int kCtas = NB == 1 && D <= 128 ? 3 : D == 256 && NB == 2 ? 1 : 2;  // an SM
 };
 
-// Where a CTA is in the flattened list of tiles: sequence, item of it, tile.
+// Where a CTA is in the flattened list of slots: sequence, item of it, slot of the
+// item (its tiles first).
 struct Place {
   int b, item, tile, tiles;  // tiles: of each of the sequence's items
 };
@@ -78,51 +81,53 @@ struct Bars {
   uint32_t pages[4];  // which pages of a stage's tile are there
 };
 
-// The tiles of the batch: sequence b has those of its length for each of its HK *
-// blocks items; first[b] counts those of one item before b.  Every CTA takes an
-// equal run of the whole list (the first `more` of them one tile more), so that
-// ragged batches fill the device evenly.
+// The work of the batch as a list of slots: an item's tiles, and kJoinSlots more for
+// what an item costs besides (its queries, the join of the warps' sums).  first[b]
+// counts those of one item of each sequence before b.  Every CTA takes an equal run
+// of the whole list (the first `more` of them one slot more), so that ragged batches
+// fill the device evenly (64 sequences of 512 to 8192 tokens, 64 heads over 8: 64 us
+// with no slots for the joins, 58.1, 56.0 and 56.7 with one, two and three).
+constexpr int kJoinSlots = 2;
 struct Plan {
   const int *first;  // [B + 1]
   int B, items;      // items a sequence: HK * blocks
-  int each, more;    // tiles a CTA, and CTAs with one more
+  int each, more;    // slots a CTA, and CTAs with one more
   __device__ Plan(const int *f, int B_, int items_) : first(f), B(B_), items(items_) {
     const int total = f[B_] * items_;
-    // fewer CTAs than the grid has take part where there are fewer tiles
+    // fewer CTAs than the grid has take part where there are fewer slots
     const int ctas = min(max(total, 1), static_cast<int>(gridDim.x));
     each = total / ctas;
     more = total - each * ctas;
-    if (total == 0) each = 0;
   }
   __device__ int total() const { return first[B] * items; }
   __device__ int start(int cta) const { return min(total(), cta * each + min(cta, more)); }
-  __device__ int cta_of(int tile) const {
+  __device__ int cta_of(int slot) const {
     const int longer = more * (each + 1);
-    return tile < longer ? tile / (each + 1) : more + (tile - longer) / each;
+    return slot < longer ? slot / (each + 1) : more + (slot - longer) / each;
   }
   __device__ Place at(int f) const {
-    int lo = 0, hi = B;  // the last b with first[b] * items <= f that has tiles
+    int lo = 0, hi = B;  // the last b with first[b] * items <= f, which has slots
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (first[mid] * items <= f) lo = mid; else hi = mid;
     }
     Place p;
     p.b = lo;
-    p.tiles = first[lo + 1] - first[lo];
-    const int in = f - first[lo] * items;
-    p.item = in / p.tiles;
-    p.tile = in - p.item * p.tiles;
+    const int slots = first[lo + 1] - first[lo], in = f - first[lo] * items;
+    p.tiles = slots - kJoinSlots;
+    p.item = in / slots;
+    p.tile = in - p.item * slots;
     return p;
   }
   __device__ void next(Place &p) const {
-    if (++p.tile < p.tiles) return;
+    if (++p.tile < p.tiles + kJoinSlots) return;
     p.tile = 0;
     if (++p.item < items) return;
     p.item = 0;
     do {
       ++p.b;
     } while (p.b < B && first[p.b + 1] == first[p.b]);
-    if (p.b < B) p.tiles = first[p.b + 1] - first[p.b];
+    if (p.b < B) p.tiles = first[p.b + 1] - first[p.b] - kJoinSlots;
   }
 };
 
@@ -152,7 +157,10 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
   const int R = a.G * a.Tq, blocks = (R + kRows - 1) / kRows;
   const Kv4Page pg = kv4_page(P, D);
   auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), a.max_len); };
-  for (int b = tid; b < a.B; b += kThreads) first[b + 1] = (length(b) + kTile - 1) / kTile;
+  for (int b = tid; b < a.B; b += kThreads) {
+    const int tiles = (length(b) + kTile - 1) / kTile;
+    first[b + 1] = tiles ? tiles + kJoinSlots : 0;
+  }
   if (tid == 0) first[0] = 0;
   __syncthreads();
   if (warp == 0) {
@@ -180,14 +188,18 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     const int per_tile = kTile >> a.page_log2;
     auto look_up = [&]() -> int {  // this lane's page of tile p, -1 where there is none
       const int at = p.tile * per_tile + lane;
-      if (lane >= per_tile || (at << a.page_log2) >= length(p.b)) return -1;
+      if (p.tile >= p.tiles || lane >= per_tile || (at << a.page_log2) >= length(p.b)) return -1;
       const int page = __ldg(a.table + static_cast<int64_t>(p.b) * a.width + at);
       return page < a.pages ? page : -1;
     };
     int page = f0 < f1 ? look_up() : -1;
-    int st = 0, ph = 1;
-    int f = f0;
-    for (; f < f1; ++f) {
+    int st = 0, ph = 1, filled = 0;
+    for (int f = f0; f < f1; ++f) {
+      if (p.tile >= p.tiles) {
+        plan.next(p);
+        if (f + 1 < f1) page = look_up();
+        continue;
+      }
       const int head = p.item / blocks, row = (p.item - head * blocks) * kRows + lane;
       const bool q_too = f == f0 || p.tile == 0;
       const bool q_on = q_too && lane < kRows && row < R;
@@ -207,19 +219,18 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
                          static_cast<int64_t>(head * a.G + row - i * a.G) * a.q_hs,
                      D * 2, &bars.full[st]);
       }
-      if (on && !(a.fault && blockIdx.x == 0 && f == f0))
+      if (on && !(a.fault && blockIdx.x == 0 && filled == 0))
         bulk_load_1d(smem + st * S::kStageBytes + lane * pg.bytes,
                      a.cache + (static_cast<int64_t>(page) * a.HK + head) * pg.bytes, pg.bytes,
                      &bars.full[st]);
       if (++st == kStages) st = 0, ph ^= 1;
-      if (f + 1 < f1) {
-        plan.next(p);
-        page = look_up();
-      }
+      ++filled;
+      plan.next(p);
+      if (f + 1 < f1) page = look_up();
     }
     if (*abort) {  // copies in flight land before the memory is given up
-      for (int k = max(f - kStages, f0); k < f; ++k)
-        mbar_wait(&bars.full[(k - f0) % kStages], (k - f0) / kStages & 1, &bars.never, a.wait_limit_ns);
+      for (int k = max(filled - kStages, 0); k < filled; ++k)
+        mbar_wait(&bars.full[k % kStages], k / kStages & 1, &bars.never, a.wait_limit_ns);
     }
   } else {
     const int g = lane >> 2, t = lane & 3;
@@ -256,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
               make_float2(m[c], l[c]);
       }
     };
-    for (int f = f0; f < f1; ++f) {
+    for (int f = f0; f < f1; ++f, plan.next(p)) {
+      if (p.tile >= p.tiles) continue;
       // (after a wait that gave up the walk goes on, over whatever the memory holds,
       // so that no warp leaves the others at a barrier)
       mbar_wait(&bars.full[st], ph, abort, a.wait_limit_ns);
@@ -289,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
           const int e = top >> 7;
           const int up = e == 255 ? 0 : 14 + 127 - max(e, 24);
           const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale_log2;
+          // (never 0: -inf times it has to stay -inf)
+          const float back = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale_log2, 1.2e-38f);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             qs[nb][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + c) * 4);
@@ -312,11 +325,12 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         }
       }
       const int tok0 = p.tile * kTile + warp * (16 * kMB);
-      const uint32_t there = __shfl_sync(0xFFFFFFFFu, bars.pages[st], 0);
+      const uint32_t there = bars.pages[st];
       const int per_tile = kTile >> a.page_log2;
       // every token of the warp's seen by every row, and the pages there
       const int seen_by_all = len - (a.Tq - 1);
-      const bool whole = tok0 + 16 * kMB <= seen_by_all && there == (1u << per_tile) - 1u;
+      const bool whole = __all_sync(
+          0xFFFFFFFFu, tok0 + 16 * kMB <= seen_by_all && there == (1u << per_tile) - 1u);
       auto block_of = [&](int mb, int &in) {  // page of the warp's 16-token block, place in it
         const int at = (warp * kMB + mb) * 16;
         in = at & (P - 1);
@@ -374,15 +388,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
             }
           }
         }
-        // ---- log2 units; what a row may not see goes to -inf
-        if (whole) {
-#pragma unroll
-          for (int mb = 0; mb < kMB; ++mb)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) s[mb][nb][c] *= qs[nb][c & 1];
-        } else {
+        // ---- what a row may not see goes to -inf
+        if (!whole) {
 #pragma unroll
           for (int mb = 0; mb < kMB; ++mb) {
             const bool here = there >> ((warp * kMB + mb) * 16 >> a.page_log2) & 1u;
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int tok = tok0 + mb * 16 + key_row + (c >> 1) * 8;
-                s[mb][nb][c] = here && tok < ends[nb][c & 1] ? s[mb][nb][c] * qs[nb][c & 1] : -INFINITY;
+                if (!here || tok >= ends[nb][c & 1]) s[mb][nb][c] = -INFINITY;
               }
           }
         }
@@ -405,59 +412,101 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
                 const int r = row0 + nb * 8 + 2 * t + (c & 1);
                 const int tok = tok0 + mb * 16 + key_row + (c >> 1) * 8;
                 if (r < R && tok < a.max_len)
-                  a.logits[((static_cast<int64_t>(p.b) * a.HK + head) * R + r) * a.max_len + tok] = s[mb][nb][c];
+                  a.logits[((static_cast<int64_t>(p.b) * a.HK + head) * R + r) * a.max_len + tok] =
+                      s[mb][nb][c] * qs[nb][c & 1];
               }
         }
-        // ---- the running maximum; what was summed before follows it
+        // ---- the reference that p is held to: a score of the row that no other has
+        // passed by more than 8 in log2 units (p <= 2^8); what was summed follows it.
+        // (The difference is taken before the scale, so that it is exact where it is
+        // small, however large the scores are.)
         bool grew = false;
-        float fix[NB][2];
+        float lm[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = fmaxf(s[0][nb][c], s[0][nb][c + 2]);
+            lm[nb][c] = fmaxf(s[0][nb][c], s[0][nb][c + 2]);
 #pragma unroll
-            for (int mb = 1; mb < kMB; ++mb) m = fmaxf(m, fmaxf(s[mb][nb][c], s[mb][nb][c + 2]));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-            m = fmaxf(m, mx[nb][c]);
-            fix[nb][c] = m > mx[nb][c] ? ex2(mx[nb][c] - m) : 1.0f;
-            grew |= m > mx[nb][c];
-            mx[nb][c] = m;
+            for (int mb = 1; mb < kMB; ++mb) lm[nb][c] = fmaxf(lm[nb][c], fmaxf(s[mb][nb][c], s[mb][nb][c + 2]));
+            grew |= (lm[nb][c] - mx[nb][c]) * qs[nb][c] > kGrowth;
           }
         if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            sum[nb][0] *= fix[nb][0], sum[nb][1] *= fix[nb][1];
+            float fix[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float m = lm[nb][c];
+              m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+              const bool up = (m - mx[nb][c]) * qs[nb][c] > kGrowth;
+              fix[c] = up ? ex2((mx[nb][c] - m) * qs[nb][c]) : 1.0f;
+              if (up) mx[nb][c] = m;
+              sum[nb][c] *= fix[c];
+            }
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) o[j][nb][c] *= fix[nb][c & 1];
+              for (int c = 0; c < 4; ++c) o[j][nb][c] *= fix[c & 1];
           }
         }
         // ---- p, and its fragments for the second product: rows become columns
         uint32_t pf[kMB][NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float m0 = mx[nb][0] == -INFINITY ? 0.0f : mx[nb][0];
-          const float m1 = mx[nb][1] == -INFINITY ? 0.0f : mx[nb][1];
+          // (a row that has seen nothing: -inf - 0)
+          const uint64_t ref = pair(mx[nb][0] == -INFINITY ? 0.0f : -mx[nb][0],
+                                    mx[nb][1] == -INFINITY ? 0.0f : -mx[nb][1]);
+          const uint64_t by = pair(qs[nb][0], qs[nb][1]);
 #pragma unroll
           for (int mb = 0; mb < kMB; ++mb) {
-            const float p0 = ex2(s[mb][nb][0] - m0), p1 = ex2(s[mb][nb][1] - m1);
-            const float p2 = ex2(s[mb][nb][2] - m0), p3 = ex2(s[mb][nb][3] - m1);
+            float p0, p1, p2, p3;
+            unpair(mul2(add2(pair(s[mb][nb][0], s[mb][nb][1]), ref), by), p0, p1);
+            unpair(mul2(add2(pair(s[mb][nb][2], s[mb][nb][3]), ref), by), p2, p3);
+            p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
             sum[nb][0] += p0 + p2, sum[nb][1] += p1 + p3;
             pf[mb][nb][0] = transpose8x8(pack_f16(p0, p1));
             pf[mb][nb][1] = transpose8x8(pack_f16(p2, p3));
           }
         }
-        // ---- p times the values
+        // ---- p times the values.  Those of tokens that no row may see count as 0,
+        // whatever their bytes hold; a NaN that some rows see goes to those rows alone.
+        auto seen_scales = [&](uint32_t b, int r, int mb) -> uint32_t {
+          const bool here = there >> ((warp * kMB + mb) * 16 >> a.page_log2) & 1u;
+          const int base = tok0 + mb * 16 + r * 8, tok = base + key_row;
+          if (!here || tok >= len) b = 0;
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            const bool bad = (b >> (8 * k) & 0x7Fu) == kE4m3Nan && tok >= seen_by_all;
+            if (bad) b &= ~(0xFFu << (8 * k));
+            for (uint32_t who = __ballot_sync(0xFFFFFFFFu, bad); who; who &= who - 1) {
+              const int from = __ffs(who) - 1, fg = from >> 2;
+              const int group = (from & 3) * (D / 64) + k, other = base + (fg >> 1) + (fg & 1) * 4;
+              // this lane's values are D/8 from g * D/8 on
+              constexpr int kPer = D == 256 ? 2 : 1;
+#pragma unroll
+              for (int w = 0; w < kPer; ++w) {
+                if (group != (D == 64 ? g >> 1 : g * kPer + w)) continue;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    if (other < ends[nb][c])
+#pragma unroll
+                      for (int j = w * (kTiles / kPer); j < (w + 1) * (kTiles / kPer); ++j)
+                        o[j][nb][c] = o[j][nb][c + 2] = NAN;
+              }
+            }
+          }
+          return b;
+        };
 #pragma unroll
         for (int mb = 0; mb < kMB; ++mb) {
           int in;
           const uint8_t *page = block_of(mb, in);
           uint32_t w[4][kValueWords];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the products' order
-          uint32_t sb[4];              // their scale bytes (two groups for D == 256)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = in + t + r * 4;
@@ -471,48 +520,29 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
               const uint4 v = *reinterpret_cast<const uint4 *>(codes);
               w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
             }
-            const uint8_t *scales = page + pg.v_scales + row * (D / 16);
-            if constexpr (D == 256) sb[r] = *reinterpret_cast<const uint16_t *>(scales + 2 * g);
-            else sb[r] = scales[D == 128 ? g : g >> 1];
           }
-          if (!whole) {
-            // values of tokens that no row may see count as 0 whatever their bytes
-            // hold; a NaN that some rows see goes to those rows alone
-            const bool here = there >> ((warp * kMB + mb) * 16 >> a.page_log2) & 1u;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int tok = tok0 + mb * 16 + t + r * 4;
-              if (!here || tok >= len) sb[r] = 0;
-              constexpr int kGroups = D == 256 ? 2 : 1;  // groups of this lane's values
-#pragma unroll
-              for (int k = 0; k < kGroups; ++k) {
-                const uint32_t one = sb[r] >> (8 * k) & 0xFFu;
-                const bool bad = (one & 0x7Fu) == kE4m3Nan && tok >= seen_by_all;
-                if (bad) sb[r] &= ~(0xFFu << (8 * k));
-                const uint32_t who = __ballot_sync(0xFFFFFFFFu, bad);
-                if (who == 0) continue;
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {  // the lanes of the same values, other tokens
-                  if (!(who >> (g * 4 + tt) & 1u)) continue;
-                  const int other = tok0 + mb * 16 + tt + r * 4;
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                      if (other < ends[nb][c])
-#pragma unroll
-                        for (int j = k * (kTiles / kGroups); j < (k + 1) * (kTiles / kGroups); ++j)
-                          o[j][nb][c] = o[j][nb][c + 2] = NAN;
-                }
-              }
-            }
-          }
+          // the tokens' scales: a lane has those of one of 8 tokens for two columns of
+          // lanes (its own of the key scales' pattern), and gets those of two tokens for
+          // its own by a transposition
           constexpr int kScales = D == 256 ? 2 : 1;
-          uint32_t sv[2][kScales];  // scales of tokens 2t, 2t+1 | 2t+8, 2t+9
+          uint32_t sv[2][kScales];  // of tokens 2t, 2t+1 | 2t+8, 2t+9
 #pragma unroll
-          for (int k = 0; k < kScales; ++k) {
-            sv[0][k] = e4m3x2_to_f16((sb[0] >> (8 * k) & 0xFFu) | (sb[1] >> (8 * k) & 0xFFu) << 8);
-            sv[1][k] = e4m3x2_to_f16((sb[2] >> (8 * k) & 0xFFu) | (sb[3] >> (8 * k) & 0xFFu) << 8);
+          for (int r = 0; r < 2; ++r) {
+            const int row = in + key_row + r * 8;
+            const uint8_t *scales = page + pg.v_scales + row * (D / 16) + t * (D / 64);
+            uint32_t b = D == 64    ? *scales
+                         : D == 128 ? *reinterpret_cast<const uint16_t *>(scales)
+                                    : *reinterpret_cast<const uint32_t *>(scales);
+            if (!whole) b = seen_scales(b, r, mb);
+            if constexpr (D == 64) {
+              sv[r][0] = transpose8x8(both_low(e4m3x2_to_f16(b)));
+            } else if constexpr (D == 128) {
+              sv[r][0] = transpose8x8(e4m3x2_to_f16(b));
+            } else {
+              const uint32_t lo = e4m3x2_to_f16(b & 0xFFFFu), hi = e4m3x2_to_f16(b >> 16);
+              sv[r][0] = transpose8x8(__byte_perm(lo, hi, 0x5410));
+              sv[r][1] = transpose8x8(__byte_perm(lo, hi, 0x7632));
+            }
           }
 #pragma unroll
           for (int i = 0; i < kValueWords; ++i) {
@@ -553,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            if (g == 0) join_stat[warp * kRows + nb * 8 + 2 * t + c] = make_float2(mx[nb][c], l);
+            if (g == 0) join_stat[warp * kRows + nb * 8 + 2 * t + c] = make_float2(mx[nb][c] * qs[nb][c], l);
           }
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
@@ -618,7 +648,6 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
           else early = p, has_early = true;
         }
       }
-      if (f + 1 < f1) plan.next(p);
     }
     // ---- items that other CTAs have parts of: the last to leave its part sums all of
     // them, in the order of the tokens
@@ -628,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
       for (int n = 0; n < 2; ++n) {
         if (!(n ? has_late : has_early)) continue;
         const Place &e = n ? late : early;
-        const int s0 = first[e.b] * plan.items + e.item * e.tiles;
+        const int s0 = first[e.b] * plan.items + e.item * (e.tiles + kJoinSlots);
         const int c0 = plan.cta_of(s0), c1 = plan.cta_of(s0 + e.tiles - 1);
         if (bars.ticket[n] != static_cast<uint32_t>(c1 - c0)) continue;
         if (tid == 0) a.tickets[e.b * plan.items + e.item] = 0u;

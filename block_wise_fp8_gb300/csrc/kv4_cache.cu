@@ -30,120 +30,138 @@ __device__ __forceinline__ Slot slot_of(const void *slots, int is64, int64_t t, 
   return r;
 }
 
-// ---------------------------------------------------------------- append
+// ---------------------------------------------------------------- append and read
+//
+// Both are bound by HBM: 4D bytes of rows and 9D/8 of a page a token and head.  A
+// thread has 8 values (half a group): rows, codes and scales are then whole runs of a
+// warp's lanes (with whole groups a thread 8192 tokens x 8 heads x 128 took 15 us to
+// write and 12 to read, cold), and kRowTokens tokens, whose loads are in flight
+// together.
+constexpr int kRowTokens = 4;
 
-// A thread quantises one group: 32 bytes in, 8 bytes of codes and a scale out; a
-// row's groups are neighbouring threads.  Bound by HBM (4D bytes a token and head
-// in, 9D/8 out).
+template <int D>
+struct RowPlace {
+  static constexpr int kLanes = D / 4;               // threads a token: keys, then values
+  static constexpr int kTokens = kRowThreads / kLanes;  // tokens at a time
+  int in, kv, piece;                                 // token of those, values?, run of 8 values
+  __device__ RowPlace() : in(threadIdx.x / kLanes) {
+    const int x = threadIdx.x % kLanes;
+    kv = x >= D / 8;
+    piece = x % (D / 8);
+  }
+  __device__ int64_t token(int u) const {
+    return (static_cast<int64_t>(blockIdx.x) * kRowTokens + u) * kTokens + in;
+  }
+};
+
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int groups = a.D / 16;
-  const int64_t per_token = static_cast<int64_t>(a.HK) * 2 * groups;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  const int64_t t = i / per_token;
-  if (t >= a.T) return;
-  const int in_token = static_cast<int>(i - t * per_token);
-  const int g = in_token % groups, kv = in_token / groups % 2, h = in_token / groups / 2;
-  const Slot s = slot_of(a.slots, a.slots64, t, a.pages, a.page_log2);
-  if (!s.on) return;
-  const uint16_t *x = (kv ? a.v + t * a.v_ts + h * a.v_hs : a.k + t * a.k_ts + h * a.k_hs) + g * 16;
-  const float inv = kv ? a.v_inv : a.k_inv;
-  uint32_t w[8];
-  {
-    const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(x));
-    const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
-    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
-    w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+  const RowPlace<D> at;
+  const int h = blockIdx.y;
+  const Kv4Page p = kv4_page(1 << a.page_log2, D);
+  const uint16_t *x = (at.kv ? a.v + h * a.v_hs : a.k + h * a.k_hs) + at.piece * 8;
+  const int64_t ts = at.kv ? a.v_ts : a.k_ts;
+  const float inv = at.kv ? a.v_inv : a.k_inv;
+  Slot s[kRowTokens];
+  uint4 w[kRowTokens];
+#pragma unroll
+  for (int u = 0; u < kRowTokens; ++u) {
+    const int64_t t = at.token(u);
+    s[u].on = false;
+    if (t < a.T) s[u] = slot_of(a.slots, a.slots64, t, a.pages, a.page_log2);
+    w[u] = t < a.T ? __ldg(reinterpret_cast<const uint4 *>(x + t * ts)) : make_uint4(0, 0, 0, 0);
   }
-  // BF16 magnitudes are ordered as their bits are, infinity and then NaN on top
-  uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
-  top = max(top & 0xFFFFu, top >> 16);
-  const float amax = __uint_as_float(top << 16) * inv;
-  uint32_t sb;  // RNE, saturating at 448
-  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %1, %2;\n\tcvt.u32.u16 %0, h;\n\t}"
-      : "=r"(sb)
-      : "f"(0.0f), "f"(__fdiv_rn(amax, kE2m1Max)));
-  sb = max(sb & 0xFFu, 1u);
-  const bool nan = top > 0x7F80u;
-  if (nan) sb = kE4m3Nan;
-  // the scale as binary32: four significant bits, so that q below is the nearest to
-  // the exact quotient after one correction (Markstein), and no tie is moved
-  const uint32_t e = sb >> 3, m = sb & 7u;
-  const float sv = e ? __uint_as_float((e + 120u) << 23 | m << 20) : static_cast<float>(m) * kE4m3Least;
-  const float r = __fdiv_rn(1.0f, sv);
-  auto quotient = [&](float v) {
-    v = fminf(fmaxf(v * inv, -4096.0f), 4096.0f);  // more than 6 * 448: infinities too
-    const float q = v * r;
-    return copysignf(__fmaf_rn(__fmaf_rn(-sv, q, v), r, q), v);  // -0 stays -0
-  };
-  uint32_t codes[2];
+  for (int u = 0; u < kRowTokens; ++u) {
+    const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+    // BF16 magnitudes are ordered as their bits are, infinity and then NaN on top
+    uint32_t top = 0;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+    for (int j = 0; j < 4; ++j) top = __vmaxu2(top, v[j] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    const float amax = __uint_as_float(top << 16) * inv;
+    uint32_t sb;  // RNE, saturating at 448
+    asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %1, %2;\n\tcvt.u32.u16 %0, h;\n\t}"
+        : "=r"(sb)
+        : "f"(0.0f), "f"(__fdiv_rn(amax, kE2m1Max)));
+    sb = max(sb & 0xFFu, 1u);
+    const bool nan = top > 0x7F80u;
+    if (nan) sb = kE4m3Nan;
+    // the scale as binary32: four significant bits, so that q below is the nearest to
+    // the exact quotient after one correction (Markstein), and no tie is moved
+    const uint32_t e = sb >> 3, m = sb & 7u;
+    const float sv = e ? __uint_as_float((e + 120u) << 23 | m << 20) : static_cast<float>(m) * kE4m3Least;
+    const float r = __fdiv_rn(1.0f, sv);
+    auto quotient = [&](float y) {
+      y = fminf(fmaxf(y * inv, -4096.0f), 4096.0f);  // more than 6 * 448: infinities too
+      const float q = y * r;
+      return copysignf(__fmaf_rn(__fmaf_rn(-sv, q, y), r, q), y);  // -0 stays -0
+    };
     uint32_t c = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t two = w[half * 4 + j];
       uint32_t b;
       asm("{\n\t.reg .b8 p;\n\t.reg .b8 z;\n\tmov.b16 {z, p}, 0;\n\t"
           "cvt.rn.satfinite.e2m1x2.f32 p, %1, %2;\n\tmov.b32 %0, {p, z, z, z};\n\t}"
           : "=r"(b)
-          : "f"(quotient(__uint_as_float(two & 0xFFFF0000u))), "f"(quotient(__uint_as_float(two << 16))));
+          : "f"(quotient(__uint_as_float(v[j] & 0xFFFF0000u))), "f"(quotient(__uint_as_float(v[j] << 16))));
       c |= b << (8 * j);
     }
-    codes[half] = nan ? 0u : c;
+    if (!s[u].on) continue;
+    uint8_t *page = a.cache + (s[u].page * a.HK + h) * p.bytes;
+    *reinterpret_cast<uint32_t *>(page + (at.kv ? p.v_codes : 0) + s[u].at * p.code_bytes + at.piece * 4) =
+        nan ? 0u : c;
+    if ((at.piece & 1) == 0)
+      page[(at.kv ? p.v_scales : p.k_scales) + s[u].at * p.scale_bytes + at.piece / 2] = static_cast<uint8_t>(sb);
+    if (a.weights && at.kv == 0 && at.piece == 0)
+      a.weights[((s[u].page * a.HK + h) << a.page_log2) + s[u].at] = 0.0f;
   }
-  const Kv4Page p = kv4_page(1 << a.page_log2, a.D);
-  uint8_t *page = a.cache + (s.page * a.HK + h) * p.bytes;
-  uint8_t *row = page + (kv ? p.v_codes : 0) + s.at * p.code_bytes;
-  *reinterpret_cast<uint2 *>(row + g * 8) = make_uint2(codes[0], codes[1]);
-  page[(kv ? p.v_scales : p.k_scales) + s.at * p.scale_bytes + g] = static_cast<uint8_t>(sb);
-  if (a.weights && kv == 0 && g == 0)
-    a.weights[((s.page * a.HK + h) << a.page_log2) + s.at] = 0.0f;
 }
 
-// ---------------------------------------------------------------- read
-
-// A thread reads one group back: 9 bytes in, 32 out.
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int groups = a.D / 16;
-  const int64_t per_token = static_cast<int64_t>(a.HK) * 2 * groups;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  const int64_t t = i / per_token;
-  if (t >= a.T) return;
-  const int in_token = static_cast<int>(i - t * per_token);
-  const int g = in_token % groups, kv = in_token / groups % 2, h = in_token / groups / 2;
-  const Slot s = slot_of(a.slots, a.slots64, t, a.pages, a.page_log2);
-  if (!s.on) return;
-  const Kv4Page p = kv4_page(1 << a.page_log2, a.D);
-  const uint8_t *page = a.cache + (s.page * a.HK + h) * p.bytes;
-  const uint2 c = *reinterpret_cast<const uint2 *>(page + (kv ? p.v_codes : 0) +
-                                                   s.at * p.code_bytes + g * 8);
-  const uint32_t sc =
-      both_low(e4m3x2_to_f16(page[(kv ? p.v_scales : p.k_scales) + s.at * p.scale_bytes + g]));
-  const float gs = kv ? a.v_scale : a.k_scale;
-  uint32_t out[8];
+  const RowPlace<D> at;
+  const int h = blockIdx.y;
+  const Kv4Page p = kv4_page(1 << a.page_log2, D);
+  uint16_t *y = (at.kv ? a.v + h * a.v_hs : a.k + h * a.k_hs) + at.piece * 8;
+  const int64_t ts = at.kv ? a.v_ts : a.k_ts;
+  const float gs = at.kv ? a.v_scale : a.k_scale;
+  bool on[kRowTokens];
+  uint32_t c[kRowTokens], sc[kRowTokens];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t f[4];
-    e2m1x8_to_f16(half ? c.y : c.x, f);
+  for (int u = 0; u < kRowTokens; ++u) {
+    const int64_t t = at.token(u);
+    on[u] = false;
+    if (t >= a.T) continue;
+    const Slot s = slot_of(a.slots, a.slots64, t, a.pages, a.page_log2);
+    on[u] = s.on;
+    if (!s.on) continue;
+    const uint8_t *page = a.cache + (s.page * a.HK + h) * p.bytes;
+    c[u] = *reinterpret_cast<const uint32_t *>(page + (at.kv ? p.v_codes : 0) + s.at * p.code_bytes + at.piece * 4);
+    sc[u] = page[(at.kv ? p.v_scales : p.k_scales) + s.at * p.scale_bytes + at.piece / 2];
+  }
+#pragma unroll
+  for (int u = 0; u < kRowTokens; ++u) {
+    if (!on[u]) continue;
+    const uint32_t scale = both_low(e4m3x2_to_f16(sc[u]));
+    uint32_t f[4], out[4];
+    e2m1x8_to_f16(c[u], f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float lo, hi;
       asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
           "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
           : "=f"(lo), "=f"(hi)
-          : "r"(hmul2(f[j], sc)));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[half * 4 + j]) : "f"(hi * gs), "f"(lo * gs));
+          : "r"(hmul2(f[j], scale)));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[j]) : "f"(hi * gs), "f"(lo * gs));
     }
+    *reinterpret_cast<uint4 *>(y + at.token(u) * ts) = make_uint4(out[0], out[1], out[2], out[3]);
   }
-  uint16_t *y = (kv ? a.v + t * a.v_ts + h * a.v_hs : a.k + t * a.k_ts + h * a.k_hs) + g * 16;
-  reinterpret_cast<uint4 *>(y)[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  reinterpret_cast<uint4 *>(y)[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 // ---------------------------------------------------------------- evict: the choice
@@ -151,6 +169,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
 constexpr int kChooseThreads = 1024;
 constexpr int kChooseWarps = kChooseThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kBinCopies = 4;           // counts of every fourth lane: weights are close together
 constexpr int kKeysCached = 40 * 1024;  // keys kept in shared memory (160 KB)
 
 // Weights in the order of whole numbers: NaN below everything, -0 as 0.
@@ -164,10 +183,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // m = n - recent weights: their smallest key by a radix selection (11 + 11 + 10
 // bits), of the keys equal to it the first ones.  A warp then has a run of the
 // tokens of its own, so that one exchange between the warps numbers them all in
-// order.  Latency of one CTA: a gather of n weights, three counts, two walks.
+// order.  Latency of one CTA: a gather of n weights, three counts, two walks (2203
+// tokens: 18 us with one warp looking for the bin, 64 bins a lane).
 __global__ void __launch_bounds__(kChooseThreads) kv4_choose_kernel(const Kv4EvictArgs a) {
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t bins[kBins];
+  __shared__ uint32_t bins[kBinCopies][kBins];
   __shared__ uint32_t sums[2][kChooseWarps];
   __shared__ uint32_t s_prefix, s_left;
   griddep_launch_dependents();
@@ -189,8 +209,10 @@ __global__ void __launch_bounds__(kChooseThreads) kv4_choose_kernel(const Kv4Evi
     return weight_key(a.weights[((static_cast<int64_t>(pg) * a.HK + h) << a.page_log2) + (i & (P - 1))]);
   };
   const bool cached = m <= kKeysCached;
-  if (cached)
+  if (cached) {
+#pragma unroll 4
     for (int i = tid; i < m; i += kChooseThreads) keys[i] = key_at(i);
+  }
   auto key = [&](int i) { return cached ? keys[i] : key_at(i); };
   // the key of the heavy-th largest, and how many of the keys equal to it are taken
   uint32_t prefix = 0, left = static_cast<uint32_t>(heavy);
@@ -201,31 +223,33 @@ __global__ void __launch_bounds__(kChooseThreads) kv4_choose_kernel(const Kv4Evi
       const int bits = pass == 2 ? 10 : 11;
       const int high = shift;  // bits above are settled
       shift -= bits;
-      for (int i = tid; i < kBins; i += kChooseThreads) bins[i] = 0;
+      for (int i = tid; i < kBins * kBinCopies; i += kChooseThreads) (&bins[0][0])[i] = 0;
       __syncthreads();
       for (int i = tid; i < m; i += kChooseThreads) {
         const uint32_t k = key(i);
-        if (pass == 0 || k >> high == prefix) atomicAdd(&bins[k >> shift & ((1u << bits) - 1)], 1u);
+        if (pass == 0 || k >> high == prefix)
+          atomicAdd(&bins[lane & (kBinCopies - 1)][k >> shift & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      if (warp == 0) {  // from the top: a lane has a run of bins
-        const int per = (1 << bits) / 32;
-        const int top = (1 << bits) - 1 - lane * per;
-        uint32_t mine = 0;
-        for (int j = 0; j < per; ++j) mine += bins[top - j];
-        uint32_t upto = mine;
+      // from the top bin down, two a thread: how many lie above, up to the wanted one
+      const int top = kBins - 1 - 2 * tid;
+      uint32_t n0 = 0, n1 = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-          if (lane >= d) upto += v;
-        }
-        uint32_t before = upto - mine;
-        if (before < left && left <= upto) {
-          int j = 0;
-          while (before + bins[top - j] < left) before += bins[top - j++];
-          s_prefix = prefix << bits | static_cast<uint32_t>(top - j);
-          s_left = left - before;
-        }
+      for (int c = 0; c < kBinCopies; ++c) n0 += bins[c][top], n1 += bins[c][top - 1];
+      uint32_t upto = n0 + n1;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      if (lane == 31) sums[0][warp] = upto;
+      __syncthreads();
+      upto += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[0][lane] : 0u);
+      const uint32_t above = upto - n0 - n1;
+      if (above < left && left <= upto) {  // one thread's
+        const bool second = above + n0 < left;
+        s_prefix = prefix << bits | static_cast<uint32_t>(top - second);
+        s_left = left - above - (second ? n0 : 0u);
       }
       __syncthreads();
       prefix = s_prefix, left = s_left;
@@ -265,60 +289,101 @@ __global__ void __launch_bounds__(kChooseThreads) kv4_choose_kernel(const Kv4Evi
 
 // ---------------------------------------------------------------- evict: the move
 
-// D/16 threads a kept token and head, 16 bytes of codes each; the first of the keys'
-// half also takes their scales, the first of the values' half theirs, the second
-// thread the weight.
+// A CTA moves kMoveRows kept tokens of a sequence and head: their old and new pages
+// are looked up once, then the 16-byte words of codes, the scales and the weights go
+// as whole runs of threads, several a thread in flight.  Bound by HBM: 2 x (9D/8 + 4)
+// bytes a token (with all of a word's indexes worked out by its own thread, 32
+// sequences of up to 4096 tokens x 8 heads took 104 us).
+constexpr int kMoveRows = 128;
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_move_kernel(const Kv4EvictArgs a) {
+  __shared__ int64_t from[kMoveRows], to[kMoveRows];  // byte offsets of key codes, -1: none
+  __shared__ int from_at[kMoveRows], to_at[kMoveRows];
   griddep_launch_dependents();
   griddep_wait();
-  const int parts = a.D / 16;  // 16-byte words of a row's codes, keys then values
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  const int64_t row = i / parts;  // (b, h, place)
-  if (row >= static_cast<int64_t>(a.B) * a.HK * a.budget) return;
-  const int part = static_cast<int>(i - row * parts);
-  const int j = static_cast<int>(row % a.budget);
-  const int64_t bh = row / a.budget;
-  const int h = static_cast<int>(bh % a.HK);
-  const int64_t b = bh / a.HK;
-  const int from = a.kept[row];
-  if (from < 0) return;
+  const int h = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * kMoveRows, tid = threadIdx.x;
   const int P = 1 << a.page_log2;
-  const int src = __ldg(a.table + b * a.width + (from >> a.page_log2));
-  const int dst = __ldg(a.new_table + b * a.new_width + (j >> a.page_log2));
-  if (src < 0 || src >= a.pages || dst < 0 || dst >= a.pages) return;
-  const Kv4Page p = kv4_page(P, a.D);
-  const uint8_t *sp = a.cache + (static_cast<int64_t>(src) * a.HK + h) * p.bytes;
-  uint8_t *dp = a.cache + (static_cast<int64_t>(dst) * a.HK + h) * p.bytes;
-  const int si = from & (P - 1), di = j & (P - 1);
-  const int half = parts / 2, kv = part >= half, word = part - kv * half;
-  const int codes = kv ? p.v_codes : 0;
-  *reinterpret_cast<uint4 *>(dp + codes + di * p.code_bytes + word * 16) =
-      *reinterpret_cast<const uint4 *>(sp + codes + si * p.code_bytes + word * 16);
-  if (word == 0) {
-    const uint8_t *ss = sp + (kv ? p.v_scales : p.k_scales) + si * p.scale_bytes;
-    uint8_t *ds = dp + (kv ? p.v_scales : p.k_scales) + di * p.scale_bytes;
-    for (int w = 0; w < p.scale_bytes / 4; ++w)
-      reinterpret_cast<uint32_t *>(ds)[w] = reinterpret_cast<const uint32_t *>(ss)[w];
+  const Kv4Page p = kv4_page(P, D);
+  if (tid < kMoveRows) {
+    const int j = j0 + tid;
+    int64_t f = -1, t = -1;
+    int fi = 0, ti = 0;
+    if (j < a.budget) {
+      const int k = a.kept[(static_cast<int64_t>(b) * a.HK + h) * a.budget + j];
+      if (k >= 0) {
+        const int src = __ldg(a.table + b * a.width + (k >> a.page_log2));
+        const int dst = __ldg(a.new_table + b * a.new_width + (j >> a.page_log2));
+        if (src >= 0 && src < a.pages && dst >= 0 && dst < a.pages) {
+          f = (static_cast<int64_t>(src) * a.HK + h), t = (static_cast<int64_t>(dst) * a.HK + h);
+          fi = k & (P - 1), ti = j & (P - 1);
+          a.weights[(t << a.page_log2) + ti] = a.weights[(f << a.page_log2) + fi];
+        }
+      }
+    }
+    from[tid] = f < 0 ? -1 : f * p.bytes, to[tid] = t * p.bytes;
+    from_at[tid] = fi, to_at[tid] = ti;
   }
-  if (part == 1)
-    a.weights[((static_cast<int64_t>(dst) * a.HK + h) << a.page_log2) + di] =
-        a.weights[((static_cast<int64_t>(src) * a.HK + h) << a.page_log2) + si];
+  __syncthreads();
+  constexpr int kWords = D / 16;  // 16-byte words of a token's codes, keys then values
+  constexpr int kEach = kMoveRows * kWords / kRowThreads;
+  uint4 w[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int i = u * kRowThreads + tid, r = i / kWords, x = i % kWords, kv = x >= kWords / 2;
+    if (from[r] >= 0)
+      w[u] = *reinterpret_cast<const uint4 *>(a.cache + from[r] + (kv ? p.v_codes : 0) +
+                                              from_at[r] * p.code_bytes + x % (kWords / 2) * 16);
+  }
+  // a token's scales, D/16 bytes of keys and of values: a thread each
+  const int r = tid % kMoveRows, kv = tid / kMoveRows;
+  uint32_t s[D / 64];
+  if (from[r] >= 0) {
+    const uint32_t *ss = reinterpret_cast<const uint32_t *>(
+        a.cache + from[r] + (kv ? p.v_scales : p.k_scales) + from_at[r] * p.scale_bytes);
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) s[x] = ss[x];
+  }
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int i = u * kRowThreads + tid, q = i / kWords, x = i % kWords, v = x >= kWords / 2;
+    if (from[q] >= 0)
+      *reinterpret_cast<uint4 *>(a.cache + to[q] + (v ? p.v_codes : 0) + to_at[q] * p.code_bytes +
+                                 x % (kWords / 2) * 16) = w[u];
+  }
+  if (from[r] >= 0) {
+    uint32_t *ds = reinterpret_cast<uint32_t *>(
+        a.cache + to[r] + (kv ? p.v_scales : p.k_scales) + to_at[r] * p.scale_bytes);
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) ds[x] = s[x];
+  }
 }
 
-unsigned blocks_of(int64_t threads) {
-  return static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads);
+// calls f(D as a constant)
+template <typename F>
+cudaError_t by_size(int D, F f) {
+  return D == 64    ? f(std::integral_constant<int, 64>{})
+         : D == 128 ? f(std::integral_constant<int, 128>{})
+                    : f(std::integral_constant<int, 256>{});
 }
+
+unsigned blocks_of(int64_t n, int each) { return static_cast<unsigned>((n + each - 1) / each); }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, cudaStream_t st) {
-  return launch_pdl(kv4_append_kernel, dim3(blocks_of(a.T * a.HK * (a.D / 8))), dim3(kRowThreads), 0,
-                    st, a);
+  return by_size(a.D, [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return launch_pdl(kv4_append_kernel<D>, dim3(blocks_of(a.T, RowPlace<D>::kTokens * kRowTokens), a.HK),
+                      dim3(kRowThreads), 0, st, a);
+  });
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs &a, cudaStream_t st) {
-  return launch_pdl(kv4_read_kernel, dim3(blocks_of(a.T * a.HK * (a.D / 8))), dim3(kRowThreads), 0,
-                    st, a);
+  return by_size(a.D, [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return launch_pdl(kv4_read_kernel<D>, dim3(blocks_of(a.T, RowPlace<D>::kTokens * kRowTokens), a.HK),
+                      dim3(kRowThreads), 0, st, a);
+  });
 }
 
 cudaError_t launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st) {
@@ -328,9 +393,10 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st) {
   const size_t smem = static_cast<size_t>(most <= 0 ? 0 : most < kKeysCached ? most : kKeysCached) * 4;
   e = launch_pdl(kv4_choose_kernel, dim3(a.HK, a.B), dim3(kChooseThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_move_kernel,
-                    dim3(blocks_of(static_cast<int64_t>(a.B) * a.HK * a.budget * (a.D / 16))),
-                    dim3(kRowThreads), 0, st, a);
+  return by_size(a.D, [&](auto d) {
+    return launch_pdl(kv4_move_kernel<decltype(d)::value>, dim3(blocks_of(a.budget, kMoveRows), a.HK, a.B),
+                      dim3(kRowThreads), 0, st, a);
+  });
 }
 
 }  // namespace fp8bq
