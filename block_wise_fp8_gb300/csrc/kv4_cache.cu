@@ -54,6 +54,13 @@ struct RowPlace {
   }
 };
 
+// RN(x / s) with r = RN(1 / s): one correction (Markstein).  No tie is moved, so that
+// what is rounded to fewer bits next is the exact quotient's.
+__device__ __forceinline__ float nearest_quotient(float x, float s, float r) {
+  const float q = x * r;
+  return __fmaf_rn(__fmaf_rn(-s, q, x), r, q);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   griddep_launch_dependents();
@@ -82,23 +89,24 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     for (int j = 0; j < 4; ++j) top = __vmaxu2(top, v[j] & 0x7FFF7FFFu);
     top = max(top & 0xFFFFu, top >> 16);
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    const float amax = __uint_as_float(top << 16) * inv;
+    const float amax = fminf(__uint_as_float(top << 16) * inv, 4096.0f);  // (over 6 * 448)
     uint32_t sb;  // RNE, saturating at 448
     asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %1, %2;\n\tcvt.u32.u16 %0, h;\n\t}"
         : "=r"(sb)
-        : "f"(0.0f), "f"(__fdiv_rn(amax, kE2m1Max)));
+        : "f"(0.0f), "f"(nearest_quotient(amax, kE2m1Max, 1.0f / kE2m1Max)));
     sb = max(sb & 0xFFu, 1u);
     const bool nan = top > 0x7F80u;
     if (nan) sb = kE4m3Nan;
-    // the scale as binary32: four significant bits, so that q below is the nearest to
-    // the exact quotient after one correction (Markstein), and no tie is moved
+    // the scale as binary32, and its reciprocal, correctly rounded after one Newton step
+    // from the approximate one (for each of the 15 significands that a scale may have)
     const uint32_t e = sb >> 3, m = sb & 7u;
     const float sv = e ? __uint_as_float((e + 120u) << 23 | m << 20) : static_cast<float>(m) * kE4m3Least;
-    const float r = __fdiv_rn(1.0f, sv);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sv));
+    r = __fmaf_rn(__fmaf_rn(-sv, r, 1.0f), r, r);
     auto quotient = [&](float y) {
-      y = fminf(fmaxf(y * inv, -4096.0f), 4096.0f);  // more than 6 * 448: infinities too
-      const float q = y * r;
-      return copysignf(__fmaf_rn(__fmaf_rn(-sv, q, y), r, q), y);  // -0 stays -0
+      y = fminf(fmaxf(y * inv, -4096.0f), 4096.0f);  // infinities too
+      return copysignf(nearest_quotient(y, sv, r), y);  // -0 stays -0
     };
     uint32_t c = 0;
 #pragma unroll

@@ -150,6 +150,33 @@ def test_append_every_bf16():
             assert torch.equal(p[i][at // 128, :, at % 128], codes), top
 
 
+def test_append_every_scale():
+    """Groups whose maxima give every scale that there is, values at and beside every tie
+    of the codes: the nearest code of the exact quotient."""
+    s = SCALES[1:].float()
+    ties = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    x = torch.zeros(len(s), 2, 16)
+    x[:, :, 0] = (s * 6.0)[:, None]
+    x[:, 0, 1:8] = s[:, None] * ties
+    x[:, 1, 1:8] = -s[:, None] * ties
+    up = x[:, 0, 1:8].to(BF16).view(torch.int16)
+    x[:, 0, 8:15] = (up + 1).view(BF16).float()
+    x[:, 1, 8:15] = -(up - 1).view(BF16).float()
+    k = torch.zeros(len(s), 1, 64)
+    k[:, 0, :32] = x.view(len(s), 32)
+    k[:, 0, 32:] = -x.view(len(s), 32)
+    k = k.to(BF16).cuda()
+    at = torch.arange(len(s), device="cuda")
+    cache = fb.new_kv4_cache(-(-len(s) // 64), 1, 64, 64)
+    fb.fp8bq_kv4_append(k, -k, at, cache)
+    p = parts(cache, 64, 64)
+    for i, y in ((0, k), (2, -k)):
+        codes, sc = quantise(y)
+        assert torch.equal(p[i + 1][at // 64, :, at % 64], sc)
+        assert torch.equal(p[i][at // 64, :, at % 64], codes)
+    assert len(sc.unique()) == len(s)  # every scale was met
+
+
 def test_append_special_values():
     inf, nan = math.inf, math.nan
     k = torch.zeros(4, 1, 64, dtype=BF16, device="cuda")
