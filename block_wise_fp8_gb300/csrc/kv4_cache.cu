@@ -35,11 +35,12 @@ __device__ __forceinline__ Slot slot_of(const void *slots, int is64, int64_t t, 
 // Both are bound by HBM: 4D bytes of rows and 9D/8 of a page a token and head.  A
 // thread has 8 values (half a group): rows, codes and scales are then whole runs of a
 // warp's lanes (with whole groups a thread 8192 tokens x 8 heads x 128 took 15 us to
-// write and 12 to read, cold), and kRowTokens tokens, whose loads are in flight
-// together.
-constexpr int kRowTokens = 4;
+// write and 12 to read, cold), and several tokens, whose loads are in flight together:
+// 8192 tokens written and read back took 28.9, 25.4, 26.1 and 31.9 us with 1, 2, 4 and 8
+// of each, 700000 rows read 243, 211, 198 and 250 (with what goes before).
+constexpr int kAppendTokens = 2, kReadTokens = 4;
 
-template <int D>
+template <int D, int kRowTokens>
 struct RowPlace {
   static constexpr int kLanes = D / 4;               // threads a token: keys, then values
   static constexpr int kTokens = kRowThreads / kLanes;  // tokens at a time
@@ -65,23 +66,23 @@ template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const RowPlace<D> at;
+  const RowPlace<D, kAppendTokens> at;
   const int h = blockIdx.y;
   const Kv4Page p = kv4_page(1 << a.page_log2, D);
   const uint16_t *x = (at.kv ? a.v + h * a.v_hs : a.k + h * a.k_hs) + at.piece * 8;
   const int64_t ts = at.kv ? a.v_ts : a.k_ts;
   const float inv = at.kv ? a.v_inv : a.k_inv;
-  Slot s[kRowTokens];
-  uint4 w[kRowTokens];
+  Slot s[kAppendTokens];
+  uint4 w[kAppendTokens];
 #pragma unroll
-  for (int u = 0; u < kRowTokens; ++u) {
+  for (int u = 0; u < kAppendTokens; ++u) {
     const int64_t t = at.token(u);
     s[u].on = false;
     if (t < a.T) s[u] = slot_of(a.slots, a.slots64, t, a.pages, a.page_log2);
     w[u] = t < a.T ? __ldg(reinterpret_cast<const uint4 *>(x + t * ts)) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int u = 0; u < kRowTokens; ++u) {
+  for (int u = 0; u < kAppendTokens; ++u) {
     const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
     // BF16 magnitudes are ordered as their bits are, infinity and then NaN on top
     uint32_t top = 0;
@@ -133,16 +134,16 @@ template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const RowPlace<D> at;
+  const RowPlace<D, kReadTokens> at;
   const int h = blockIdx.y;
   const Kv4Page p = kv4_page(1 << a.page_log2, D);
   uint16_t *y = (at.kv ? a.v + h * a.v_hs : a.k + h * a.k_hs) + at.piece * 8;
   const int64_t ts = at.kv ? a.v_ts : a.k_ts;
   const float gs = at.kv ? a.v_scale : a.k_scale;
-  bool on[kRowTokens];
-  uint32_t c[kRowTokens], sc[kRowTokens];
+  bool on[kReadTokens];
+  uint32_t c[kReadTokens], sc[kReadTokens];
 #pragma unroll
-  for (int u = 0; u < kRowTokens; ++u) {
+  for (int u = 0; u < kReadTokens; ++u) {
     const int64_t t = at.token(u);
     on[u] = false;
     if (t >= a.T) continue;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
     sc[u] = page[(at.kv ? p.v_scales : p.k_scales) + s.at * p.scale_bytes + at.piece / 2];
   }
 #pragma unroll
-  for (int u = 0; u < kRowTokens; ++u) {
+  for (int u = 0; u < kReadTokens; ++u) {
     if (!on[u]) continue;
     const uint32_t scale = both_low(e4m3x2_to_f16(sc[u]));
     uint32_t f[4], out[4];
@@ -381,7 +382,7 @@ unsigned blocks_of(int64_t n, int each) { return static_cast<unsigned>((n + each
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, cudaStream_t st) {
   return by_size(a.D, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    return launch_pdl(kv4_append_kernel<D>, dim3(blocks_of(a.T, RowPlace<D>::kTokens * kRowTokens), a.HK),
+    return launch_pdl(kv4_append_kernel<D>, dim3(blocks_of(a.T, kRowThreads / (D / 4) * kAppendTokens), a.HK),
                       dim3(kRowThreads), 0, st, a);
   });
 }
@@ -389,7 +390,7 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs &a, cudaStream_t st) {
 cudaError_t launch_kv4_read(const Kv4ReadArgs &a, cudaStream_t st) {
   return by_size(a.D, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    return launch_pdl(kv4_read_kernel<D>, dim3(blocks_of(a.T, RowPlace<D>::kTokens * kRowTokens), a.HK),
+    return launch_pdl(kv4_read_kernel<D>, dim3(blocks_of(a.T, kRowThreads / (D / 4) * kReadTokens), a.HK),
                       dim3(kRowThreads), 0, st, a);
   });
 }
