@@ -25,8 +25,8 @@ namespace fp8bq {
 namespace {
 
 constexpr int kKeys = 128;                 // keys a tile
-constexpr int kThreads = 384;              // 2 x 4 softmax warps, MMA warp, copy warp, 2 idle
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kThreads = 384;              // 2 x 4 softmax warps, 2 MMA warps, copy warp, 1 idle
+constexpr int kMmaWarp = 8, kCopyWarp = 10;
 // registers: a softmax thread holds a row's 128 scores, which the third warpgroup
 // makes room for (384 x 168 at launch)
 constexpr int kHighRegs = 224, kLowRegs = 56;
@@ -54,7 +54,7 @@ struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
-  uint64_t v_clean[2], u_full[2], u_empty[2], done;
+  uint64_t v_clean[2], u_full[2], u_empty[2], turn[2], done[2];
   uint32_t abort, never, tmem, pad;
   Unit unit[2];
   int bound[kMaxPrompts + 1];
@@ -131,11 +131,11 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.s_full[i], 1), mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_free[i], 4);
-      mbar_init(&sh.u_full[i], 1), mbar_init(&sh.u_empty[i], 9);
+      mbar_init(&sh.u_full[i], 1), mbar_init(&sh.u_empty[i], 10);
       mbar_init(&sh.v_clean[i], 8), mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.turn[i], 1), mbar_init(&sh.done[i], 1);
     }
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 1);
-    mbar_init(&sh.done, 1);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 2);
     sh.abort = sh.never = 0;
     fence_mbar_init();
   }
@@ -224,32 +224,44 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       for (int i = 0; i < 2 && k > 0; ++i) mbar_wait(&sh.q_full[i], (k - 1) & 1, &sh.never, limit);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ---- products: S of both row tiles, then P V and the next S of each in turn.
-    // The whole warp walks, so that addresses stay in uniform registers; one lane of
-    // it issues.
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ---- products of row tile i: S first, then P V and the next S as one block.  The
+    // whole warp walks, so that addresses stay in uniform registers; one lane of it
+    // issues.  An MMA takes the tensor cores 67 cycles, and they queue few of them:
+    // every commit, fence or wait of the issuing thread between MMAs leaves a gap (a
+    // commit 97 cycles).  So each tile has an issuer of its own, and they pass the
+    // turn: while one commits and waits, the other's MMAs run.  (Without turns both
+    // tiles' blocks mingle, both S come late and nothing runs beside the softmax: 1.95
+    // ms for 16384 tokens, 32 heads over 4; one issuer for both: 1.62.)
     setmaxnreg_dec<kLowRegs>();
+    const int i = warp - kMmaWarp;
     const uint32_t lead = lane == 0;
     const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
-    const uint64_t q_base = sdesc_kmajor_sw128(smem_u32(smem));
+    const uint64_t q_at = sdesc_kmajor_sw128(smem_u32(smem)) + i * (C::kTileBytes / 16);
     const uint64_t k_base = sdesc_kmajor_sw128(smem_u32(ring));
     const uint64_t v_base = sdesc_nmajor_sw128(smem_u32(ring), kHalf);
+    const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * 128;
     const int steps = a.D / 16;
-    uint32_t pph[2] = {0, 0}, looked = 0;  // tiles whose values were looked through
+    uint32_t pph = 0, tph = i ^ 1, looked = 0;  // tiles whose values were looked through
     int st = 0;
     uint32_t ring_ph = 0;  // the ring's place and round
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, limit));
     };
-    auto scores = [&](int i, int s_) {
-      const uint64_t qd = q_base + i * (C::kTileBytes / 16), kd = k_base + s_ * (C::kTileBytes / 16);
+    auto turn = [&] {
+      const bool r = wait(&sh.turn[i], tph);
+      tph ^= 1;
+      tc_fence_after();
+      return r;
+    };
+    auto scores = [&](int at) {
+      const uint64_t kd = k_base + at * (C::kTileBytes / 16);
 #pragma unroll
       for (int s = 0; s < DP / 16; ++s) {
         const uint64_t off = (s >> 2) * (kHalf / 16) + (s & 3) * 2;
-        if (s < steps) umma_bf16_if(lead, tmem + i * 128, qd + off, kd + off, s_desc, s > 0);
+        if (s < steps) umma_bf16_if(lead, s_at, q_at + off, kd + off, s_desc, s > 0);
       }
-      umma_commit_if(lead, &sh.s_full[i]);
     };
     for (int k = 0; ok; ++k) {
       ok = wait(&sh.u_full[k & 1], k >> 1 & 1);
@@ -259,54 +271,47 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       __syncwarp();
       if (lead) mbar_arrive(&sh.u_empty[k & 1]);
       if (tiles == 0) break;
-      ok = wait(&sh.kv_full[st], ring_ph);
-      for (int i = 0; i < 2 && ok; ++i) {
-        ok = wait(&sh.q_full[i], k & 1);
-        tc_fence_after();
-        if (ok) scores(i, st);
-      }
+      ok = wait(&sh.kv_full[st], ring_ph) && wait(&sh.q_full[i], k & 1) && turn();
       if (!ok) break;
+      scores(st);
+      if (lead) mbar_arrive(&sh.turn[i ^ 1]);
+      umma_commit_if(lead, &sh.s_full[i]);
       umma_commit_if(lead, &sh.kv_empty[st]);
-      if (tiles == 1) umma_commit_if(lead, &sh.q_empty[0]), umma_commit_if(lead, &sh.q_empty[1]);
+      if (tiles == 1) umma_commit_if(lead, &sh.q_empty[i]);
       if (++st == C::kStages) st = 0, ring_ph ^= 1;
-      for (int j = 0; j < tiles && ok; ++j) {
+      for (int j = 0; j < tiles; ++j) {
         const int vs = st;
         const bool more = j + 1 < tiles;
         ok = wait(&sh.kv_full[vs], ring_ph);
         if (++st == C::kStages) st = 0, ring_ph ^= 1;
+        if (ok && more) ok = wait(&sh.kv_full[st], ring_ph);
         if (ok && j >= special) {
           ok = wait(&sh.v_clean[looked & 1], looked >> 1 & 1);
           ++looked;
         }
+        ok = ok && wait(&sh.p_ready[i], pph);
+        pph ^= 1;
+        if (ok && j == 0) ok = wait(&sh.o_free[i], (k & 1) ^ 1);
+        ok = ok && turn();
+        if (!ok) break;
+        const uint64_t vd = v_base + vs * (C::kTileBytes / 16);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          ok = ok && wait(&sh.p_ready[i], pph[i]);
-          pph[i] ^= 1;
-          if (ok && j == 0) ok = wait(&sh.o_free[i], (k & 1) ^ 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t vd = v_base + vs * (C::kTileBytes / 16);
-#pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            umma_bf16_ta_if(lead, tmem + 256 + i * 128, tmem + i * 128 + s * 8, vd + s * (2048 / 16),
-                            o_desc, j > 0 || s > 0);
-          umma_commit_if(lead, &sh.o_done[i]);
-          if (i == 1) umma_commit_if(lead, &sh.kv_empty[vs]);
-          if (more) {
-            if (i == 0) ok = wait(&sh.kv_full[st], ring_ph);
-            if (!ok) break;
-            scores(i, st);
-            if (j + 2 == tiles) umma_commit_if(lead, &sh.q_empty[i]);
-            if (i == 1) umma_commit_if(lead, &sh.kv_empty[st]);
-          }
+        for (int s = 0; s < kKeys / 16; ++s)
+          umma_bf16_ta_if(lead, o_at, s_at + s * 8, vd + s * (2048 / 16), o_desc, j > 0 || s > 0);
+        if (more) scores(st);
+        if (lead) mbar_arrive(&sh.turn[i ^ 1]);
+        if (more) umma_commit_if(lead, &sh.s_full[i]);
+        umma_commit_if(lead, &sh.o_done[i]);
+        umma_commit_if(lead, &sh.kv_empty[vs]);
+        if (more) {
+          umma_commit_if(lead, &sh.kv_empty[st]);
+          if (j + 2 == tiles) umma_commit_if(lead, &sh.q_empty[i]);
+          if (++st == C::kStages) st = 0, ring_ph ^= 1;
         }
-        if (more && ++st == C::kStages) st = 0, ring_ph ^= 1;
       }
     }
-    if (lead) {
-      umma_commit(&sh.done);
-      mbar_wait(&sh.done, 0, &sh.never, limit);
-    }
+    umma_commit_if(lead, &sh.done[i]);
+    if (lead) mbar_wait(&sh.done[i], 0, &sh.never, limit);
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: a thread a row of tile i
