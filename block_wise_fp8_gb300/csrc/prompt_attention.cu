@@ -25,7 +25,7 @@ namespace fp8bq {
 namespace {
 
 constexpr int kKeys = 128;                 // keys a tile
-constexpr int kThreads = 384;              // 2 x 4 softmax warps, 2 MMA warps, copy warp, 1 more
+constexpr int kThreads = 384;              // 2 x 4 softmax warps, 2 MMA warps, copy warp, 1 idle
 constexpr int kMmaWarp = 8, kCopyWarp = 10;
 // registers: a softmax thread holds a row's 128 scores, which the third warpgroup
 // makes room for (384 x 168 at launch)
@@ -33,15 +33,12 @@ constexpr int kHighRegs = 224, kLowRegs = 56;
 constexpr int kHalf = 128 * 128;           // bytes of 128 rows x 64 values
 constexpr float kGrowth = 8.0f;            // log2: a maximum within it keeps its reference
 
-template <int DP, bool PAIR>
+template <int DP>
 struct Cfg {
-  static constexpr int kRanks = PAIR ? 2 : 1;
   static constexpr int kHalves = DP / 64;
-  static constexpr int kTileBytes = kHalves * kHalf;       // 128 rows of Q
-  static constexpr int kKvBytes = kTileBytes / kRanks;     // this CTA's part of a tile of K or V
-  static constexpr int kKeyHalf = kHalf / kRanks;          // 64 values of its keys
-  static constexpr int kStages = DP == 64 || PAIR ? 8 : 4;
-  static constexpr int kSmem = 2 * kTileBytes + kStages * kKvBytes + 1024;  // 1024: alignment
+  static constexpr int kTileBytes = kHalves * kHalf;  // 128 rows of Q, K or V
+  static constexpr int kStages = DP == 128 ? 4 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;  // 1024: alignment
 };
 
 struct Unit {
@@ -57,7 +54,7 @@ struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
-  uint64_t v_clean[2], v_landed[2], u_full[2], u_empty[2], turn[2], done[2];
+  uint64_t v_clean[2], u_full[2], u_empty[2], turn[2], done[2];
   uint32_t abort, never, tmem, pad;
   Unit unit[2];
   int bound[kMaxPrompts + 1];
@@ -117,56 +114,47 @@ struct Units {
   }
 };
 
-template <int DP, bool PAIR>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                         const __grid_constant__ CUtensorMap vm, const PromptArgs a) {
-  using C = Cfg<DP, PAIR>;
+  using C = Cfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   uint8_t *ring = smem + 2 * C::kTileBytes;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // CTA of the pair: 0 issues the products for both, and has the barriers that both
-  // arrive on
-  const int rank = PAIR ? cluster_ctarank() : 0;
   volatile uint32_t *abort = &sh.abort;
   const uint64_t limit = a.wait_limit_ns;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.s_full[i], 1), mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.p_ready[i], 4 * C::kRanks), mbar_init(&sh.o_free[i], 4 * C::kRanks);
-      mbar_init(&sh.u_full[i], 1), mbar_init(&sh.u_empty[i], rank ? 8 : PAIR ? 11 : 10);
-      mbar_init(&sh.v_clean[i], 8 * C::kRanks), mbar_init(&sh.q_empty[i], 1);
-      mbar_init(&sh.v_landed[i], 1), mbar_init(&sh.turn[i], 1), mbar_init(&sh.done[i], 1);
+      mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_free[i], 4);
+      mbar_init(&sh.u_full[i], 1), mbar_init(&sh.u_empty[i], 10);
+      mbar_init(&sh.v_clean[i], 8), mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.turn[i], 1), mbar_init(&sh.done[i], 1);
     }
     for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 2);
     sh.abort = sh.never = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    if constexpr (PAIR) tmem_alloc_pair(&sh.tmem, 512), tmem_relinquish_pair();
-    else tmem_alloc(&sh.tmem, 512), tmem_relinquish();
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
   }
   if (warp == kCopyWarp && lane == 0) tma_prefetch_desc(&qm), tma_prefetch_desc(&km), tma_prefetch_desc(&vm);
   griddep_launch_dependents();
   griddep_wait();
-  const int G = a.HQ / a.HK, half_tokens = 128 / G, unit_tokens = 2 * C::kRanks * half_tokens;
+  const int G = a.HQ / a.HK, half_tokens = 128 / G, unit_tokens = 2 * half_tokens;
   for (int s = tid; s <= a.S; s += kThreads) sh.bound[s] = min(max(__ldg(a.offsets + s), 0), a.T);
   __syncthreads();
   for (int s = tid; s < a.S; s += kThreads)
     sh.blocks[s] = (max(sh.bound[s + 1] - sh.bound[s], 0) + unit_tokens - 1) / unit_tokens;
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  // arrival on a barrier of the CTA that issues the products, after accesses to TMEM
-  auto arrive = [&](uint64_t *bar) {
-    if constexpr (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bar), 0));
-    else mbar_arrive(bar);
-  };
 
   if (warp == kCopyWarp) {
     // ---- copies, and the units for everybody
@@ -176,36 +164,20 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     for (int s = lane; s < a.S; s += 32) top = max(top, sh.blocks[s]);
     units.top = __reduce_max_sync(0xFFFFFFFFu, top);
     units.total = units.above(0, lane) * a.HK;
-    const int64_t grid = gridDim.x / C::kRanks, cta = blockIdx.x / C::kRanks;
+    const int64_t grid = gridDim.x, cta = blockIdx.x;
     const uint32_t q_bytes = C::kHalves * half_tokens * G * 128;
     int64_t c = 0;  // copies into the ring so far
     bool ok = true;
     int k = 0;
-    // bytes are counted for both CTAs of a pair, on the first one's barriers
-    auto expect = [&](uint64_t *bar, uint32_t bytes) {
-      if (rank == 0) mbar_arrive_expect_tx(bar, bytes * C::kRanks);
-    };
-    auto load = [&](void *to, const CUtensorMap *map, uint64_t *bar, int x, int head, int row) {
-      if constexpr (PAIR) tma_load_3d_pair(to, map, mapa_shared(smem_u32(bar), 0), x, head, row);
-      else tma_load_3d(to, map, bar, x, head, row);
-    };
-    // a pair shares out a tile's keys, and the columns of its values
-    auto ring_copy = [&](bool keys, int head, int row, bool skip) {
+    auto ring_copy = [&](const CUtensorMap *map, int head, int row, bool skip) {
       const int st = static_cast<int>(c % C::kStages);
       if (!mbar_wait(&sh.kv_empty[st], (c / C::kStages & 1) ^ 1, abort, limit)) return false;
-      expect(&sh.kv_full[st], C::kKvBytes);
+      mbar_arrive_expect_tx(&sh.kv_full[st], C::kTileBytes);
       ++c;
       if (skip) return true;
-      uint8_t *to = ring + st * C::kKvBytes;
-      if (keys) {
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          load(to + h * C::kKeyHalf, &km, &sh.kv_full[st], h * 64, head, row + rank * (kKeys / C::kRanks));
-      } else {
-#pragma unroll
-        for (int h = 0; h < C::kHalves / C::kRanks; ++h)
-          load(to + h * kHalf, &vm, &sh.kv_full[st], (rank + h) * 64, head, row);
-      }
+      for (int h = 0; h < C::kHalves; ++h)
+        tma_load_3d(ring + st * C::kTileBytes + h * kHalf, map, &sh.kv_full[st], h * 64, head, row);
       return true;
     };
     for (;; ++k) {
@@ -227,32 +199,32 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           mbar_arrive(&sh.u_full[k & 1]);
         }
         if (ok && un.tiles > 0) {
-          ok = ring_copy(true, un.head, un.start, a.fault && cta == 0 && k == 0);
+          ok = ring_copy(&km, un.head, un.start, a.fault && cta == 0 && k == 0);
           for (int i = 0; i < 2 && ok; ++i) {
             ok = mbar_wait(&sh.q_empty[i], (k & 1) ^ 1, abort, limit);
             if (!ok) break;
-            expect(&sh.q_full[i], q_bytes);
+            mbar_arrive_expect_tx(&sh.q_full[i], q_bytes);
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-              load(smem + i * C::kTileBytes + h * kHalf, &qm, &sh.q_full[i], h * 64, un.head * G,
-                   un.start + un.t0 + (i * C::kRanks + rank) * half_tokens);
+              tma_load_3d(smem + i * C::kTileBytes + h * kHalf, &qm, &sh.q_full[i], h * 64,
+                          un.head * G, un.start + un.t0 + i * half_tokens);
           }
-          ok = ok && ring_copy(false, un.head, un.start, false);
+          ok = ok && ring_copy(&vm, un.head, un.start, false);
           for (int j = 1; j < un.tiles && ok; ++j)
-            ok = ring_copy(true, un.head, un.start + j * kKeys, false) &&
-                 ring_copy(false, un.head, un.start + j * kKeys, false);
+            ok = ring_copy(&km, un.head, un.start + j * kKeys, false) &&
+                 ring_copy(&vm, un.head, un.start + j * kKeys, false);
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok || un.tiles == 0) break;
     }
-    if (lane == 0 && *abort) {
-      // copies in flight land before the memory is given up: they take microseconds (a
-      // pair's are counted on the first CTA's barriers alone)
-      for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 2000000;) {}
+    if (lane == 0 && *abort) {  // copies in flight land before the memory is given up
+      for (int64_t i = c < C::kStages ? 0 : c - C::kStages; i < c; ++i)
+        mbar_wait(&sh.kv_full[i % C::kStages], i / C::kStages & 1, &sh.never, limit);
+      for (int i = 0; i < 2 && k > 0; ++i) mbar_wait(&sh.q_full[i], (k - 1) & 1, &sh.never, limit);
     }
     __syncwarp();
-  } else if (rank == 0 && (warp == kMmaWarp || warp == kMmaWarp + 1)) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ---- products of row tile i: S first, then P V and the next S as one block.  The
     // whole warp walks, so that addresses stay in uniform registers; one lane of it
     // issues.  An MMA takes the tensor cores 67 cycles, and they queue few of them:
@@ -264,12 +236,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     setmaxnreg_dec<kLowRegs>();
     const int i = warp - kMmaWarp;
     const uint32_t lead = lane == 0;
-    const uint32_t s_desc = idesc_bf16(128 * C::kRanks, kKeys);
-    const uint32_t o_desc = idesc_bf16(128 * C::kRanks, a.D, true);
-    auto commit = [&](uint64_t *bar) {
-      if constexpr (PAIR) umma_commit_pair_if(lead, bar, 3);
-      else umma_commit_if(lead, bar);
-    };
+    const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
     const uint64_t q_at = sdesc_kmajor_sw128(smem_u32(smem)) + i * (C::kTileBytes / 16);
     const uint64_t k_base = sdesc_kmajor_sw128(smem_u32(ring));
     const uint64_t v_base = sdesc_nmajor_sw128(smem_u32(ring), kHalf);
@@ -280,7 +247,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     uint32_t ring_ph = 0;  // the ring's place and round
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xFFFFFFFFu, mbar_wait<PAIR>(bar, parity, abort, limit));
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, limit));
     };
     auto turn = [&] {
       const bool r = wait(&sh.turn[i], tph);
@@ -289,13 +256,11 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       return r;
     };
     auto scores = [&](int at) {
-      const uint64_t kd = k_base + at * (C::kKvBytes / 16);
+      const uint64_t kd = k_base + at * (C::kTileBytes / 16);
 #pragma unroll
       for (int s = 0; s < DP / 16; ++s) {
-        const uint64_t qs = q_at + (s >> 2) * (kHalf / 16) + (s & 3) * 2;
-        const uint64_t ks = kd + (s >> 2) * (C::kKeyHalf / 16) + (s & 3) * 2;
-        if constexpr (PAIR) umma_bf16_pair_if(lead, s_at, qs, ks, s_desc, s > 0);
-        else if (s < steps) umma_bf16_if(lead, s_at, qs, ks, s_desc, s > 0);
+        const uint64_t off = (s >> 2) * (kHalf / 16) + (s & 3) * 2;
+        if (s < steps) umma_bf16_if(lead, s_at, q_at + off, kd + off, s_desc, s > 0);
       }
     };
     for (int k = 0; ok; ++k) {
@@ -310,9 +275,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       if (!ok) break;
       scores(st);
       if (lead) mbar_arrive(&sh.turn[i ^ 1]);
-      commit(&sh.s_full[i]);
-      commit(&sh.kv_empty[st]);
-      if (tiles == 1) commit(&sh.q_empty[i]);
+      umma_commit_if(lead, &sh.s_full[i]);
+      umma_commit_if(lead, &sh.kv_empty[st]);
+      if (tiles == 1) umma_commit_if(lead, &sh.q_empty[i]);
       if (++st == C::kStages) st = 0, ring_ph ^= 1;
       for (int j = 0; j < tiles; ++j) {
         const int vs = st;
@@ -329,52 +294,24 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
         if (ok && j == 0) ok = wait(&sh.o_free[i], (k & 1) ^ 1);
         ok = ok && turn();
         if (!ok) break;
-        const uint64_t vd = v_base + vs * (C::kKvBytes / 16);
+        const uint64_t vd = v_base + vs * (C::kTileBytes / 16);
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s) {
-          if constexpr (PAIR)
-            umma_bf16_ta_pair_if(lead, o_at, s_at + s * 8, vd + s * (2048 / 16), o_desc, j > 0 || s > 0);
-          else
-            umma_bf16_ta_if(lead, o_at, s_at + s * 8, vd + s * (2048 / 16), o_desc, j > 0 || s > 0);
-        }
+        for (int s = 0; s < kKeys / 16; ++s)
+          umma_bf16_ta_if(lead, o_at, s_at + s * 8, vd + s * (2048 / 16), o_desc, j > 0 || s > 0);
         if (more) scores(st);
         if (lead) mbar_arrive(&sh.turn[i ^ 1]);
-        if (more) commit(&sh.s_full[i]);
-        commit(&sh.o_done[i]);
-        commit(&sh.kv_empty[vs]);
+        if (more) umma_commit_if(lead, &sh.s_full[i]);
+        umma_commit_if(lead, &sh.o_done[i]);
+        umma_commit_if(lead, &sh.kv_empty[vs]);
         if (more) {
-          commit(&sh.kv_empty[st]);
-          if (j + 2 == tiles) commit(&sh.q_empty[i]);
+          umma_commit_if(lead, &sh.kv_empty[st]);
+          if (j + 2 == tiles) umma_commit_if(lead, &sh.q_empty[i]);
           if (++st == C::kStages) st = 0, ring_ph ^= 1;
         }
       }
     }
-    if constexpr (PAIR) umma_commit_pair_if(lead, &sh.done[i], 1);
-    else umma_commit_if(lead, &sh.done[i]);
+    umma_commit_if(lead, &sh.done[i]);
     if (lead) mbar_wait(&sh.done[i], 0, &sh.never, limit);
-    __syncwarp();
-  } else if (PAIR && warp == kCopyWarp + 1 && rank == 0) {
-    // ---- tells the other CTA that values have landed which its warps have to look
-    // through (the copies of both are counted here)
-    setmaxnreg_dec<kLowRegs>();
-    if (lane == 0) {
-      int64_t c = 0;
-      uint32_t looked = 0;
-      for (int k = 0;; ++k) {
-        if (!mbar_wait(&sh.u_full[k & 1], k >> 1 & 1, abort, limit)) break;
-        const int tiles = sh.unit[k & 1].tiles, special = sh.unit[k & 1].t0 / kKeys;
-        mbar_arrive(&sh.u_empty[k & 1]);
-        if (tiles == 0) break;
-        bool ok = true;
-        for (int j = special; j < tiles && ok; ++j) {
-          const int64_t n = c + 2 * j + 1;
-          ok = mbar_wait<true>(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit);
-          if (ok) mbar_arrive_cluster_release(mapa_shared(smem_u32(&sh.v_landed[looked++ & 1]), 1));
-        }
-        if (!ok) break;
-        c += 2 * tiles;
-      }
-    }
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: a thread a row of tile i
@@ -392,7 +329,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       if (!ok) break;
       Unit un = sh.unit[k & 1];
       if (un.tiles == 0) break;
-      const int tok = un.t0 + (i * C::kRanks + rank) * half_tokens + tok_in;
+      const int tok = un.t0 + i * half_tokens + tok_in;
       const int special = un.t0 / kKeys;
       float ref = -INFINITY, sum = 0.0f;
       for (int j = 0; j < un.tiles && ok; ++j) {
@@ -401,14 +338,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           // 0 times it would spoil them, so it is taken out here and added to the
           // rows that see it at the end
           const int64_t n = c + 2 * j + 1;
-          ok = rank == 0 ? mbar_wait<PAIR>(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit)
-                         : mbar_wait<PAIR>(&sh.v_landed[looked & 1], looked >> 1 & 1, abort, limit);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit));
           if (!ok) break;
-          uint4 *v = reinterpret_cast<uint4 *>(ring + (n % C::kStages) * C::kKvBytes) + tid;
+          uint4 *v = reinterpret_cast<uint4 *>(ring + (n % C::kStages) * C::kTileBytes) + tid;
           bool wrote = false;
 #pragma unroll
-          for (int w = 0; w < C::kKvBytes / 16 / 256; ++w) {
+          for (int w = 0; w < C::kTileBytes / 16 / 256; ++w) {
             const uint4 x = v[w * 256];
             auto flags = [](uint32_t y) { return ((y & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
             if ((flags(x.x) | flags(x.y) | flags(x.z) | flags(x.w)) == 0) continue;
@@ -419,24 +354,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
             v[w * 256] = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
             wrote = true;
           }
-          if (wrote) {  // for the rows of both
-            if constexpr (PAIR) {
-              const uint32_t at = smem_u32(&sh.unit[k & 1].bad);
-              st_shared_cluster(mapa_shared(at, 0), 1), st_shared_cluster(mapa_shared(at, 1), 1);
-            } else {
-              sh.unit[k & 1].bad = 1;
-            }
-          }
+          if (wrote) sh.unit[k & 1].bad = 1;
           fence_proxy_async_smem();
           __syncwarp();
           // (two barriers in turn: one tile's four warps may be a tile ahead)
-          if (lane == 0) {
-            if constexpr (PAIR) mbar_arrive_cluster_release(mapa_shared(smem_u32(&sh.v_clean[looked & 1]), 0));
-            else mbar_arrive(&sh.v_clean[looked & 1]);
-          }
+          if (lane == 0) mbar_arrive(&sh.v_clean[looked & 1]);
           ++looked;
         }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait<PAIR>(&sh.s_full[i], sph, abort, limit));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.s_full[i], sph, abort, limit));
         sph ^= 1;
         if (!ok) break;
         tc_fence_after();
@@ -462,7 +387,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           const float by = grow ? ex2((ref - top) * sc) : 1.0f;
           if (grow) ref = top;
           sum *= by;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait<PAIR>(&sh.o_done[i], oph ^ 1, abort, limit));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_done[i], oph ^ 1, abort, limit));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -499,12 +424,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive(&sh.p_ready[i]);
+        if (lane == 0) mbar_arrive(&sh.p_ready[i]);
       }
       if (!ok) break;
       c += 2 * un.tiles;
       // ---- the unit's end
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait<PAIR>(&sh.o_done[i], oph ^ 1, abort, limit));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_done[i], oph ^ 1, abort, limit));
       if (!ok) break;
       tc_fence_after();
       const bool bad = *reinterpret_cast<volatile int *>(&sh.unit[k & 1].bad) != 0;
@@ -544,7 +469,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(&sh.o_free[i]), mbar_arrive(&sh.u_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&sh.o_free[i]), mbar_arrive(&sh.u_empty[k & 1]);
     }
   } else {
     setmaxnreg_dec<kLowRegs>();
@@ -552,55 +477,37 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) atomicMax(a.status, kStatusTimeout);
-  if constexpr (PAIR) cluster_sync();  // neither leaves before the other's products and arrivals
-  if (warp == kMmaWarp) {
-    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
-    else tmem_dealloc(tmem, 512);
-  }
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, int num_sms, cudaStream_t st) {
   const int G = a.HQ / a.HK, half_tokens = 128 / G;
-  auto run = [&](auto d, auto two) {
+  CUtensorMap qm, km, vm;
+  if (!make_heads_map(&qm, a.q, a.T, a.HQ, a.D, a.q_ts, a.q_hs, half_tokens, G) ||
+      !make_heads_map(&km, a.k, a.T, a.HK, a.D, a.k_ts, a.k_hs, kKeys, 1) ||
+      !make_heads_map(&vm, a.v, a.T, a.HK, a.D, a.v_ts, a.v_hs, kKeys, 1))
+    return cudaErrorInvalidValue;
+  // units at most: every sequence may end inside one
+  const int64_t blocks = (a.T + 2 * half_tokens - 1) / (2 * half_tokens) + a.S;
+  const int64_t most = blocks * a.HK;
+  const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
+  auto run = [&](auto d) {
     constexpr int DP = decltype(d)::value;
-    constexpr bool PAIR = decltype(two)::value;
-    using C = Cfg<DP, PAIR>;
-    CUtensorMap qm, km, vm;
-    if (!make_heads_map(&qm, a.q, a.T, a.HQ, a.D, a.q_ts, a.q_hs, half_tokens, G) ||
-        !make_heads_map(&km, a.k, a.T, a.HK, a.D, a.k_ts, a.k_hs, kKeys / C::kRanks, 1) ||
-        !make_heads_map(&vm, a.v, a.T, a.HK, a.D, a.v_ts, a.v_hs, kKeys, 1))
-      return cudaErrorInvalidValue;
-    constexpr auto kern = prompt_attention_kernel<DP, PAIR>;
-    cudaError_t e = allow_smem<kern>(C::kSmem);
+    cudaError_t e = allow_smem<prompt_attention_kernel<DP>>(Cfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc waits for registers that the block was launched with: no launch
     // unless the compiled count covers the split
     static const int regs = [] {
       cudaFuncAttributes fa;
-      return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+      return cudaFuncGetAttributes(&fa, prompt_attention_kernel<DP>) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs * kThreads < 256 * kHighRegs + 128 * kLowRegs) return cudaErrorInvalidConfiguration;
-    // units at most: every sequence may end inside one
-    const int unit_tokens = 2 * C::kRanks * half_tokens;
-    const int64_t most = ((a.T + unit_tokens - 1) / unit_tokens + a.S) * static_cast<int64_t>(a.HK);
-    const int64_t room = num_sms / C::kRanks;
-    const unsigned grid = static_cast<unsigned>((most < room ? most : room) * C::kRanks);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C::kRanks, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st, cfg.attrs = attr, cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, qm, km, vm, a);
+    return launch_pdl(prompt_attention_kernel<DP>, dim3(grid), dim3(kThreads), Cfg<DP>::kSmem, st, qm,
+                      km, vm, a);
   };
-  using two = std::true_type;
-  using one = std::false_type;
-  if (a.D == 128 && a.T >= 2048 * static_cast<int64_t>(a.S)) return run(std::integral_constant<int, 128>{}, two{});
-  return a.D <= 64 ? run(std::integral_constant<int, 64>{}, one{}) : run(std::integral_constant<int, 128>{}, one{});
+  return a.D <= 64 ? run(std::integral_constant<int, 64>{}) : run(std::integral_constant<int, 128>{});
 }
 
 }  // namespace fp8bq

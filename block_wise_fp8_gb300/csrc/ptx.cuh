@@ -569,37 +569,6 @@ __device__ __forceinline__ void umma_f8f6f4_pair(uint32_t d_tmem, uint64_t adesc
       : "memory");
 }
 
-// kind::f16 pair MMAs (BF16) and their commit, issued by the lanes with `on` of a warp
-// of the even CTA that walks together; in the second form A lies in both CTAs' TMEM.
-__device__ __forceinline__ void umma_bf16_pair_if(uint32_t on, uint32_t d_tmem, uint64_t adesc,
-                                                  uint64_t bdesc, uint32_t idesc,
-                                                  uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void umma_bf16_ta_pair_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem,
-                                                     uint64_t bdesc, uint32_t idesc,
-                                                     uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_pair_if(uint32_t on, uint64_t *bar, uint16_t cta_mask) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "h"(cta_mask), "r"(on)
-      : "memory");
-}
-
 // Block-scaled pair MMA (MXFP8), issued by the even CTA: each CTA's tensor core
 // reads the scale factors from its own TMEM at the given columns.
 __device__ __forceinline__ void umma_mxf8f6f4_pair(uint32_t d_tmem, uint64_t adesc,
@@ -642,30 +611,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const void *tma
       "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster_addr), "r"(c0), "r"(c1)
       : "memory");
-}
-
-// The same for a 3-D map.
-__device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const void *tmap,
-                                                 uint32_t bar_cluster_addr, int32_t c0,
-                                                 int32_t c1, int32_t c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
-// Arrival that orders nothing but what tcgen05.fence::before_thread_sync before it
-// does (this thread's finished TMEM accesses): a release at cluster scope takes about
-// 1000 cycles.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
-// A 32-bit store to shared memory of the cluster, given by its shared::cluster address.
-__device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
 }  // namespace fp8bq
