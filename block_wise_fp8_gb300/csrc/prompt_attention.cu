@@ -38,7 +38,8 @@ struct Cfg {
   static constexpr int kHalves = DP / 64;
   static constexpr int kTileBytes = kHalves * kHalf;  // 128 rows of Q, K or V
   static constexpr int kStages = DP == 128 ? 4 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;  // 1024: alignment
+  static constexpr int kOutBytes = 8 * 32 * 64;       // a softmax warp's 32 rows x 32 values
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + kOutBytes + 1024;  // 1024: alignment
 };
 
 struct Unit {
@@ -321,8 +322,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
     const int tok_in = row / G, head_in = row - tok_in * G;
     const float sc = a.scale_log2;
-    int64_t c = 0;
+    uint4 *out = reinterpret_cast<uint4 *>(ring + C::kStages * C::kTileBytes) + warp * 128;
     uint32_t sph = 0, oph = 0, looked = 0;
+    int64_t c = 0;  // copies into the ring of the units before
     bool ok = true;
     for (int k = 0;; ++k) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.u_full[k & 1], k >> 1 & 1, abort, limit));
@@ -334,27 +336,33 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       float ref = -INFINITY, sum = 0.0f;
       for (int j = 0; j < un.tiles && ok; ++j) {
         if (j >= special) {
-          // values of these tokens are hidden from some rows: where one is not finite
-          // 0 times it would spoil them, so it is taken out here and added to the
-          // rows that see it at the end
+          // values of these tokens are hidden from some rows: one that is not finite would
+          // spoil those (0 times it is NaN), so it is taken out here and added to the rows
+          // that see it at the end.  (One warp for it, beside the others, took 3800 cycles
+          // that the last product waited for.)
           const int64_t n = c + 2 * j + 1;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.kv_full[n % C::kStages], n / C::kStages & 1, abort, limit));
           if (!ok) break;
           uint4 *v = reinterpret_cast<uint4 *>(ring + (n % C::kStages) * C::kTileBytes) + tid;
-          bool wrote = false;
+          // halves whose exponent is all ones
+          auto flags = [](uint32_t y) { return ((y & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+          auto clean = [&](uint32_t y) {
+            const uint32_t f = flags(y);
+            return y & ~((f >> 31) * 0xFFFF0000u) & ~((f >> 15 & 1u) * 0xFFFFu);
+          };
+          constexpr int kWords = C::kTileBytes / 16 / 256;
+          uint4 x[kWords];
+          uint32_t f = 0;
 #pragma unroll
-          for (int w = 0; w < C::kTileBytes / 16 / 256; ++w) {
-            const uint4 x = v[w * 256];
-            auto flags = [](uint32_t y) { return ((y & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
-            if ((flags(x.x) | flags(x.y) | flags(x.z) | flags(x.w)) == 0) continue;
-            auto clean = [&](uint32_t y) {
-              const uint32_t f = flags(y);
-              return y & ~((f >> 31) * 0xFFFF0000u) & ~((f >> 15 & 1u) * 0xFFFFu);
-            };
-            v[w * 256] = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
-            wrote = true;
+          for (int w = 0; w < kWords; ++w) x[w] = v[w * 256];
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) f |= flags(x[w].x) | flags(x[w].y) | flags(x[w].z) | flags(x[w].w);
+          if (f) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+              v[w * 256] = make_uint4(clean(x[w].x), clean(x[w].y), clean(x[w].z), clean(x[w].w));
+            sh.unit[k & 1].bad = 1;
           }
-          if (wrote) sh.unit[k & 1].bad = 1;
           fence_proxy_async_smem();
           __syncwarp();
           // (two barriers in turn: one tile's four warps may be a tile ahead)
@@ -435,41 +443,58 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       const bool bad = *reinterpret_cast<volatile int *>(&sh.unit[k & 1].bad) != 0;
       const bool live = tok_in < half_tokens && tok < un.len;
       const float by = 1.0f / sum;
-      uint16_t *y = a.y + static_cast<int64_t>(un.start + tok) * a.y_ts +
-                    static_cast<int64_t>(un.head * G + head_in) * a.y_hs;
+      uint16_t *y = live ? a.y + static_cast<int64_t>(un.start + tok) * a.y_ts +
+                               static_cast<int64_t>(un.head * G + head_in) * a.y_hs
+                         : nullptr;
+      // by way of shared memory, so that four lanes write 64 bytes of a row (a row a
+      // lane: 16 bytes of 32 rows a store).  Little code: what runs once a unit comes
+      // from afar.
+      uint16_t *to[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        to[x] = reinterpret_cast<uint16_t *>(
+            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(y), x * 8 + (lane >> 2)));
 #pragma unroll 1
       for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
         tmem_ld32(o_at + q * 32, o);
         tmem_ld_wait();
-        if (!live) continue;
 #pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
-        if (bad)
-          for (int t = special * kKeys; t <= tok; ++t) {
-            const uint16_t *v = a.v + static_cast<int64_t>(un.start + t) * a.v_ts +
-                                static_cast<int64_t>(un.head) * a.v_hs + q * 32;
+        for (int x = 0; x < 4; ++x) {
+          uint32_t w[4];
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (q * 32 + x < a.D) {
-                const uint32_t bits = v[x];
-                if ((bits & 0x7F80u) == 0x7F80u)
-                  o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(bits << 16));
-              }
-          }
+          for (int z = 0; z < 4; ++z)
+            w[z] = pack_bf16(__uint_as_float(o[x * 8 + 2 * z]) * by, __uint_as_float(o[x * 8 + 2 * z + 1]) * by);
+          out[lane * 4 + (x ^ (lane >> 1 & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        const int piece = lane & 3;
 #pragma unroll
-        for (int x = 0; x < 32; x += 8)
-          if (q * 32 + x < a.D) {
-            uint32_t w[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              w[z] = pack_bf16(__uint_as_float(o[x + 2 * z]), __uint_as_float(o[x + 2 * z + 1]));
-            *reinterpret_cast<uint4 *>(y + q * 32 + x) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int x = 0; x < 4; ++x) {
+          const int r = x * 8 + (lane >> 2);
+          const uint4 v = out[r * 4 + (piece ^ (r >> 1 & 3))];
+          if (to[x] && q * 32 + piece * 8 < a.D)
+            *reinterpret_cast<uint4 *>(to[x] + q * 32 + piece * 8) = v;
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_free[i]), mbar_arrive(&sh.u_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&sh.o_free[i]);
+      if (bad && live) {  // (the row is written; an infinity or a NaN outdoes its rounding)
+        for (int t = special * kKeys; t <= tok; ++t) {
+          const uint16_t *v = a.v + static_cast<int64_t>(un.start + t) * a.v_ts +
+                              static_cast<int64_t>(un.head) * a.v_hs;
+#pragma unroll 1
+          for (int x = 0; x < a.D; ++x)
+            if ((v[x] & 0x7F80u) == 0x7F80u) {
+              const float sum_ = __uint_as_float(static_cast<uint32_t>(*(volatile uint16_t *)(y + x)) << 16) +
+                                 __uint_as_float(static_cast<uint32_t>(v[x]) << 16);
+              y[x] = static_cast<uint16_t>(pack_bf16(sum_, 0.0f));
+            }
+        }
+      }
+      if (lane == 0) mbar_arrive(&sh.u_empty[k & 1]);
     }
   } else {
     setmaxnreg_dec<kLowRegs>();
