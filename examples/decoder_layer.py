@@ -3,13 +3,18 @@
     residual add + RMSNorm + quantisation   fp8bq_add_rmsnorm_quant_act
     QKV projection, adapters beside it      fp8bq_gemm, fp8bq_lora_add
     head norms and rotary embedding         fp8bq_qk_norm_rope
-    attention                               (torch; the library has none)
+    attention                               plain torch over BF16 rows, or with
+                                            cache4=True fp8bq_kv4_append and
+                                            fp8bq_kv4_attention over a paged cache in
+                                            4 bits; whole prompts (offsets given):
+                                            fp8bq_prompt_attention
     output projection, adapters             fp8bq_linear, fp8bq_lora_add
     residual add + RMSNorm                  fp8bq_add_rmsnorm_quant_act
     mixture of experts                      fp8bq_moe_layer
 
 Every request has its own adapter (or none); the tokens are grouped by adapter
-once a step.  `python examples/decoder_layer.py` times the step on a GPU and
+once a step.  With a 4-bit cache the softmax weight that each cached token gets is
+added up, and `evict` keeps the heaviest and the last ones.  `python examples/decoder_layer.py` times the step on a GPU and
 prints how far it is from the same layer in 64 bits with unquantised
 activations.
 """
@@ -31,7 +36,7 @@ class Layer:
     """Weights, quantised once, and the buffers of a step of `M` tokens."""
 
     def __init__(self, M: int, seed: int = 0, H=2048, heads=16, kv_heads=2, D=128, E=32, I=512,
-                 topk=4, adapters=8, rank=16, context=256):
+                 topk=4, adapters=8, rank=16, context=256, cache4=False, page=32):
         g = torch.Generator("cuda").manual_seed(seed)
         rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
         self.M, self.H, self.heads, self.kv, self.D = M, H, heads, kv_heads, D
@@ -62,6 +67,10 @@ class Layer:
         self.qkv, self.q, self.k = e(M, nqkv), e(M, heads, D), e(M, kv_heads, D)
         self.attn, self.o, self.y = e(M, nq), e(M, H), e(M, H)
         self.order, self.offsets = e(M, dtype=I32), e(adapters + 1, dtype=I32)
+        self.cache4 = None
+        if cache4:
+            self._new_cache(context, page)
+        self.ws_prompt = fb.new_workspace(fb.OP_PROMPT_ATTENTION, M, heads, D)
         self.ws_qkv = fb.new_workspace(fb.OP_GEMM, M, nqkv, H)
         self.ws_o = fb.new_workspace(fb.OP_LINEAR, M, H, nq)
         lora = max(fb.fp8bq_workspace_bytes(fb.OP_LORA_ADD, M, rank, k) for k in (H, nq))
@@ -76,6 +85,54 @@ class Layer:
         fb.fp8bq_quant_weight_block(w, q, s)
         return q, s
 
+    # ------------------------------------------------------------ the 4-bit cache
+
+    def _new_cache(self, context, page, spare=64):
+        """A cache with room for `context` rows of every request and `spare` more, its
+        pages in no order, holding what k_cache and v_cache hold."""
+        M, self.page = self.M, page
+        width = -(-(context + spare) // page)
+        self.cache4 = fb.new_kv4_cache(2 * M * width, self.kv, page, self.D)
+        self.weights = torch.zeros(2 * M * width, self.kv, page, device="cuda")
+        order = torch.randperm(2 * M * width, device="cuda").to(I32)
+        self.pages, self.free = order[:M * width].view(M, width), order[M * width:].view(M, width)
+        self.lens = torch.full((M,), context, dtype=I32, device="cuda")
+        self.ws_kv4 = fb.new_kv4_workspace(M, 1, self.heads, self.kv, self.D, width * page, True)
+        at = torch.arange(context, device="cuda").repeat(M, 1)
+        self.write_rows(self.k_cache.flatten(0, 1), self.v_cache.flatten(0, 1),
+                        self.slots(torch.arange(M, device="cuda")[:, None], at).flatten())
+
+    def slots(self, request, at):
+        """Slots of the requests' tokens `at`, by the block table."""
+        return self.pages.long()[request, at // self.page] * self.page + at % self.page
+
+    def write_rows(self, k, v, slots):
+        fb.fp8bq_kv4_append(k, v, slots, self.cache4, weights=self.weights)
+
+    def read_rows(self, slots):
+        k, v = [torch.empty(slots.numel(), self.kv, self.D, dtype=BF16, device="cuda")
+                for _ in range(2)]
+        fb.fp8bq_kv4_read(self.cache4, slots, k, v)
+        return k, v
+
+    def _attend4(self, q, k, v):
+        """One new token a request: into the cache, then attention over all of it."""
+        self.write_rows(k, v, self.slots(torch.arange(self.M, device="cuda"), self.lens.long()))
+        fb.fp8bq_kv4_attention(q, self.cache4, self.pages, self.lens + 1,
+                               self.attn.view(self.M, self.heads, self.D), self.ws_kv4,
+                               weights=self.weights)
+
+    def evict(self, budget, recent):
+        """Keeps `budget` of each request's tokens a head, in the spare pages."""
+        lens, kept = torch.empty_like(self.lens), torch.empty(self.M, self.kv, budget, dtype=I32,
+                                                              device="cuda")
+        fb.fp8bq_kv4_evict(self.cache4, self.pages, self.lens, self.weights, self.free, lens, kept,
+                           recent, self.D)
+        self.pages, self.free, self.lens = self.free, self.pages, lens
+        return kept
+
+    # ------------------------------------------------------------ a step
+
     def _attend(self, q, k, v, kc, vc):
         """Plain attention of one new token a request over its context."""
         k = torch.cat([kc, k[:, None]], 1).repeat_interleave(self.heads // self.kv, 2)
@@ -83,8 +140,19 @@ class Layer:
         p = torch.softmax(torch.einsum("mhd,mthd->mht", q, k) * self.D ** -0.5, -1)
         return torch.einsum("mht,mthd->mhd", p, v).reshape(self.M, -1)
 
-    def step(self, x, residual, positions, adapter_ids):
-        """x, residual [M, H] BF16 -> the layer's output and new residual."""
+    def _attend_prompts(self, q, k, v, bounds):
+        """Plain causal attention of whole prompts, rows bounds[i] .. bounds[i+1]-1 each."""
+        k, v = [t.repeat_interleave(self.heads // self.kv, 1) for t in (k, v)]
+        y = torch.zeros_like(q)
+        for a, b in zip(bounds, bounds[1:]):
+            s = torch.einsum("ihd,jhd->hij", q[a:b], k[a:b]) * self.D ** -0.5
+            s = s.masked_fill(torch.ones_like(s).triu(1).bool(), float("-inf"))
+            y[a:b] = torch.einsum("hij,jhd->ihd", torch.softmax(s, -1), v[a:b])
+        return y.reshape(self.M, -1)
+
+    def step(self, x, residual, positions, adapter_ids, offsets=None):
+        """x, residual [M, H] BF16 -> the layer's output and new residual.  The rows are
+        one new token of each request, or with `offsets` (int32 [S + 1]) whole prompts."""
         fb.fp8bq_lora_group(adapter_ids, self.order, self.offsets)
         fb.fp8bq_add_rmsnorm_quant_act(x, self.g1, 1e-6, residual=residual,
                                        residual_out=self.resid1, y=self.n1, q=self.q8, s=self.q8s)
@@ -95,8 +163,14 @@ class Layer:
         k = self.qkv[:, nq:nq + nk].view(self.M, self.kv, self.D)
         v = self.qkv[:, nq + nk:].view(self.M, self.kv, self.D)
         fb.fp8bq_qk_norm_rope(q, k, self.gq, self.gk, self.table, positions, self.q, self.k)
-        self.attn.copy_(self._attend(self.q.float(), self.k.float(), v.float(),
-                                     self.k_cache.float(), self.v_cache.float()))
+        if offsets is not None:
+            fb.fp8bq_prompt_attention(self.q, self.k, v, offsets,
+                                      self.attn.view(self.M, self.heads, self.D), self.ws_prompt)
+        elif self.cache4 is not None:
+            self._attend4(self.q, self.k, v)
+        else:
+            self.attn.copy_(self._attend(self.q.float(), self.k.float(), v.float(),
+                                         self.k_cache.float(), self.v_cache.float()))
         fb.fp8bq_linear(self.attn, self.o_w, self.o_s, self.o, self.ws_o)
         self._adapters(self.attn, self.o_lora, self.o)
         fb.fp8bq_add_rmsnorm_quant_act(self.o, self.g2, 1e-6, residual=self.resid1,
@@ -111,10 +185,11 @@ class Layer:
 
     # ------------------------------------------------------------ 64 bits
 
-    def reference(self, x, residual, positions, adapter_ids):
+    def reference(self, x, residual, positions, adapter_ids, offsets=None):
         """The same layer in 64 bits from the quantised weights, its activations
         not quantised.  The experts are those that the step's own norm output
-        chooses, so that a close choice cannot differ."""
+        chooses, so that a close choice cannot differ.  With a 4-bit cache, keys and
+        values are those that the step has left in it (of equal lengths)."""
         d = torch.float64
         deq = lambda q, s: q.to(d) * s.to(d).repeat_interleave(128, 0)[:q.shape[0]].repeat_interleave(  # noqa: E731
             128, 1)[:, :q.shape[1]]
@@ -142,7 +217,16 @@ class Layer:
         q = rotate(qkv[:, :nq].view(self.M, self.heads, self.D), self.gq)
         k = rotate(qkv[:, nq:nq + nk].view(self.M, self.kv, self.D), self.gk)
         v = qkv[:, nq + nk:].view(self.M, self.kv, self.D)
-        at = self._attend(q, k, v, self.k_cache.to(d), self.v_cache.to(d))
+        if offsets is not None:
+            at = self._attend_prompts(q, k, v, offsets.tolist())
+        elif self.cache4 is not None:
+            n = int(self.lens[0])
+            rows = self.read_rows(self.slots(torch.arange(self.M, device="cuda")[:, None],
+                                             torch.arange(n + 1, device="cuda")[None]).flatten())
+            kc, vc = [r.to(d).view(self.M, n + 1, self.kv, self.D) for r in rows]
+            at = self._attend(q, kc[:, n], vc[:, n], kc[:, :n], vc[:, :n])
+        else:
+            at = self._attend(q, k, v, self.k_cache.to(d), self.v_cache.to(d))
         r2 = r1 + at @ deq(self.o_w, self.o_s).t() + adapters(at, self.o_lora)
         n2 = norm(r2, self.g2)
         logits = self.n2.float() @ self.router.t()
@@ -168,8 +252,8 @@ def inputs(layer: Layer, seed: int = 1, adapters: int = 8):
 
 
 def main():
-    for M in (1, 16, 64):
-        layer = Layer(M, **SIZES)
+    for M, cache4 in ((1, False), (16, False), (64, False), (1, True), (16, True), (64, True)):
+        layer = Layer(M, cache4=cache4, **SIZES)
         args = inputs(layer)
         y, r = layer.step(*args)
         ry, rr = layer.reference(*args)
@@ -181,7 +265,7 @@ def main():
             layer.step(*args)
         end.record()
         torch.cuda.synchronize()
-        print(f"{M:3d} tokens: {start.elapsed_time(end) * 20:.0f} us a step; relative error of the "
+        print(f"{M:3d} tokens{', 4-bit cache' if cache4 else ''}: {start.elapsed_time(end) * 20:.0f} us a step; relative error of the "
               f"output {err[0]:.3f}, of the residual {err[1]:.4f}")
 
 
