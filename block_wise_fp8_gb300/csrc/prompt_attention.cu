@@ -409,7 +409,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           }
         }
         oph ^= 1;
-        const float neg = ref == -INFINITY ? 0.0f : -ref * sc;
+        // (the difference is taken before the scale, so that it is exact where it is
+        // small, however large the scores are; one rounding less, s * sc - ref * sc, is
+        // 2 % faster and gives infinite p where ref * sc passes 2^30)
+        const float neg = ref == -INFINITY ? 0.0f : -ref;
         const uint64_t sc2 = pair(sc, sc), neg2 = pair(neg, neg);
         uint64_t l[2] = {0, 0};
 #pragma unroll
@@ -418,8 +421,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             float p0, p1;
-            unpair(fma2(pair(__uint_as_float(s[q * 64 + 2 * x]), __uint_as_float(s[q * 64 + 2 * x + 1])),
-                        sc2, neg2), p0, p1);
+            unpair(mul2(add2(pair(__uint_as_float(s[q * 64 + 2 * x]), __uint_as_float(s[q * 64 + 2 * x + 1])),
+                             neg2), sc2), p0, p1);
             p0 = ex2(p0), p1 = ex2(p1);
             l[x & 1] = add2(l[x & 1], pair(p0, p1));
             p[x] = pack_bf16(p0, p1);

@@ -138,6 +138,29 @@ def test_bad_rows_past_the_sequences():
     check(*run([150, 0, 33], 8, 2, 128, lead=13, tail=77, edit=edit))
 
 
+@pytest.mark.parametrize("size", [1e6, 1e12, 1e16])
+def test_scores_of_any_size(size):
+    """Scores so far apart that one key has all of a row's weight: its value, exactly."""
+    g = torch.Generator("cuda").manual_seed(6)
+    T, HQ, HK, D = 400, 4, 2, 128
+    q, k, v = packed(g, T, HQ, HK, D)
+    q.mul_(size), k.mul_(size)
+    y = torch.empty(T, HQ, D, dtype=BF16, device="cuda")
+    ws = fb.new_workspace(fb.OP_PROMPT_ATTENTION, T, HQ, D)
+    fb.fp8bq_prompt_attention(q, k, v, torch.tensor([0, T], dtype=I32, device="cuda"), y, ws)
+    s = torch.einsum("ihd,jhd->hij", q.double(), k.double().repeat_interleave(2, 1))
+    s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1), -math.inf)
+    top = s.topk(2, -1)
+    # FP32 sums cannot turn which of the two is larger, and e^-200 of the other is nothing
+    mag = torch.einsum("ihd,jhd->hij", q.double().abs(), k.double().abs().repeat_interleave(2, 1))
+    clear = (top.values[..., 0] - top.values[..., 1]) > mag.amax(-1) * (D + 8) * 2.0 ** -22 + 200 * D ** 0.5
+    clear[:, 0] = True
+    want = v.repeat_interleave(2, 1).transpose(0, 1).gather(1, top.indices[..., :1].expand(-1, -1, D))
+    assert float(clear.float().mean()) > 0.9
+    assert torch.equal(y.transpose(0, 1)[clear], want[clear])
+    assert bool(y.isfinite().all())
+
+
 def test_in_place_and_other_layouts():
     g = torch.Generator("cuda").manual_seed(3)
     T, HQ, HK, D = 333, 8, 2, 128
