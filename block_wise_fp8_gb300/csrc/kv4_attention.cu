@@ -403,18 +403,20 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
           }
         }
         if (a.logits) {
+          float *row = a.logits + ((static_cast<int64_t>(p.b) * a.HK + head) * R + row0 + 2 * t) * a.max_len + tok0 + key_row;
 #pragma unroll
-          for (int mb = 0; mb < kMB; ++mb)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int c = 0; c < 2; ++c) {
+              if (row0 + nb * 8 + 2 * t + c >= R) continue;
+              float *at = row + static_cast<int64_t>(nb * 8 + c) * a.max_len;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int r = row0 + nb * 8 + 2 * t + (c & 1);
-                const int tok = tok0 + mb * 16 + key_row + (c >> 1) * 8;
-                if (r < R && tok < a.max_len)
-                  a.logits[((static_cast<int64_t>(p.b) * a.HK + head) * R + r) * a.max_len + tok] =
-                      s[mb][nb][c] * qs[nb][c & 1];
-              }
+              for (int mb = 0; mb < kMB; ++mb)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                  if (whole || tok0 + key_row + mb * 16 + half * 8 < a.max_len)
+                    at[mb * 16 + half * 8] = s[mb][nb][half * 2 + c] * qs[nb][c];
+            }
         }
         // ---- the reference that p is held to: a score of the row that no other has
         // passed by more than 8 in log2 units (p <= 2^8); what was summed follows it.
