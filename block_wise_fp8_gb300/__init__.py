@@ -859,12 +859,25 @@ def fp8bq_moe_experts(x, ids, weights, w13, s13, w2, s2, y, ws, stream=None):
 
 # ---------------------------------------------------------------- attention and its cache
 
+def _fit_all(heads, contig, dev):
+    for _, t, shape in heads:
+        if not _fit_heads(t, shape, dev):
+            return False
+    try:
+        for _, t, dtypes, shape in contig:
+            if (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or
+                    t.get_device() != dev):
+                return False
+    except AttributeError:  # None, or no tensor
+        return False
+    return True
+
+
 def _check_heads(what, dev, stream, heads, contig, optional=None):
     """`heads`: (name, tensor, shape), `contig`: (name, tensor, dtypes, shape) each;
     `optional`: one more of `contig`, whose tensor may be None."""
     more = contig if optional is None or optional[1] is None else (*contig, optional)
-    if stream is None and dev >= 0 and all(_fit_heads(t, s, dev) for _, t, s in heads) and \
-            _fits(dev, [c[1:] for c in more]):
+    if stream is None and dev >= 0 and _fit_all(heads, more, dev):
         return
     _validate(what, [_Spec(n, t, _BF16, s, kind="heads") for n, t, s in heads] +
               [_Spec(*c) for c in more], stream)
