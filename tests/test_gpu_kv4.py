@@ -451,6 +451,26 @@ def test_one_workspace_for_calls_of_any_sizes():
         assert bool(((y.double() - want).abs() <= bound).all())
 
 
+def test_empty_batches_and_tables():
+    """No sequences, block tables without a column, sequences all empty: zeros, and the
+    weights left as they were."""
+    cache = fb.new_kv4_cache(2, 2, 16, 64)
+    ws = fb.new_kv4_workspace(3, 2, 4, 2, 64, 16, weights=True)
+    w = torch.full((2, 2, 16), 3.0, device="cuda")
+    for B, width, n in ((0, 1, 0), (3, 0, 9), (3, 1, 0), (3, 1, -4)):
+        q = torch.ones(2 * B, 4, 64, dtype=BF16, device="cuda")
+        y = torch.full_like(q, 5.0)
+        table = torch.zeros(B, width, dtype=I32, device="cuda")
+        lens = torch.full((B,), n, dtype=I32, device="cuda")
+        fb.fp8bq_kv4_attention(q, cache, table, lens, y, ws, weights=w)
+        assert bool((y == 0).all()) and bool((w == 3.0).all())
+    none = torch.empty(0, 2, 64, dtype=BF16, device="cuda")
+    slots = torch.empty(0, dtype=I64, device="cuda")
+    fb.fp8bq_kv4_append(none, none, slots, cache)
+    fb.fp8bq_kv4_read(cache, slots, none, none)
+    assert fb.fp8bq_poll_status(ws) == 0 and bool((cache == 0).all())
+
+
 def test_streams_and_graphs():
     """The whole use of the cache on a stream of its own, captured and replayed with new
     lengths and rows; eager calls on the same workspace in between."""

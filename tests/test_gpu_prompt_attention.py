@@ -211,3 +211,17 @@ def test_bounds_outside_the_rows_are_clamped():
     ws = fb.new_workspace(fb.OP_PROMPT_ATTENTION, 50, 4, 64)
     fb.fp8bq_prompt_attention(q, k, v, torch.tensor([-9, 20, 10 ** 9], dtype=I32, device="cuda"), y, ws)
     check(y.double(), *reference(q, k, v, [0, 20, 50], 0.125))
+
+
+def test_no_rows_at_all():
+    """Sequences that are all empty, or none: nothing is written."""
+    g = torch.Generator("cuda").manual_seed(5)
+    q, k, v = packed(g, 50, 4, 2, 128)
+    ws = fb.new_workspace(fb.OP_PROMPT_ATTENTION, 50, 4, 128)
+    for cuts in ([0], [0, 0, 0], [50, 50], [70, 70, 90], [30, 10]):
+        y = torch.full((50, 4, 128), 7.0, dtype=BF16, device="cuda")
+        fb.fp8bq_prompt_attention(q, k, v, torch.tensor(cuts, dtype=I32, device="cuda"), y, ws)
+        assert bool((y == 7.0).all()), cuts
+    e = torch.empty(0, 4, 128, dtype=BF16, device="cuda")
+    fb.fp8bq_prompt_attention(e, e[:, :2], e[:, :2], torch.zeros(2, dtype=I32, device="cuda"), e, ws)
+    assert fb.fp8bq_poll_status(ws) == 0
