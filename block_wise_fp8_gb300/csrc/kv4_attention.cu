@@ -270,6 +270,64 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
               make_float2(m[c], l[c]);
       }
     };
+    // The warps' sums together, put(query rows nb, product j, its sums, maxima, sums of
+    // p): every warp has sums of the same values in the same places, and ends up with a
+    // quarter of them.
+    auto together = [&](const float (&m)[NB][2], const float (&l)[NB][2], auto &&put) {
+      named_bar_sync(1, kWarps * 32);  // what the memory held before has been read
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (g == 0) join_stat[warp * kRows + nb * 8 + 2 * t + c] = make_float2(m[nb][c], l[nb][c]);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          const int to = j / kQuarter, from = warp - (warp > to);  // place among the other three
+          if (to != warp)
+            join[((j * NB + nb) * 3 + from) * 32 + lane] =
+                make_float4(o[j][nb][0], o[j][nb][1], o[j][nb][2], o[j][nb][3]);
+        }
+      }
+      named_bar_sync(1, kWarps * 32);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float ma[2], la[2], by[kWarps][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float2 st2[kWarps];
+          ma[c] = -INFINITY, la[c] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            st2[w] = join_stat[w * kRows + nb * 8 + 2 * t + c];
+            ma[c] = fmaxf(ma[c], st2[w].x);
+          }
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            by[w][c] = factor(st2[w].x, ma[c]);
+            la[c] += st2[w].y * by[w][c];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kQuarter; ++k) {
+          float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {  // the warps in order, whoever sums
+            float4 x;
+            if (w == warp) {
+#pragma unroll
+              for (int q = 0; q < kWarps; ++q)
+                if (q == warp)
+                  x = make_float4(o[q * kQuarter + k][nb][0], o[q * kQuarter + k][nb][1],
+                                  o[q * kQuarter + k][nb][2], o[q * kQuarter + k][nb][3]);
+            } else {
+              x = join[(((warp * kQuarter + k) * NB + nb) * 3 + w - (w > warp)) * 32 + lane];
+            }
+            v.x += x.x * by[w][0], v.y += x.y * by[w][1], v.z += x.z * by[w][0], v.w += x.w * by[w][1];
+          }
+          put(nb, warp * kQuarter + k, v, ma, la);
+        }
+      }
+    };
     for (int f = f0; f < f1; ++f, plan.next(p)) {
       if (p.tile >= p.tiles) continue;
       // (after a wait that gave up the walk goes on, over whatever the memory holds,
@@ -574,78 +632,34 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
       if (lane == 0) mbar_arrive(&bars.empty[st]);
       if (++st == kStages) st = 0, ph ^= 1;
 
-      // ---- the item's end, or the run's: the warps' sums together.  Every warp has
-      // sums of the same values in the same places, and ends up with a quarter of them.
+      // ---- the item's end, or the run's: the warps' sums together
       const bool ends_here = p.tile + 1 == p.tiles;
       if (ends_here || f + 1 == f1) {
         const bool begun_here = f - p.tile >= f0;
-        named_bar_sync(1, kWarps * 32);  // what the memory held before has been read
+        float m[NB][2], l[NB][2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float l = sum[nb][c];
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            if (g == 0) join_stat[warp * kRows + nb * 8 + 2 * t + c] = make_float2(mx[nb][c] * qs[nb][c], l);
-          }
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j) {
-            const int to = j / kQuarter, from = warp - (warp > to);  // place among the other three
-            if (to != warp)
-              join[((j * NB + nb) * 3 + from) * 32 + lane] =
-                  make_float4(o[j][nb][0], o[j][nb][1], o[j][nb][2], o[j][nb][3]);
-          }
-        }
-        named_bar_sync(1, kWarps * 32);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float m[2], l[2], by[kWarps][2];
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float2 st[kWarps];
-            m[c] = -INFINITY, l[c] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              st[w] = join_stat[w * kRows + nb * 8 + 2 * t + c];
-              m[c] = fmaxf(m[c], st[w].x);
-            }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              by[w][c] = factor(st[w].x, m[c]);
-              l[c] += st[w].y * by[w][c];
-            }
+            m[nb][c] = mx[nb][c] * qs[nb][c];
+            l[nb][c] = sum[nb][c];
+            l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 4);
+            l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 8);
+            l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 16);
           }
-#pragma unroll
-          for (int k = 0; k < kQuarter; ++k) {
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {  // the warps in order, whoever sums
-              float4 x;
-              if (w == warp) {
-#pragma unroll
-                for (int q = 0; q < kWarps; ++q)
-                  if (q == warp)
-                    x = make_float4(o[q * kQuarter + k][nb][0], o[q * kQuarter + k][nb][1],
-                                    o[q * kQuarter + k][nb][2], o[q * kQuarter + k][nb][3]);
-              } else {
-                x = join[(((warp * kQuarter + k) * NB + nb) * 3 + w - (w > warp)) * 32 + lane];
-              }
-              v.x += x.x * by[w][0], v.y += x.y * by[w][1], v.z += x.z * by[w][0], v.w += x.w * by[w][1];
-            }
-            if (begun_here && ends_here) {  // no other CTA has a part of it
-              finish(p.b, head, row0, nb, warp * kQuarter + k, v, m, l);
-            } else {
-              float *to = a.part + (2 * static_cast<int64_t>(blockIdx.x) + begun_here) * S::kPart;
-              reinterpret_cast<float4 *>(to)[((warp * kQuarter + k) * NB + nb) * 32 + lane] = v;
-              if (k == 0 && warp == 0 && g == 0)
-                *reinterpret_cast<float4 *>(to + kRows * D + (nb * 8 + 2 * t) * 2) =
-                    make_float4(m[0], l[0], m[1], l[1]);
-            }
+        float *part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + begun_here) * S::kPart;
+        const bool alone = begun_here && ends_here;  // no other CTA has a part of it
+        together(m, l, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
+          if (alone) {
+            finish(p.b, head, row0, nb, j, v, ma, la);
+          } else {
+            reinterpret_cast<float4 *>(part)[(j * NB + nb) * 32 + lane] = v;
+            if (j == 0 && g == 0)
+              *reinterpret_cast<float4 *>(part + kRows * D + (nb * 8 + 2 * t) * 2) =
+                  make_float4(ma[0], la[0], ma[1], la[1]);
           }
-        }
-        if (!(begun_here && ends_here)) {
+        });
+        if (!alone) {
           named_bar_sync(1, kWarps * 32);
           if (tid == 0)  // (the addition releases what the barrier has gathered)
             bars.ticket[begun_here] = atom_add_acq_rel_gpu(a.tickets + p.b * plan.items + p.item, 1u);
@@ -655,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
       }
     }
     // ---- items that other CTAs have parts of: the last to leave its part sums all of
-    // them, in the order of the tokens
+    // them, every warp each fourth one in the order of the tokens (a warp's quarter of all
+    // of them, four in flight: 57 parts took 9 to 14 us)
     if (has_early || has_late) {
       named_bar_sync(1, kWarps * 32);
 #pragma unroll 1
@@ -668,38 +683,41 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         if (tid == 0) a.tickets[e.b * plan.items + e.item] = 0u;
         __threadfence();
         const int hd = e.item / blocks, r0 = (e.item - hd * blocks) * kRows;
-        // the item begins in the second slot of its first CTA, and goes on in the first
-        // one of each of the others
-        auto at = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * S::kPart; };
+        float m[NB][2], l[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          auto stat = [&](int c) {
-            return __ldcg(reinterpret_cast<const float4 *>(at(c) + kRows * D + (nb * 8 + 2 * t) * 2));
-          };
-          float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const float4 s = stat(c);
-            m[0] = fmaxf(m[0], s.x), m[1] = fmaxf(m[1], s.z);
-          }
-          float4 v[kQuarter];
+          m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.0f;
 #pragma unroll
-          for (int k = 0; k < kQuarter; ++k) v[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const float4 s = stat(c);
-            const float f0_ = factor(s.x, m[0]), f1_ = factor(s.z, m[1]);
-            l[0] += s.y * f0_, l[1] += s.w * f1_;
+          for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-            for (int k = 0; k < kQuarter; ++k) {
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(at(c)) +
-                                      ((warp * kQuarter + k) * NB + nb) * 32 + lane);
-              v[k].x += x.x * f0_, v[k].y += x.y * f1_, v[k].z += x.z * f0_, v[k].w += x.w * f1_;
+            for (int c = 0; c < 4; ++c) o[j][nb][c] = 0.0f;
+        }
+        for (int c = c0 + warp; c <= c1; c += kWarps) {
+          // the item begins in the second slot of its first CTA, and goes on in the first
+          // one of each of the others
+          const float *part = a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * S::kPart;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float4 st4 = __ldcg(reinterpret_cast<const float4 *>(part + kRows * D + (nb * 8 + 2 * t) * 2));
+            float4 x[kTiles];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+              x[j] = __ldcg(reinterpret_cast<const float4 *>(part) + (j * NB + nb) * 32 + lane);
+            const float u0 = fmaxf(m[nb][0], st4.x), u1 = fmaxf(m[nb][1], st4.z);
+            const float a0 = factor(m[nb][0], u0), a1 = factor(m[nb][1], u1);
+            const float b0 = factor(st4.x, u0), b1 = factor(st4.z, u1);
+            m[nb][0] = u0, m[nb][1] = u1;
+            l[nb][0] = l[nb][0] * a0 + st4.y * b0, l[nb][1] = l[nb][1] * a1 + st4.w * b1;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+              o[j][nb][0] = o[j][nb][0] * a0 + x[j].x * b0, o[j][nb][1] = o[j][nb][1] * a1 + x[j].y * b1;
+              o[j][nb][2] = o[j][nb][2] * a0 + x[j].z * b0, o[j][nb][3] = o[j][nb][3] * a1 + x[j].w * b1;
             }
           }
-#pragma unroll
-          for (int k = 0; k < kQuarter; ++k) finish(e.b, hd, r0, nb, warp * kQuarter + k, v[k], m, l);
         }
+        together(m, l, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
+          finish(e.b, hd, r0, nb, j, v, ma, la);
+        });
       }
     }
     // ---- sequences without a cached token: zeros
