@@ -226,7 +226,7 @@ struct Kv4AttnArgs {
   uint64_t wait_limit_ns;
   int fault;          // fault injection, as GemmArgs::fault_skip_first_load
   // set by the launcher: the workspace's parts
-  uint32_t *tickets;  // [kKv4MaxItems] CTAs that have left their part of an item
+  uint32_t *tickets;  // [kKv4MaxItems] groups that have left their part of an item
   float *part;        // unfinished items' sums
   float *stats;       // [B * HK * rows] maximum and sum (with weights)
   float *logits;      // [B * HK * rows][max_len] (with weights)

@@ -23,8 +23,7 @@
 namespace fp8bq {
 namespace {
 
-constexpr int kWarps = 4;       // consumer warps
-constexpr int kThreads = kWarps * 32 + 32;
+constexpr int kWarps = 4;       // of a group
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -59,17 +58,25 @@ struct Sizes {
   static constexpr int kRows = 8 * NB;             // query rows of an item
   static constexpr int kMB = 2;                    // blocks of 16 tokens, a warp's of a tile
   static constexpr int kTile = kWarps * 16 * kMB;  // tokens a stage holds
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? 4 : D == 128 && NB == 1 ? 3 : 2;
   static constexpr int kKvBytes = kTile * 9 * D / 8;
   static constexpr int kStageBytes = kKvBytes + kRows * D * 2;  // and an item's query rows
-  static constexpr int kPart = kRows * (D + 2);    // floats of a CTA's part of an item
+  static constexpr int kPart = kRows * (D + 2);    // floats of a group's part of an item
   // three quarters of every warp's sums, and all rows' maxima and sums
   static constexpr int kJoinBytes = 3 * kRows * D * 4 + kWarps * kRows * 8;
-  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes;  // and (B + 1) * 4
-  static constexpr int kCtas = NB == 1 && D <= 128 ? 3 : D == 256 && NB == 2 ? 1 : 2;  // an SM
+  static constexpr int kGroupBytes = kStages * kStageBytes + kJoinBytes;
+  // Groups of warps that work for themselves, and one more for the copies, which leaves
+  // its registers to them: 160 a thread, three warps on a scheduler.  (Three CTAs of four
+  // warps and a copying one: 128; two: 168.  16 sequences of 6600 tokens, 64 heads over
+  // 8, eight new tokens each: 156 us, with two such CTAs 180; with one new token 36 and
+  // with three such CTAs 37.)
+  static constexpr int kGroups = D <= 128 ? 3 : NB == 1 ? 2 : 1;
+  static constexpr int kThreads = (kGroups + 1) * 128;
+  static constexpr int kRegs = kGroups == 3 ? 160 : 232, kCopyRegs = kGroups == 3 ? 32 : 40;
+  static constexpr int kSmem = kGroups * kGroupBytes;  // and (B + 1) * 4
 };
 
-// Where a CTA is in the flattened list of slots: sequence, item of it, slot of the
+// Where a group is in the flattened list of slots: sequence, item of it, slot of the
 // item (its tiles first).
 struct Place {
   int b, item, tile, tiles;  // tiles: of each of the sequence's items
@@ -83,7 +90,7 @@ struct Bars {
 
 // The work of the batch as a list of slots: an item's tiles, and kJoinSlots more for
 // what an item costs besides (its queries, the join of the warps' sums).  first[b]
-// counts those of one item of each sequence before b.  Every CTA takes an equal run
+// counts those of one item of each sequence before b.  Every group takes an equal run
 // of the whole list (the first `more` of them one slot more), so that ragged batches
 // fill the device evenly (64 sequences of 512 to 8192 tokens, 64 heads over 8: 64 us
 // with no slots for the joins, 58.1, 56.0 and 56.7 with one, two and three).
@@ -91,20 +98,20 @@ constexpr int kJoinSlots = 2;
 struct Plan {
   const int *first;  // [B + 1]
   int B, items;      // items a sequence: HK * blocks
-  int each, more;    // slots a CTA, and CTAs with one more
-  __device__ Plan(const int *f, int B_, int items_) : first(f), B(B_), items(items_) {
+  int each, more;    // slots a group, and groups with one more
+  __device__ Plan(const int *f, int B_, int items_, int most) : first(f), B(B_), items(items_) {
     const int total = f[B_] * items_;
-    // fewer CTAs than the grid has take part where there are few slots: at least two
+    // fewer groups than there are take part where there are few slots: at least two
     // each, since a part costs as much as a tile to add to the others' (one sequence of
     // 8192 tokens, 64 heads over 8: 22.3, 17.3, 16.7 and 18.7 us with 1, 2, 4 and 6; of
     // 701: 10.4, 10.4, 11.7 and 14.2)
-    const int ctas = min((max(total, 1) + 1) / 2, static_cast<int>(gridDim.x));
-    each = total / ctas;
-    more = total - each * ctas;
+    const int active = min((max(total, 1) + 1) / 2, most);
+    each = total / active;
+    more = total - each * active;
   }
   __device__ int total() const { return first[B] * items; }
-  __device__ int start(int cta) const { return min(total(), cta * each + min(cta, more)); }
-  __device__ int cta_of(int slot) const {
+  __device__ int start(int group) const { return min(total(), group * each + min(group, more)); }
+  __device__ int group_of(int slot) const {
     const int longer = more * (each + 1);
     return slot < longer ? slot / (each + 1) : more + (slot - longer) / each;
   }
@@ -135,23 +142,28 @@ struct Plan {
 };
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kernel(const Kv4AttnArgs a) {
   using S = Sizes<D, NB>;
   constexpr int kRows = S::kRows, kStages = S::kStages, kMB = S::kMB, kTile = S::kTile;
   constexpr int kKeyWords = D / 32;       // 32-bit words of codes a lane takes of a key row
   constexpr int kTiles = D / 16;          // products of 16 values of the D
   constexpr int kValueWords = D / 64;     // words of codes a lane takes of a value row
   constexpr int kQuarter = kTiles / kWarps;
-  extern __shared__ __align__(128) uint8_t smem[];
-  float4 *join = reinterpret_cast<float4 *>(smem + kStages * S::kStageBytes);
-  float2 *join_stat = reinterpret_cast<float2 *>(join + 3 * kRows * D / 4);
-  int *first = reinterpret_cast<int *>(smem + S::kSmem);
-  __shared__ Bars bars;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  volatile uint32_t *abort = &bars.abort;
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], kWarps);
-    bars.abort = bars.never = 0;
+  constexpr int kGroups = S::kGroups, kThreads = S::kThreads;
+  extern __shared__ __align__(128) uint8_t all_smem[];
+  int *first = reinterpret_cast<int *>(all_smem + S::kSmem);
+  __shared__ Bars all_bars[kGroups];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & 3;  // of its group
+  // the last group of warps has a copying warp for each of the others
+  const bool copies = threadIdx.x >= kGroups * 128;
+  const int group = copies ? warp : threadIdx.x >> 7;
+  // what a group has as its number: neighbours are on different SMs, for when there is
+  // less work than groups
+  const int me = group * gridDim.x + blockIdx.x, everyone = kGroups * gridDim.x;
+  if (threadIdx.x < kGroups) {
+    Bars &b = all_bars[threadIdx.x];
+    for (int i = 0; i < kStages; ++i) mbar_init(&b.full[i], 1), mbar_init(&b.empty[i], kWarps);
+    b.abort = b.never = 0;
     fence_mbar_init();
   }
   griddep_launch_dependents();
@@ -160,13 +172,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
   const int R = a.G * a.Tq, blocks = (R + kRows - 1) / kRows;
   const Kv4Page pg = kv4_page(P, D);
   auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), a.max_len); };
-  for (int b = tid; b < a.B; b += kThreads) {
+  for (int b = threadIdx.x; b < a.B; b += kThreads) {
     const int tiles = (length(b) + kTile - 1) / kTile;
     first[b + 1] = tiles ? tiles + kJoinSlots : 0;
   }
-  if (tid == 0) first[0] = 0;
+  if (threadIdx.x == 0) first[0] = 0;
   __syncthreads();
-  if (warp == 0) {
+  if (threadIdx.x < 32) {
     int run = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       int v = b0 + lane < a.B ? first[b0 + lane + 1] : 0;
@@ -181,10 +193,14 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     }
   }
   __syncthreads();
-  const Plan plan(first, a.B, a.HK * blocks);
-  const int f0 = plan.start(blockIdx.x), f1 = plan.start(blockIdx.x + 1);
-
-  if (warp == kWarps) {
+  if (copies) {
+    if constexpr (kGroups > 1) setmaxnreg_dec<S::kCopyRegs>();
+    // (the group's warps beyond the others' number have no run: the list ends before it)
+    const Plan plan(first, a.B, a.HK * blocks, everyone);
+    const int f0 = plan.start(me), f1 = plan.start(me + 1);
+    Bars &bars = all_bars[min(group, kGroups - 1)];
+    volatile uint32_t *abort = &bars.abort;
+    uint8_t *smem = all_smem + group * S::kGroupBytes;
     // ---- copies: a tile's pages, each one run of bytes, into the stage, and with an
     // item's first tile its query rows
     Place p = f0 < f1 ? plan.at(f0) : Place{};
@@ -222,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
                          static_cast<int64_t>(head * a.G + row - i * a.G) * a.q_hs,
                      D * 2, &bars.full[st]);
       }
-      if (on && !(a.fault && blockIdx.x == 0 && filled == 0))
+      if (on && !(a.fault && me == 0 && filled == 0))
         bulk_load_1d(smem + st * S::kStageBytes + lane * pg.bytes,
                      a.cache + (static_cast<int64_t>(page) * a.HK + head) * pg.bytes, pg.bytes,
                      &bars.full[st]);
@@ -236,6 +252,16 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         mbar_wait(&bars.full[k % kStages], k / kStages & 1, &bars.never, a.wait_limit_ns);
     }
   } else {
+    if constexpr (kGroups > 1) setmaxnreg_inc<S::kRegs>();
+    const Plan plan(first, a.B, a.HK * blocks, everyone);
+    const int f0 = plan.start(me), f1 = plan.start(me + 1);
+    const int tid = threadIdx.x & 127;  // of the group
+    Bars &bars = all_bars[group];
+    volatile uint32_t *abort = &bars.abort;
+    uint8_t *smem = all_smem + group * S::kGroupBytes;
+    float4 *join = reinterpret_cast<float4 *>(smem + kStages * S::kStageBytes);
+    float2 *join_stat = reinterpret_cast<float2 *>(join + 3 * kRows * D / 4);
+    auto meet = [&] { named_bar_sync(1 + group, kWarps * 32); };  // the group's warps
     const int g = lane >> 2, t = lane & 3;
     // tokens of a block of 16 as the products' rows take them
     const int key_row = (g >> 1) + (g & 1) * 4;
@@ -274,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     // p): every warp has sums of the same values in the same places, and ends up with a
     // quarter of them.
     auto together = [&](const float (&m)[NB][2], const float (&l)[NB][2], auto &&put) {
-      named_bar_sync(1, kWarps * 32);  // what the memory held before has been read
+      meet();  // what the memory held before has been read
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -288,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
                 make_float4(o[j][nb][0], o[j][nb][1], o[j][nb][2], o[j][nb][3]);
         }
       }
-      named_bar_sync(1, kWarps * 32);
+      meet();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float ma[2], la[2], by[kWarps][2];
@@ -647,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
             l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 8);
             l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 16);
           }
-        float *part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + begun_here) * S::kPart;
-        const bool alone = begun_here && ends_here;  // no other CTA has a part of it
+        float *part = a.part + (2 * static_cast<int64_t>(me) + begun_here) * S::kPart;
+        const bool alone = begun_here && ends_here;  // no other group has a part of it
         together(m, l, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
           if (alone) {
             finish(p.b, head, row0, nb, j, v, ma, la);
@@ -660,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
           }
         });
         if (!alone) {
-          named_bar_sync(1, kWarps * 32);
+          meet();
           if (tid == 0)  // (the addition releases what the barrier has gathered)
             bars.ticket[begun_here] = atom_add_acq_rel_gpu(a.tickets + p.b * plan.items + p.item, 1u);
           if (begun_here) late = p, has_late = true;
@@ -668,17 +694,17 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
         }
       }
     }
-    // ---- items that other CTAs have parts of: the last to leave its part sums all of
+    // ---- items that other groups have parts of: the last to leave its part sums all of
     // them, every warp each fourth one in the order of the tokens (a warp's quarter of all
     // of them, four in flight: 57 parts took 9 to 14 us)
     if (has_early || has_late) {
-      named_bar_sync(1, kWarps * 32);
+      meet();
 #pragma unroll 1
       for (int n = 0; n < 2; ++n) {
         if (!(n ? has_late : has_early)) continue;
         const Place &e = n ? late : early;
         const int s0 = first[e.b] * plan.items + e.item * (e.tiles + kJoinSlots);
-        const int c0 = plan.cta_of(s0), c1 = plan.cta_of(s0 + e.tiles - 1);
+        const int c0 = plan.group_of(s0), c1 = plan.group_of(s0 + e.tiles - 1);
         if (bars.ticket[n] != static_cast<uint32_t>(c1 - c0)) continue;
         if (tid == 0) a.tickets[e.b * plan.items + e.item] = 0u;
         __threadfence();
@@ -693,8 +719,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
             for (int c = 0; c < 4; ++c) o[j][nb][c] = 0.0f;
         }
         for (int c = c0 + warp; c <= c1; c += kWarps) {
-          // the item begins in the second slot of its first CTA, and goes on in the first
-          // one of each of the others
+          // the item begins in the second part of its first group, and goes on in the
+          // first one of each of the others
           const float *part = a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * S::kPart;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -722,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     }
     // ---- sequences without a cached token: zeros
     const int64_t rows = static_cast<int64_t>(a.Tq) * a.HK * a.G;
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    for (int b = me; b < a.B; b += everyone) {
       if (first[b + 1] != first[b]) continue;
       for (int64_t e = tid; e < rows * (D / 4); e += kWarps * 32) {
         const int64_t row = e / (D / 4), i = row / (a.HK * a.G), h = row - i * (a.HK * a.G);
@@ -732,7 +758,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<D, NB>::kCtas) kv4_attention_k
     }
   }
   __syncthreads();
-  if (tid == 0 && *abort) atomicMax(a.status, kStatusTimeout);
+  if (threadIdx.x < kGroups && *static_cast<volatile uint32_t *>(&all_bars[threadIdx.x].abort))
+    atomicMax(a.status, kStatusTimeout);
 }
 
 // ---------------------------------------------------------------- the weights
@@ -770,7 +797,7 @@ __global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4At
 
 // ---------------------------------------------------------------- host
 
-constexpr int kMaxCtas = 3 * 160;  // more than three on each of a GB300's SMs
+constexpr int kMaxSms = 160;  // more than a GB300 has
 
 struct Layout {
   size_t tickets, part, stats, logits, total;
@@ -782,7 +809,7 @@ Layout layout(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t 
   // serves calls of several
   l.tickets = 256;
   l.part = l.tickets + kKv4MaxItems * 4;
-  l.stats = l.part + up(static_cast<size_t>(2) * kMaxCtas * 16 * (D + 2) * 4);
+  l.stats = l.part + up(static_cast<size_t>(2) * 3 * kMaxSms * 16 * (D + 2) * 4);
   const size_t rows = static_cast<size_t>(B) * HQ * Tq;
   l.logits = l.stats + (weights ? up(rows * 8) : 0);
   l.total = l.logits + (weights ? up(rows * static_cast<size_t>(max_len) * 4) : 0);
@@ -812,12 +839,19 @@ cudaError_t launch_kv4_attention(Kv4AttnArgs a, void *ws, int num_sms, cudaStrea
     using S = Sizes<D, NB>;
     cudaError_t e = allow_smem<kv4_attention_kernel<D, NB>>(S::kSmem + (kKv4MaxBatch + 1) * 4);
     if (e != cudaSuccess) return e;
+    // setmaxnreg.inc waits for registers that the block was launched with: no launch
+    // unless the compiled count covers the split
+    static const int regs = [] {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, kv4_attention_kernel<D, NB>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (S::kGroups > 1 && regs * S::kThreads < 128 * (S::kGroups * S::kRegs + S::kCopyRegs))
+      return cudaErrorInvalidConfiguration;
     const int64_t tiles = static_cast<int64_t>(a.B) * a.HK * ((R + S::kRows - 1) / S::kRows) *
                           ((a.max_len + S::kTile - 1) / S::kTile);
-    const int64_t most = static_cast<int64_t>(num_sms) * S::kCtas;
-    const int64_t grid = tiles < most ? (tiles < 1 ? 1 : tiles) : most;
+    const int64_t grid = tiles < num_sms ? (tiles < 1 ? 1 : tiles) : num_sms;
     return launch_pdl(kv4_attention_kernel<D, NB>,
-                      dim3(static_cast<unsigned>(grid < kMaxCtas ? grid : kMaxCtas)), dim3(kThreads),
+                      dim3(static_cast<unsigned>(grid < kMaxSms ? grid : kMaxSms)), dim3(S::kThreads),
                       S::kSmem + (a.B + 1) * 4, st, a);
   };
   auto by_rows = [&](auto d) {
