@@ -99,13 +99,14 @@ struct Plan {
   const int *first;  // [B + 1]
   int B, items;      // items a sequence: HK * blocks
   int each, more;    // slots a group, and groups with one more
-  __device__ Plan(const int *f, int B_, int items_, int most) : first(f), B(B_), items(items_) {
+  __device__ Plan(const int *f, int B_, int items_, int most, int least) : first(f), B(B_), items(items_) {
     const int total = f[B_] * items_;
-    // fewer groups than there are take part where there are few slots: at least two
-    // each, since a part costs as much as a tile to add to the others' (one sequence of
-    // 8192 tokens, 64 heads over 8: 22.3, 17.3, 16.7 and 18.7 us with 1, 2, 4 and 6; of
-    // 701: 10.4, 10.4, 11.7 and 14.2)
-    const int active = min((max(total, 1) + 1) / 2, most);
+    // fewer groups than there are take part where there are few slots: at least `least`
+    // each, since a part costs as much as a tile to add to the others'.  With 8 rows an
+    // item two (one sequence of 8192 tokens, 64 heads over 8: 22.3, 17.3, 16.7 and 18.7 us
+    // with 1, 2, 4 and 6; of 701: 10.4, 10.4, 11.7 and 14.2), with 16, whose parts are
+    // twice as large, three (two of 6600, four tokens each, 32 heads: 23.5 with 2, 21.9)
+    const int active = min((max(total, 1) + least - 1) / least, most);
     each = total / active;
     more = total - each * active;
   }
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
   if (copies) {
     if constexpr (kGroups > 1) setmaxnreg_dec<S::kCopyRegs>();
     // (the group's warps beyond the others' number have no run: the list ends before it)
-    const Plan plan(first, a.B, a.HK * blocks, everyone);
+    const Plan plan(first, a.B, a.HK * blocks, everyone, NB + 1);
     const int f0 = plan.start(me), f1 = plan.start(me + 1);
     Bars &bars = all_bars[min(group, kGroups - 1)];
     volatile uint32_t *abort = &bars.abort;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
     }
   } else {
     if constexpr (kGroups > 1) setmaxnreg_inc<S::kRegs>();
-    const Plan plan(first, a.B, a.HK * blocks, everyone);
+    const Plan plan(first, a.B, a.HK * blocks, everyone, NB + 1);
     const int f0 = plan.start(me), f1 = plan.start(me + 1);
     const int tid = threadIdx.x & 127;  // of the group
     Bars &bars = all_bars[group];
