@@ -14,9 +14,9 @@
 
 Every request has its own adapter (or none); the tokens are grouped by adapter
 once a step.  With a 4-bit cache the softmax weight that each cached token gets is
-added up, and `evict` keeps the heaviest and the last ones.  `python examples/decoder_layer.py` times the step on a GPU and
-prints how far it is from the same layer in 64 bits with unquantised
-activations.
+added up, and `evict` keeps the heaviest and the last ones.
+`python examples/decoder_layer.py` times the step on a GPU and prints how far it is
+from the same layer in 64 bits with unquantised activations.
 """
 from __future__ import annotations
 

@@ -451,6 +451,25 @@ def test_one_workspace_for_calls_of_any_sizes():
         assert bool(((y.double() - want).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("lens,Tq,HQ,HK", [([9000, 3], 1, 8, 2), ([5000], 4, 8, 1), ([700] * 9, 2, 16, 2)])
+def test_output_in_place_of_the_queries(lens, Tq, HQ, HK):
+    """y = q, with heads whose rows and tokens are split between CTAs."""
+    g = gen(len(lens))
+    D, page = 128, 32
+    width = -(-max(lens) // page)
+    cache = make_cache(g, len(lens) * width, HK, page, D)
+    table = table_of(g, lens, page, width, len(lens) * width)
+    lens_d = torch.tensor(lens, dtype=I32, device="cuda")
+    q = rn(g, len(lens) * Tq, HQ, D).to(BF16)
+    y = torch.empty_like(q)
+    ws = fb.new_kv4_workspace(len(lens), Tq, HQ, HK, D, width * page)
+    fb.fp8bq_kv4_attention(q, cache, table, lens_d, y, ws)
+    for _ in range(3):
+        own = q.clone()
+        fb.fp8bq_kv4_attention(own, cache, table, lens_d, own, ws)
+        assert torch.equal(own, y)
+
+
 def test_empty_batches_and_tables():
     """No sequences, block tables without a column, sequences all empty: zeros, and the
     weights left as they were."""
