@@ -7,7 +7,7 @@
 // code, beyond 6 to 6; x is the BF16 value times RN(1 / g).  A NaN among the 16
 // makes the scale NaN, so that it stays visible.
 //
-// Measured (8 heads of 128): 8192 tokens written and read back 24.2 us, over 12.8 at the
+// Measured (8 heads of 128): 8192 tokens written and read back 23.3 us, over 12.8 at the
 // copy rate; 32 sequences of up to 16384 tokens cut to 4096 by weight 194 us with the
 // read-back of what is kept, over 117.
 #include "kv4.cuh"
@@ -40,8 +40,9 @@ __device__ __forceinline__ Slot slot_of(const void *slots, int is64, int64_t t, 
 // thread has 8 values (half a group): rows, codes and scales are then whole runs of a
 // warp's lanes (with whole groups a thread 8192 tokens x 8 heads x 128 took 15 us to
 // write and 12 to read, cold), and several tokens, whose loads are in flight together:
-// 8192 tokens written and read back took 28.9, 25.4, 26.1 and 31.9 us with 1, 2, 4 and 8
-// of each, 700000 rows read 243, 211, 198 and 250 (with what goes before).
+// 8192 tokens written and read back take 23.7, 24.0 and 24.8 us with 2, 3 and 4 to write
+// (28.9 with 1 of each), 24.4 with 2 to read; 700000 rows read 210 and 198 with 2 and 4,
+// 250 with 8 (with what goes before).  The quotients two at a time: 24.6 -> 23.7.
 constexpr int kAppendTokens = 2, kReadTokens = 4;
 
 template <int D, int kRowTokens>
@@ -109,18 +110,26 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sv));
     r = __fmaf_rn(__fmaf_rn(-sv, r, 1.0f), r, r);
-    auto quotient = [&](float y) {
-      y = fminf(fmaxf(y * inv, -4096.0f), 4096.0f);  // infinities too
-      return copysignf(nearest_quotient(y, sv, r), y);  // -0 stays -0
-    };
+    // the quotients two at a time, as in nearest_quotient, of -x and -r: -0 stays -0
+    const bool huge = __uint_as_float(top << 16) * inv > 4096.0f;
+    const uint64_t minus_inv = pair(-inv, -inv), minus_r = pair(-r, -r), by = pair(sv, sv);
     uint32_t c = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      uint64_t y = mul2(pair(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xFFFF0000u)), minus_inv);
+      if (huge) {  // infinities too
+        float y0, y1;
+        unpair(y, y0, y1);
+        y = pair(fminf(fmaxf(y0, -4096.0f), 4096.0f), fminf(fmaxf(y1, -4096.0f), 4096.0f));
+      }
+      const uint64_t q = mul2(y, minus_r);
+      float q0, q1;
+      unpair(fma2(fma2(by, q, y), minus_r, q), q0, q1);
       uint32_t b;
       asm("{\n\t.reg .b8 p;\n\t.reg .b8 z;\n\tmov.b16 {z, p}, 0;\n\t"
           "cvt.rn.satfinite.e2m1x2.f32 p, %1, %2;\n\tmov.b32 %0, {p, z, z, z};\n\t}"
           : "=r"(b)
-          : "f"(quotient(__uint_as_float(v[j] & 0xFFFF0000u))), "f"(quotient(__uint_as_float(v[j] << 16))));
+          : "f"(q1), "f"(q0));
       c |= b << (8 * j);
     }
     if (!s[u].on) continue;
@@ -171,7 +180,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs
           "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
           : "=f"(lo), "=f"(hi)
           : "r"(hmul2(f[j], scale)));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[j]) : "f"(hi * gs), "f"(lo * gs));
+      unpair(mul2(pair(lo, hi), pair(gs, gs)), lo, hi);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[j]) : "f"(hi), "f"(lo));
     }
     *reinterpret_cast<uint4 *>(y + at.token(u) * ts) = make_uint4(out[0], out[1], out[2], out[3]);
   }
