@@ -76,6 +76,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float reciprocal(float x) {  // within 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -454,18 +459,17 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       tc_fence_after();
       const bool bad = *reinterpret_cast<volatile int *>(&sh.unit[k & 1].bad) != 0;
       const bool live = tok_in < half_tokens && tok < un.len;
-      const float by = 1.0f / sum;
-      uint16_t *y = live ? a.y + static_cast<int64_t>(un.start + tok) * a.y_ts +
-                               static_cast<int64_t>(un.head * G + head_in) * a.y_hs
-                         : nullptr;
+      const float by = reciprocal(sum);
+      const int64_t y_at = live ? static_cast<int64_t>(un.start + tok) * a.y_ts +
+                                      static_cast<int64_t>(un.head * G + head_in) * a.y_hs
+                                : -1;
       // by way of shared memory, so that four lanes write 64 bytes of a row (a row a
       // lane: 16 bytes of 32 rows a store).  Little code: what runs once a unit comes
       // from afar.
-      uint16_t *to[4];
+      const int piece = lane & 3;
+      int64_t to[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        to[x] = reinterpret_cast<uint16_t *>(
-            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(y), x * 8 + (lane >> 2)));
+      for (int x = 0; x < 4; ++x) to[x] = __shfl_sync(0xFFFFFFFFu, y_at, x * 8 + (lane >> 2));
 #pragma unroll 1
       for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
@@ -480,20 +484,23 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           out[lane * 4 + (x ^ (lane >> 1 & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
-        const int piece = lane & 3;
+        uint4 v[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int r = x * 8 + (lane >> 2);
-          const uint4 v = out[r * 4 + (piece ^ (r >> 1 & 3))];
-          if (to[x] && q * 32 + piece * 8 < a.D)
-            *reinterpret_cast<uint4 *>(to[x] + q * 32 + piece * 8) = v;
+          v[x] = out[r * 4 + (piece ^ (r >> 1 & 3))];
         }
+        const bool in = q * 32 + piece * 8 < a.D;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (in && to[x] >= 0) *reinterpret_cast<uint4 *>(a.y + to[x] + q * 32 + piece * 8) = v[x];
         __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free[i]);
-      if (bad && live) {  // (the row is written; an infinity or a NaN outdoes its rounding)
+      if (bad && live) {
+        uint16_t *y = a.y + y_at;  // (the row is written; an infinity or a NaN outdoes its rounding)
         for (int t = special * kKeys; t <= tok; ++t) {
           const uint16_t *v = a.v + static_cast<int64_t>(un.start + t) * a.v_ts +
                               static_cast<int64_t>(un.head) * a.v_hs;
