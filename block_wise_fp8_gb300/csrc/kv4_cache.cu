@@ -7,8 +7,8 @@
 // code, beyond 6 to 6; x is the BF16 value times RN(1 / g).  A NaN among the 16
 // makes the scale NaN, so that it stays visible.
 //
-// Measured (8 heads of 128): 8192 tokens written and read back 23.3 us, over 12.8 at the
-// copy rate; 32 sequences of up to 16384 tokens cut to 4096 by weight 194 us with the
+// Measured (8 heads of 128): 8192 tokens written and read back 23.1 us, over 12.8 at the
+// copy rate; 32 sequences of up to 16384 tokens cut to 4096 by weight 192 us with the
 // read-back of what is kept, over 117.
 #include "kv4.cuh"
 
