@@ -129,7 +129,9 @@ struct Units {
   }
 };
 
-template <int DP>
+// DP: the head size that tiles are laid out for, FULL: a.D is that, so that S has as many
+// steps (asked at each step: 2 % of 16384 tokens)
+template <int DP, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                         const __grid_constant__ CUtensorMap vm, const PromptArgs a) {
@@ -241,16 +243,16 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ---- products of row tile i: S first, then P V and the next S as one block.  The
-    // whole warp walks, so that addresses stay in uniform registers; one lane of it
-    // issues.  An MMA takes the tensor cores 67 cycles, and they queue few of them:
-    // every commit, fence or wait of the issuing thread between MMAs leaves a gap (a
-    // commit 97 cycles).  So each tile has an issuer of its own, and they pass the
-    // turn: while one commits and waits, the other's MMAs run.  (Without turns both
-    // tiles' blocks mingle, both S come late and nothing runs beside the softmax: 1.95
-    // ms for 16384 tokens, 32 heads over 4; one issuer for both: 1.62.)
+    // whole warp walks; one lane of it issues a block and its commits in one branch
+    // (each by itself under a lane's predicate: 90 cycles an MMA, which takes the tensor
+    // cores 67; 16384 tokens, 32 heads over 4: 1520 us, so 1450).  A commit takes 97
+    // cycles.  So each tile has an issuer of its own, and they pass the turn: while one
+    // commits and waits, the other's MMAs run.  (Without turns both tiles' blocks
+    // mingle, both S come late and nothing runs beside the softmax: 1950 us; one issuer
+    // for both: 1620.)  P is waited for last, with the turn in hand: once it is there
+    // nothing but the issue is left (before the turn: 1397 against 1343 us, on one GPU).
     setmaxnreg_dec<kLowRegs>();
     const int i = warp - kMmaWarp;
-    const uint32_t lead = lane == 0;
     const uint32_t s_desc = idesc_bf16(128, kKeys), o_desc = idesc_bf16(128, a.D, true);
     const uint64_t q_at = sdesc_kmajor_sw128(smem_u32(smem)) + i * (C::kTileBytes / 16);
     const uint64_t k_base = sdesc_kmajor_sw128(smem_u32(ring));
@@ -264,18 +266,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, limit));
     };
-    auto turn = [&] {
-      const bool r = wait(&sh.turn[i], tph);
-      tph ^= 1;
-      tc_fence_after();
-      return r;
-    };
     auto scores = [&](int at) {
       const uint64_t kd = k_base + at * (C::kTileBytes / 16);
 #pragma unroll
       for (int s = 0; s < DP / 16; ++s) {
         const uint64_t off = (s >> 2) * (kHalf / 16) + (s & 3) * 2;
-        if (s < steps) umma_bf16_if(lead, s_at, q_at + off, kd + off, s_desc, s > 0);
+        if (FULL || s < steps) umma_bf16(s_at, q_at + off, kd + off, s_desc, s > 0);
       }
     };
     for (int k = 0; ok; ++k) {
@@ -284,15 +280,20 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       const int tiles = __shfl_sync(0xFFFFFFFFu, sh.unit[k & 1].tiles, 0);
       const int special = __shfl_sync(0xFFFFFFFFu, sh.unit[k & 1].t0, 0) / kKeys;
       __syncwarp();
-      if (lead) mbar_arrive(&sh.u_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&sh.u_empty[k & 1]);
       if (tiles == 0) break;
-      ok = wait(&sh.kv_full[st], ring_ph) && wait(&sh.q_full[i], k & 1) && turn();
+      ok = wait(&sh.kv_full[st], ring_ph) && wait(&sh.q_full[i], k & 1) && wait(&sh.turn[i], tph);
+      tph ^= 1;
       if (!ok) break;
-      scores(st);
-      if (lead) mbar_arrive(&sh.turn[i ^ 1]);
-      umma_commit_if(lead, &sh.s_full[i]);
-      umma_commit_if(lead, &sh.kv_empty[st]);
-      if (tiles == 1) umma_commit_if(lead, &sh.q_empty[i]);
+      tc_fence_after();
+      if (elect_one()) {
+        scores(st);
+        mbar_arrive(&sh.turn[i ^ 1]);
+        umma_commit(&sh.s_full[i]);
+        umma_commit(&sh.kv_empty[st]);
+        if (tiles == 1) umma_commit(&sh.q_empty[i]);
+      }
+      __syncwarp();
       if (++st == C::kStages) st = 0, ring_ph ^= 1;
       for (int j = 0; j < tiles; ++j) {
         const int vs = st;
@@ -304,29 +305,32 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           ok = wait(&sh.v_clean[looked & 1], looked >> 1 & 1);
           ++looked;
         }
-        ok = ok && wait(&sh.p_ready[i], pph);
-        pph ^= 1;
         if (ok && j == 0) ok = wait(&sh.o_free[i], (k & 1) ^ 1);
-        ok = ok && turn();
+        ok = ok && wait(&sh.turn[i], tph) && wait(&sh.p_ready[i], pph);
+        tph ^= 1, pph ^= 1;
         if (!ok) break;
+        tc_fence_after();
         const uint64_t vd = v_base + vs * (C::kTileBytes / 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s)
-          umma_bf16_ta_if(lead, o_at, s_at + s * 8, vd + s * (2048 / 16), o_desc, j > 0 || s > 0);
-        if (more) scores(st);
-        if (lead) mbar_arrive(&sh.turn[i ^ 1]);
-        if (more) umma_commit_if(lead, &sh.s_full[i]);
-        umma_commit_if(lead, &sh.o_done[i]);
-        umma_commit_if(lead, &sh.kv_empty[vs]);
-        if (more) {
-          umma_commit_if(lead, &sh.kv_empty[st]);
-          if (j + 2 == tiles) umma_commit_if(lead, &sh.q_empty[i]);
-          if (++st == C::kStages) st = 0, ring_ph ^= 1;
+          for (int s = 0; s < kKeys / 16; ++s)
+            umma_bf16_ta(o_at, s_at + s * 8, vd + s * (2048 / 16), o_desc, j > 0 || s > 0);
+          if (more) scores(st);
+          mbar_arrive(&sh.turn[i ^ 1]);
+          if (more) umma_commit(&sh.s_full[i]);
+          umma_commit(&sh.o_done[i]);
+          umma_commit(&sh.kv_empty[vs]);
+          if (more) umma_commit(&sh.kv_empty[st]);
+          if (j + 2 == tiles) umma_commit(&sh.q_empty[i]);
         }
+        __syncwarp();
+        if (more && ++st == C::kStages) st = 0, ring_ph ^= 1;
       }
     }
-    umma_commit_if(lead, &sh.done[i]);
-    if (lead) mbar_wait(&sh.done[i], 0, &sh.never, limit);
+    if (elect_one()) {
+      umma_commit(&sh.done[i]);
+      mbar_wait(&sh.done[i], 0, &sh.never, limit);
+    }
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: a thread a row of tile i
@@ -537,21 +541,23 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, int num_sms, cudaStream
   const int64_t blocks = (a.T + 2 * half_tokens - 1) / (2 * half_tokens) + a.S;
   const int64_t most = blocks * a.HK;
   const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
-  auto run = [&](auto d) {
+  auto run = [&](auto d, auto full) {
     constexpr int DP = decltype(d)::value;
-    cudaError_t e = allow_smem<prompt_attention_kernel<DP>>(Cfg<DP>::kSmem);
+    constexpr bool FULL = decltype(full)::value;
+    cudaError_t e = allow_smem<prompt_attention_kernel<DP, FULL>>(Cfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc waits for registers that the block was launched with: no launch
     // unless the compiled count covers the split
     static const int regs = [] {
       cudaFuncAttributes fa;
-      return cudaFuncGetAttributes(&fa, prompt_attention_kernel<DP>) == cudaSuccess ? fa.numRegs : 0;
+      return cudaFuncGetAttributes(&fa, prompt_attention_kernel<DP, FULL>) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs * kThreads < 256 * kHighRegs + 128 * kLowRegs) return cudaErrorInvalidConfiguration;
-    return launch_pdl(prompt_attention_kernel<DP>, dim3(grid), dim3(kThreads), Cfg<DP>::kSmem, st, qm,
+    return launch_pdl(prompt_attention_kernel<DP, FULL>, dim3(grid), dim3(kThreads), Cfg<DP>::kSmem, st, qm,
                       km, vm, a);
   };
-  return a.D <= 64 ? run(std::integral_constant<int, 64>{}) : run(std::integral_constant<int, 128>{});
+  auto by_fit = [&](auto d) { return a.D == decltype(d)::value ? run(d, std::true_type{}) : run(d, std::false_type{}); };
+  return a.D <= 64 ? by_fit(std::integral_constant<int, 64>{}) : by_fit(std::integral_constant<int, 128>{});
 }
 
 }  // namespace fp8bq
