@@ -19,14 +19,13 @@
 // P is rounded to BF16 (half a step, 2^-8 of a p): kind::f16 takes both operands in
 // one type, and V is BF16.
 //
-// Measured: 16384 tokens, 32 heads over 4 of 128: 1.46 ms, 1.50 PFLOP/s of what the
-// causal triangle needs, 0.77 of cuBLAS's BF16 rate (in a stream of such calls 1.52 ms,
-// at the power cap, where cuBLAS has 1.74 PFLOP/s).  A pair of steps takes 3200 to
-// 3400 cycles, of which the tensor cores' 2150; the rest is the softmax that does not
-// hide and the waits of the hand-overs, with 36 % of the issue slots used.  A unit's
-// end costs 4400 more: nine ragged prompts of 4099 tokens together, 64 heads over 8,
-// take 85 us, 0.40 of that rate.  CTA pairs sharing K and V (cta_group::2) gain 2 %
-// (1473 against 1500 us) and are left out.
+// Measured: 16384 tokens, 32 heads over 4 of 128: 1.27 ms, 1.73 PFLOP/s of what the
+// causal triangle needs, 0.88 of cuBLAS's BF16 rate (in a stream of such calls 1.34 ms,
+// at the power cap, where cuBLAS has 1.74 PFLOP/s).  A pair of steps takes 2630 cycles,
+// of which the tensor cores' 2150: a tile's chain is 1200 for its softmax, 150 until its
+// products begin and 1280 until the next scores are there.  A unit's end costs some 4000
+// more: nine ragged prompts of 4099 tokens together, 64 heads over 8, take 74 us, 0.46 of
+// that rate.  CTA pairs sharing K and V (cta_group::2) gained 2 % and are left out.
 #include "common.cuh"
 #include "ptx.cuh"
 
