@@ -103,8 +103,11 @@ class Layer:
                         self.slots(torch.arange(M, device="cuda")[:, None], at).flatten())
 
     def slots(self, request, at):
-        """Slots of the requests' tokens `at`, by the block table."""
-        return self.pages.long()[request, at // self.page] * self.page + at % self.page
+        """Slots of the requests' tokens `at`, by the block table; -1, which a write leaves
+        out, behind its end."""
+        width = self.pages.shape[1]
+        pages = self.pages.long()[request, (at // self.page).clamp(max=width - 1)]
+        return torch.where(at < width * self.page, pages * self.page + at % self.page, -1)
 
     def write_rows(self, k, v, slots):
         fb.fp8bq_kv4_append(k, v, slots, self.cache4, weights=self.weights)
@@ -265,7 +268,8 @@ def main():
             layer.step(*args)
         end.record()
         torch.cuda.synchronize()
-        print(f"{M:3d} tokens{', 4-bit cache' if cache4 else ''}: {start.elapsed_time(end) * 20:.0f} us a step; relative error of the "
+        print(f"{M:3d} tokens{', 4-bit cache' if cache4 else ''}: "
+              f"{start.elapsed_time(end) * 20:.0f} us a step; relative error of the "
               f"output {err[0]:.3f}, of the residual {err[1]:.4f}")
 
 

@@ -93,3 +93,17 @@ def test_prompt_rows_into_the_cache():
     size = torch.einsum("hj,jhd->hd", p, v4.double().abs().repeat_interleave(g, 1))
     # half a step of BF16 for the output, of FP16 for the weights, and FP32 sums
     assert bool(((y[0].double() - exact).abs() <= exact.abs() * 2.0 ** -8 + size * 2.0 ** -10).all())
+
+
+def test_slots_behind_the_table():
+    """A request without room: its token is left out, and the pages stay as they were."""
+    layer = decoder_layer.Layer(3, context=45, cache4=True, page=16, **SIZES)
+    room = layer.pages.shape[1] * 16
+    layer.lens.copy_(torch.tensor([room, 45, room + 40]))
+    got = layer.slots(torch.arange(3, device="cuda"), layer.lens.long())
+    assert got[0] == got[2] == -1 and got[1] == int(layer.pages[1, 2]) * 16 + 13
+    before = layer.cache4.clone()
+    layer.step(*decoder_layer.inputs(layer, adapters=4))
+    assert fb.fp8bq_poll_status(layer.ws_kv4) == 0
+    changed = (layer.cache4 != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert changed == [int(layer.pages[1, 2])]
