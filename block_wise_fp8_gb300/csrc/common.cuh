@@ -228,8 +228,8 @@ struct Kv4AttnArgs {
   // set by the launcher: the workspace's parts
   uint32_t *tickets;  // [kKv4MaxItems] groups that have left their part of an item
   float *part;        // unfinished items' sums
-  float *stats;       // [B * HK * rows] maximum and sum (with weights)
-  float *logits;      // [B * HK * rows][max_len] (with weights)
+  float *stats;       // [B * HK * rows] maximum, its scale and sum, 4 floats (with weights)
+  float *logits;      // [B * HK * rows][max_len] products, before the scale (with weights)
 };
 size_t kv4_workspace(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t max_len,
                      bool weights);

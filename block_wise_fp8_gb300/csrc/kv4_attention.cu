@@ -70,7 +70,7 @@ struct Sizes {
   static constexpr int kStages = D == 64 ? 4 : D == 128 && NB == 1 ? 3 : 2;
   static constexpr int kKvBytes = kTile * 9 * D / 8;
   static constexpr int kStageBytes = kKvBytes + kRows * D * 2;  // and an item's query rows
-  static constexpr int kPart = kRows * (D + 2);    // floats of a group's part of an item
+  static constexpr int kPart = kRows * (D + 3);    // floats of a group's part of an item
   // three quarters of every warp's sums, and all rows' maxima and sums
   static constexpr int kJoinBytes = 3 * kRows * D * 4 + kWarps * kRows * 8;
   static constexpr int kGroupBytes = kStages * kStageBytes + kJoinBytes;
@@ -287,10 +287,16 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
     Place early = p, late = p;    // items with parts elsewhere: before this run, behind it
     bool has_early = false, has_late = false;
     // what a part with maximum m counts under the maximum of all (one with nothing seen
-    // holds zeros, or the NaN that a row was given)
-    auto factor = [](float m, float all) { return m == -INFINITY ? (all == -INFINITY ? 1.0f : 0.0f) : ex2(m - all); };
+    // holds zeros, or the NaN that a row was given).  Maxima are kept as they come out of
+    // the products, as within a warp: all parts of a row have its scale in common, and the
+    // scaled ones may pass FP32's range, or differ by less than their last place.
+    auto factor = [](float m, float all, float by) {
+      const float d = m == all ? 0.0f : m - all;  // (both may be -inf)
+      return ex2(d * by);
+    };
     // product j of query rows nb * 8 + 2t, + 1 of an item: two values of each
-    auto finish = [&](int b, int hd, int r0, int nb, int j, float4 v, const float (&m)[2], const float (&l)[2]) {
+    auto finish = [&](int b, int hd, int r0, int nb, int j, float4 v, const float (&m)[2], const float (&l)[2],
+                      const float (&qb)[NB][2]) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = r0 + nb * 8 + 2 * t + c;
@@ -303,14 +309,15 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
                                       static_cast<int64_t>(hd * a.G + r - i * a.G) * a.y_hs +
                                       g * (D / 8) + 2 * j) = out;
         if (a.stats && j == 0 && g == 0)
-          *reinterpret_cast<float2 *>(a.stats + ((static_cast<int64_t>(b) * a.HK + hd) * R + r) * 2) =
-              make_float2(m[c], l[c]);
+          *reinterpret_cast<float4 *>(a.stats + ((static_cast<int64_t>(b) * a.HK + hd) * R + r) * 4) =
+              make_float4(m[c], qb[nb][c], l[c], 0.0f);
       }
     };
     // The warps' sums together, put(query rows nb, product j, its sums, maxima, sums of
     // p): every warp has sums of the same values in the same places, and ends up with a
     // quarter of them.
-    auto together = [&](const float (&m)[NB][2], const float (&l)[NB][2], auto &&put) {
+    auto together = [&](const float (&m)[NB][2], const float (&l)[NB][2], const float (&qb)[NB][2],
+                        auto &&put) {
       meet();  // what the memory held before has been read
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
           }
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            by[w][c] = factor(st2[w].x, ma[c]);
+            by[w][c] = factor(st2[w].x, ma[c], qb[nb][c]);
             la[c] += st2[w].y * by[w][c];
           }
         }
@@ -399,8 +406,9 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
           const int e = top >> 7;
           const int up = e == 255 ? 0 : 14 + 127 - max(e, 24);
           const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          // (never 0: -inf times it has to stay -inf)
-          const float back = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale_log2, 1.2e-38f);
+          // (never 0: -inf times it has to stay -inf; nor infinite: 0 times it has to stay 0)
+          const float back = fminf(
+              fmaxf(__uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale_log2, 1.2e-38f), 3.4e38f);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             qs[nb][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + c) * 4);
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                   if (whole || tok0 + key_row + mb * 16 + half * 8 < a.max_len)
-                    at[mb * 16 + half * 8] = s[mb][nb][half * 2 + c] * qs[nb][c];
+                    at[mb * 16 + half * 8] = s[mb][nb][half * 2 + c];
             }
         }
         // ---- the reference that p is held to: a score of the row that no other has
@@ -673,12 +681,15 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
       const bool ends_here = p.tile + 1 == p.tiles;
       if (ends_here || f + 1 == f1) {
         const bool begun_here = f - p.tile >= f0;
-        float m[NB][2], l[NB][2];
+        // (scales in registers of their own: with the loop's, 8 sequences of up to 131072
+        // tokens take 111.3 us, so 109.2)
+        float m[NB][2], l[NB][2], qj[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            m[nb][c] = mx[nb][c] * qs[nb][c];
+            asm volatile("mov.b32 %0, %1;" : "=f"(qj[nb][c]) : "f"(qs[nb][c]));
+            m[nb][c] = mx[nb][c];
             l[nb][c] = sum[nb][c];
             l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 4);
             l[nb][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][c], 8);
@@ -686,14 +697,17 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
           }
         float *part = a.part + (2 * static_cast<int64_t>(me) + begun_here) * S::kPart;
         const bool alone = begun_here && ends_here;  // no other group has a part of it
-        together(m, l, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
+        together(m, l, qj, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
           if (alone) {
-            finish(p.b, head, row0, nb, j, v, ma, la);
+            finish(p.b, head, row0, nb, j, v, ma, la, qj);
           } else {
             reinterpret_cast<float4 *>(part)[(j * NB + nb) * 32 + lane] = v;
-            if (j == 0 && g == 0)
+            if (j == 0 && g == 0) {
               *reinterpret_cast<float4 *>(part + kRows * D + (nb * 8 + 2 * t) * 2) =
                   make_float4(ma[0], la[0], ma[1], la[1]);
+              *reinterpret_cast<float2 *>(part + kRows * (D + 2) + nb * 8 + 2 * t) =
+                  make_float2(qj[nb][0], qj[nb][1]);
+            }
           }
         });
         if (!alone) {
@@ -720,9 +734,12 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
         if (tid == 0) a.tickets[e.b * plan.items + e.item] = 0u;
         __threadfence();
         const int hd = e.item / blocks, r0 = (e.item - hd * blocks) * kRows;
-        float m[NB][2], l[NB][2];
+        float m[NB][2], l[NB][2], qb[NB][2];
+        const float *part0 = a.part + (2 * static_cast<int64_t>(c0) + 1) * S::kPart;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          const float2 by2 = __ldcg(reinterpret_cast<const float2 *>(part0 + kRows * (D + 2) + nb * 8 + 2 * t));
+          qb[nb][0] = by2.x, qb[nb][1] = by2.y;
           m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.0f;
 #pragma unroll
           for (int j = 0; j < kTiles; ++j)
@@ -741,8 +758,8 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
             for (int j = 0; j < kTiles; ++j)
               x[j] = __ldcg(reinterpret_cast<const float4 *>(part) + (j * NB + nb) * 32 + lane);
             const float u0 = fmaxf(m[nb][0], st4.x), u1 = fmaxf(m[nb][1], st4.z);
-            const float a0 = factor(m[nb][0], u0), a1 = factor(m[nb][1], u1);
-            const float b0 = factor(st4.x, u0), b1 = factor(st4.z, u1);
+            const float a0 = factor(m[nb][0], u0, qb[nb][0]), a1 = factor(m[nb][1], u1, qb[nb][1]);
+            const float b0 = factor(st4.x, u0, qb[nb][0]), b1 = factor(st4.z, u1, qb[nb][1]);
             m[nb][0] = u0, m[nb][1] = u1;
             l[nb][0] = l[nb][0] * a0 + st4.y * b0, l[nb][1] = l[nb][1] * a1 + st4.w * b1;
 #pragma unroll
@@ -752,8 +769,8 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
             }
           }
         }
-        together(m, l, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
-          finish(e.b, hd, r0, nb, j, v, ma, la);
+        together(m, l, qb, [&](int nb, int j, const float4 &v, const float (&ma)[2], const float (&la)[2]) {
+          finish(e.b, hd, r0, nb, j, v, ma, la, qb);
         });
       }
     }
@@ -775,12 +792,13 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
 
 // ---------------------------------------------------------------- the weights
 
-// weights[page][head][place] += sum over the query rows of exp2(s - max) / sum, from
-// the scores that the attention left: a thread has one cached token.  A thread is
+// weights[page][head][place] += sum over the query rows of exp2((s - max) * scale) / sum,
+// from the products that the attention left: a thread has one cached token.  A thread is
 // the only one to add to its place, unless sequences share a page.
 constexpr int kWeightThreads = 256;
 __global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4AttnArgs a) {
   __shared__ float2 stat[kKv4MaxRows];
+  __shared__ float inv[kKv4MaxRows];
   griddep_launch_dependents();
   griddep_wait();
   const int R = a.G * a.Tq, h = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
@@ -788,9 +806,9 @@ __global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4At
   if (blockIdx.x * kWeightThreads >= len) return;
   const int64_t bh = static_cast<int64_t>(b) * a.HK + h;
   for (int r = threadIdx.x; r < R; r += kWeightThreads) {
-    const float2 ml = *reinterpret_cast<const float2 *>(a.stats + (bh * R + r) * 2);
-    // a row that sees nothing adds nothing
-    stat[r] = make_float2(ml.x, ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
+    const float4 row = *reinterpret_cast<const float4 *>(a.stats + (bh * R + r) * 4);
+    stat[r] = make_float2(row.x, row.y);
+    inv[r] = row.z == 0.0f ? 0.0f : 1.0f / row.z;  // a row that sees nothing adds nothing
   }
   __syncthreads();
   const int tok = blockIdx.x * kWeightThreads + threadIdx.x;
@@ -801,7 +819,7 @@ __global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4At
   float w = 0.0f;
   for (int r = 0; r < R; ++r) {
     const float v = s[static_cast<int64_t>(r) * a.max_len];
-    if (v != -INFINITY) w += ex2(v - stat[r].x) * stat[r].y;
+    if (v != -INFINITY) w += ex2((v - stat[r].x) * stat[r].y) * inv[r];
   }
   atomicAdd(a.weights + ((static_cast<int64_t>(page) * a.HK + h) << a.page_log2) + (tok & ((1 << a.page_log2) - 1)), w);
 }
@@ -820,9 +838,9 @@ Layout layout(int64_t B, int64_t Tq, int64_t HQ, int64_t HK, int64_t D, int64_t 
   // serves calls of several
   l.tickets = 256;
   l.part = l.tickets + kKv4MaxItems * 4;
-  l.stats = l.part + up(static_cast<size_t>(2) * 3 * kMaxSms * 16 * (D + 2) * 4);
+  l.stats = l.part + up(static_cast<size_t>(2) * 3 * kMaxSms * 16 * (D + 3) * 4);
   const size_t rows = static_cast<size_t>(B) * HQ * Tq;
-  l.logits = l.stats + (weights ? up(rows * 8) : 0);
+  l.logits = l.stats + (weights ? up(rows * 16) : 0);
   l.total = l.logits + (weights ? up(rows * static_cast<size_t>(max_len) * 4) : 0);
   return l;
 }
