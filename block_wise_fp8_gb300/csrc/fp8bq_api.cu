@@ -1043,7 +1043,8 @@ int fp8bq_kv4_append(const void *k, int64_t k_ts, int64_t k_hs, const void *v, i
                      int64_t v_hs, const void *slots, int slot_bits, void *cache, int64_t pages,
                      int64_t page, float *weights, float k_scale, float v_scale, int64_t T,
                      int64_t HK, int64_t D, void *stream) {
-  if (T < 0 || T > (int64_t(1) << 31) - 1 || !positive(k_scale) || !positive(v_scale))
+  if (T < 0 || T > (int64_t(1) << 31) - 1 || !positive(k_scale) || !positive(v_scale) ||
+      !positive(1.0f / k_scale) || !positive(1.0f / v_scale))  // (rows are multiplied by these)
     return FP8BQ_ERR_SHAPE;
   RETURN_IF(check_kv4_sizes(pages, page, HK, D));
   if (slot_bits != 32 && slot_bits != 64) return FP8BQ_ERR_UNSUPPORTED;

@@ -607,8 +607,9 @@ FP8BQ_API int fp8bq_prompt_attention(const void *q, int64_t q_ts, int64_t q_hs, 
  *   s = max(E4M3(min(max|x'| / 6, 448)), 2^-9), code = E2M1(x' / s)
  * with a binary32 division for the scale, nearest even, and the code of the exact
  * quotient, ties to the even code, beyond 6 to 6 (infinities too); a NaN makes the
- * group's scale NaN.  weights (may be NULL): zeroed for the slots written.  Two rows
- * for one slot leave it unspecified. */
+ * group's scale NaN.  1 / k_scale and 1 / v_scale have to be finite in binary32, which
+ * scales up to 2^-128 are too small for (ERR_SHAPE).  weights (may be NULL): zeroed for
+ * the slots written.  Two rows for one slot leave it unspecified. */
 FP8BQ_API int fp8bq_kv4_append(const void *k, int64_t k_ts, int64_t k_hs, const void *v,
                                int64_t v_ts, int64_t v_hs, const void *slots, int slot_bits,
                                void *cache, int64_t pages, int64_t page, float *weights,
