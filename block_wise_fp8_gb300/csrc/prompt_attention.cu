@@ -64,7 +64,7 @@ struct Shared {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
   uint64_t v_clean[2], u_full[2], u_empty[2], turn[2], done[2];
-  uint32_t abort, never, tmem, pad;
+  uint32_t abort, tmem;
   Unit unit[2];
   int bound[kMaxPrompts + 1];
   int blocks[kMaxPrompts];
@@ -152,7 +152,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       mbar_init(&sh.turn[i], 1), mbar_init(&sh.done[i], 1);
     }
     for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 2);
-    sh.abort = sh.never = 0;
+    sh.abort = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -182,7 +182,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     units.total = units.above(0, lane) * a.HK;
     const int64_t grid = gridDim.x, cta = blockIdx.x;
     const uint32_t q_bytes = C::kHalves * half_tokens * G * 128;
-    int64_t c = 0;  // copies into the ring so far
+    int64_t c = 0;         // copies into the ring so far
+    uint32_t queries = 0;  // and of queries, the row tiles in turn
     bool ok = true;
     int k = 0;
     auto ring_copy = [&](const CUtensorMap *map, int head, int row, bool skip) {
@@ -220,6 +221,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
             ok = mbar_wait(&sh.q_empty[i], (k & 1) ^ 1, abort, limit);
             if (!ok) break;
             mbar_arrive_expect_tx(&sh.q_full[i], q_bytes);
+            ++queries;
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
               tma_load_3d(smem + i * C::kTileBytes + h * kHalf, &qm, &sh.q_full[i], h * 64,
@@ -234,10 +236,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok || un.tiles == 0) break;
     }
-    if (lane == 0 && *abort) {  // copies in flight land before the memory is given up
+    if (lane == 0) {
+      // Copies in flight land before the memory is given up, also those that nobody waits
+      // for any more: another role may give up at any time, after the last copy too.
       for (int64_t i = c < C::kStages ? 0 : c - C::kStages; i < c; ++i)
-        mbar_wait(&sh.kv_full[i % C::kStages], i / C::kStages & 1, &sh.never, limit);
-      for (int i = 0; i < 2 && k > 0; ++i) mbar_wait(&sh.q_full[i], (k - 1) & 1, &sh.never, limit);
+        mbar_wait_alone(&sh.kv_full[i % C::kStages], i / C::kStages & 1, limit);
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i)
+        if (queries > i) mbar_wait_alone(&sh.q_full[i], (queries - 1 - i) >> 1 & 1, limit);
     }
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -328,7 +334,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
     }
     if (elect_one()) {
       umma_commit(&sh.done[i]);
-      mbar_wait(&sh.done[i], 0, &sh.never, limit);
+      mbar_wait_alone(&sh.done[i], 0, limit);
     }
     __syncwarp();
   } else if (warp < 8) {

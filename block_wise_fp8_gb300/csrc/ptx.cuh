@@ -92,6 +92,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
   }
 }
 
+// The same whatever the other roles do: for what has to be over before a block gives
+// its memory up.
+__device__ __forceinline__ bool mbar_wait_alone(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // relaxed (morally strong) GPU-scope 32-bit store and load: a value written by
 // one CTA and polled by another without a fence, each element its own flag
 __device__ __forceinline__ void st_relaxed_gpu(uint32_t *p, uint32_t v) {
