@@ -93,7 +93,7 @@ struct Place {
 
 struct Bars {
   uint64_t full[4], empty[4];
-  uint32_t abort, never, ticket[2];
+  uint32_t abort, ticket[2];
   uint32_t pages[4];  // which pages of a stage's tile are there
 };
 
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
   if (threadIdx.x < kGroups) {
     Bars &b = all_bars[threadIdx.x];
     for (int i = 0; i < kStages; ++i) mbar_init(&b.full[i], 1), mbar_init(&b.empty[i], kWarps);
-    b.abort = b.never = 0;
+    b.abort = 0;
     fence_mbar_init();
   }
   griddep_launch_dependents();
@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
       plan.next(p);
       if (f + 1 < f1) page = look_up();
     }
-    if (*abort) {  // copies in flight land before the memory is given up
-      for (int k = max(filled - kStages, 0); k < filled; ++k)
-        mbar_wait(&bars.full[k % kStages], k / kStages & 1, &bars.never, a.wait_limit_ns);
-    }
+    // copies in flight land before the memory is given up, also those that nobody waits for
+    // any more: the group may give up at any time, after the last copy too
+    for (int k = max(filled - kStages, 0); k < filled; ++k)
+      mbar_wait_alone(&bars.full[k % kStages], k / kStages & 1, a.wait_limit_ns);
   } else {
     if constexpr (kGroups > 1) setmaxnreg_inc<S::kRegs>();
     const Plan plan(first, a.B, a.HK * blocks, everyone, NB + 1);
