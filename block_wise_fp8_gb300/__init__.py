@@ -944,7 +944,8 @@ def fp8bq_kv4_append(k, v, slots, cache, weights=None, k_scale: float = 1.0, v_s
                      stream=None):
     """Writes rows k, v [T, HK, D] into the slots (page * page size + place, int32 or
     int64 [T]; one outside the cache is left out) of a 4-bit cache; `weights` [pages,
-    HK, page size], if given, is zeroed there."""
+    HK, page size], if given, is zeroed there.  1 / k_scale and 1 / v_scale have to be
+    finite in FP32."""
     T, HK, D, pages, page, dev, bits = _rows_check("fp8bq_kv4_append", k, v, slots, cache, weights,
                                                    stream)
     kt, kh, _ = k.stride()
@@ -1017,7 +1018,9 @@ def fp8bq_kv4_evict(cache, table, lens, weights, new_table, new_lens, kept, rece
     """Keeps kept.shape[2] of each sequence's tokens for every head: the last `recent`
     and those of the largest weights, copied in order to the pages of new_table int32
     [B, width'] (pages that nothing else uses).  new_lens int32 [B], kept int32
-    [B, HK, budget]: the tokens' places before, then -1.  D: the heads' size."""
+    [B, HK, budget]: the tokens' places before, then -1.  D: the heads' size.  Every token
+    that lens counts has to have its page; leave missing pages out of table, and their
+    tokens out of lens, first."""
     pages, HK, page = _cache_sizes(cache, D)
     B, width = _mat(table, "table")
     new_width = _mat(new_table, "new_table")[1]

@@ -659,7 +659,12 @@ FP8BQ_API size_t fp8bq_kv4_workspace_bytes(int64_t B, int64_t Tq, int64_t HQ, in
  * names, which must not be pages that a sequence of the call still reads.  A sequence of
  * no more than `budget` tokens is copied whole.  new_lens: int32 [B] = min(len, budget)
  * (not lens itself: ERR_SHAPE); kept: int32 [B, HK, budget], the tokens' places before,
- * ascending, then -1.  A token whose old or new page is not there is not copied.
+ * ascending, then -1.
+ * Every token that lens counts has to have its page: one that lay in a page outside
+ * [0, pages) may be kept without anything to copy, and queries over new_table would see
+ * what its place there held before.  Such pages are left out first: a table without them,
+ * with their tokens taken off lens, is the same to every query.  A token whose new page
+ * is not there is not copied, and no query sees it.
  * 0 <= recent <= budget, budget >= 1, new_width * page >= budget, B <= 1024
  * (ERR_SHAPE).  Two launches. */
 FP8BQ_API int fp8bq_kv4_evict(void *cache, int64_t pages, int64_t page, const int32_t *table,
