@@ -12,8 +12,10 @@
 // from shared memory: the cache's rows are the wide side (16 tokens, or 16 of the D
 // values), the query rows the narrow one (8).  code * scale is exact in FP16.  A
 // query row is scaled by a power of two so that its largest value lies in [2^14,
-// 2^15); what FP16 then drops lies 2^-39 below that.  p is rounded to FP16 (half a
-// step: 2^-11 of a p, 2^-25 of the largest); sums, maxima and the statistics are FP32.
+// 2^15); what FP16 then drops lies 2^-39 below that.  p is rounded to FP16, 2^7 times as
+// large as it is (half a step: 2^-11 of a p, 2^-32 of the largest), since the tokens
+// beside one that draws nearly all of the weight may be what the row is made of; sums,
+// maxima and the statistics are FP32.
 //
 // The order of the D values is free in the first product and that of the tokens in
 // the second, so a lane takes D/4 neighbouring values of a key row, and D/8 of a
@@ -55,6 +57,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 constexpr float kGrowth = 8.0f;  // log2: how far a score may pass a row's reference
+constexpr float kLift = 7.0f;    // log2: p at the reference; p <= 2^15, which FP16 has room for
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
             }
         }
         // ---- the reference that p is held to: a score of the row that no other has
-        // passed by more than 8 in log2 units (p <= 2^8); what was summed follows it.
+        // passed by more than 8 in log2 units; what was summed follows it.
         // (The difference is taken before the scale, so that it is exact where it is
         // small, however large the scores are.)
         bool grew = false;
@@ -571,8 +574,8 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
 #pragma unroll
           for (int mb = 0; mb < kMB; ++mb) {
             float p0, p1, p2, p3;
-            unpair(mul2(add2(pair(s[mb][nb][0], s[mb][nb][1]), ref), by), p0, p1);
-            unpair(mul2(add2(pair(s[mb][nb][2], s[mb][nb][3]), ref), by), p2, p3);
+            unpair(fma2(add2(pair(s[mb][nb][0], s[mb][nb][1]), ref), by, pair(kLift, kLift)), p0, p1);
+            unpair(fma2(add2(pair(s[mb][nb][2], s[mb][nb][3]), ref), by, pair(kLift, kLift)), p2, p3);
             p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
             sum[nb][0] += p0 + p2, sum[nb][1] += p1 + p3;
             pf[mb][nb][0] = transpose8x8(pack_f16(p0, p1));
@@ -796,6 +799,7 @@ __global__ void __launch_bounds__(Sizes<D, NB>::kThreads, 1) kv4_attention_kerne
 // from the products that the attention left: a thread has one cached token.  A thread is
 // the only one to add to its place, unless sequences share a page.
 constexpr int kWeightThreads = 256;
+static_assert(kLift == 7.0f, "the weights are divided by sums of 2^7 p");
 __global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4AttnArgs a) {
   __shared__ float2 stat[kKv4MaxRows];
   __shared__ float inv[kKv4MaxRows];
@@ -808,7 +812,8 @@ __global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4At
   for (int r = threadIdx.x; r < R; r += kWeightThreads) {
     const float4 row = *reinterpret_cast<const float4 *>(a.stats + (bh * R + r) * 4);
     stat[r] = make_float2(row.x, row.y);
-    inv[r] = row.z == 0.0f ? 0.0f : 1.0f / row.z;  // a row that sees nothing adds nothing
+    // (the sum's p are 2^kLift times as large; a row that sees nothing adds nothing)
+    inv[r] = row.z == 0.0f ? 0.0f : 128.0f / row.z;
   }
   __syncthreads();
   const int tok = blockIdx.x * kWeightThreads + threadIdx.x;

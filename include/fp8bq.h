@@ -630,7 +630,7 @@ FP8BQ_API int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, con
  *   y = sum_j softmax_j(scale * q . k_j) v_j;
  * a query that sees none gets zeros.  y may be q itself (same pointer and strides).
  * FP32 scores, maxima and sums; the weights enter the second product in FP16 (half a
- * step: 2^-11 of a weight, 2^-25 of the row's largest).  What the cache holds behind a
+ * step: 2^-11 of a weight, 2^-32 of the row's largest).  What the cache holds behind a
  * sequence's end, or in pages that are not there, has no part in y, whatever it is.
  * weights (may be NULL): each seen token's entry of its page and head grows by the sum
  * of its softmax weights over the head's HQ / HK * Tq query rows (where sequences
