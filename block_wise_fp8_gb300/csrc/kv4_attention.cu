@@ -21,14 +21,17 @@
 // the second, so a lane takes D/4 neighbouring values of a key row, and D/8 of a
 // value row, each lane's from one or two groups, with wide loads free of conflicts.
 //
-// Measured (64 heads over 8 of 128): 8 sequences of up to 131072 tokens 108 us, 0.71 of
+// Measured (64 heads over 8 of 128): 8 sequences of up to 131072 tokens 109 us, 0.71 of
 // the copy rate; 64 of 512 to 8192 54 us, 0.58; one of 701 9.7 us.  Of a long run's time
 // the issue slots are half busy and the ALU, which unpacks the codes, 46 %: latency of
-// the three warps on a scheduler is what is left.  Four groups of 112 registers and two
-// stages: 105 and 53.7, but 10.8, and 15.0 against 13.3 for 16 sequences of 1000.
+// the three warps on a scheduler is what is left.  (Four groups of 112 registers and two
+// stages, where three groups had 108 and 54.5, 10.0 and 13.3: 105 and 53.7, but 10.8, and
+// 15.0 for 16 sequences of 1000.)
 //
-// Query rows an item: 8 up to 8 rows of a head, else 16, which share the unpacking (16
-// sequences of 6600 tokens, 4 x 4 rows: 56 us; as two items of 8: 61).
+// Query rows an item: 8 up to 8 rows of a head, else 16, which share the unpacking.  16
+// sequences of 6600 tokens, 16 rows: 56.8 us, as two items of 8 59.0; 64 rows: 158 and
+// 200; one such sequence alone, which does not fill the device: 20.1 and 15.0.  The
+// kernels of 16 rows with heads of 128 and 256 spill (184 and 188 bytes stored).
 #include "kv4.cuh"
 
 namespace fp8bq {
@@ -104,9 +107,8 @@ struct Bars {
 // what an item costs besides (its queries, the join of the warps' sums).  first[b]
 // counts those of one item of each sequence before b.  Every group takes an equal run
 // of the whole list (the first `more` of them one slot more), so that ragged batches
-// fill the device evenly (64 sequences of 512 to 8192 tokens, 64 heads over 8: 64 us
-// with no slots for the joins, 58.1, 56.0 and 56.7 with one, two and three).
-// (Measured with three CTAs an SM and no least number of slots.)
+// fill the device evenly (64 sequences of 512 to 8192 tokens, 64 heads over 8: 61.5 us
+// with no slots for the joins, 56.7, 55.2, 55.5 and 57.0 with one to four).
 constexpr int kJoinSlots = 2;
 struct Plan {
   const int *first;  // [B + 1]
@@ -116,9 +118,9 @@ struct Plan {
     const int total = f[B_] * items_;
     // fewer groups than there are take part where there are few slots: at least `least`
     // each, since a part costs as much as a tile to add to the others'.  With 8 rows an
-    // item two (one sequence of 8192 tokens, 64 heads over 8: 22.3, 17.3, 16.7 and 18.7 us
-    // with 1, 2, 4 and 6; of 701: 10.4, 10.4, 11.7 and 14.2), with 16, whose parts are
-    // twice as large, three (two of 6600, four tokens each, 32 heads: 23.5 with 2, 21.9)
+    // item two (one sequence of 8192 tokens, 64 heads over 8: 18.0, 14.1, 14.2 and 13.4 us
+    // with 1 to 4; of 701: 10.2, 10.1, 10.6 and 11.2), with 16, whose parts are twice as
+    // large, three (two of 6600, four tokens each, 32 heads: 26.4, 24.1, 22.5 and 23.3)
     const int active = min((max(total, 1) + least - 1) / least, most);
     each = total / active;
     more = total - each * active;

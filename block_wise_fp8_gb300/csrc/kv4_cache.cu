@@ -8,8 +8,8 @@
 // makes the scale NaN, so that it stays visible.
 //
 // Measured (8 heads of 128): 8192 tokens written and read back 23.1 us, over 12.8 at the
-// copy rate; 32 sequences of up to 16384 tokens cut to 4096 by weight 192 us with the
-// read-back of what is kept, over 117.
+// copy rate; 32 sequences of up to 16384 tokens cut to 4096 by weight 192 us, of which the
+// choice is 25, the move 46 and the read-back of what is kept the rest, over 117 in all.
 #include "kv4.cuh"
 
 namespace fp8bq {
@@ -36,13 +36,16 @@ __device__ __forceinline__ Slot slot_of(const void *slots, int is64, int64_t t, 
 
 // ---------------------------------------------------------------- append and read
 //
-// Both are bound by HBM: 4D bytes of rows and 9D/8 of a page a token and head.  A
-// thread has 8 values (half a group): rows, codes and scales are then whole runs of a
-// warp's lanes (with whole groups a thread 8192 tokens x 8 heads x 128 took 15 us to
-// write and 12 to read, cold), and several tokens, whose loads are in flight together:
-// 8192 tokens written and read back take 23.7, 24.0 and 24.8 us with 2, 3 and 4 to write
-// (28.9 with 1 of each), 24.4 with 2 to read; 700000 rows read 210 and 198 with 2 and 4,
-// 250 with 8 (with what goes before).  The quotients two at a time: 24.6 -> 23.7.
+// 4D bytes of rows and 9D/8 of a page a token and head.  HBM would be the floor; each of a
+// token's D/4 threads looks its slot up and works its address out, so that a write, with
+// the quotients, is bound by the ALU (73 %, issue slots 81 %) and a read by issue (67 %, at
+// half the copy rate): 16.8 and 12.0 us cold for 8192 tokens x 8 heads x 128.  A thread
+// has 8 values (half a group), so that rows, codes and scales are whole runs of a warp's
+// lanes, and several tokens, whose loads are in flight together: 8192 tokens written and
+// read back take 23.7, 24.0 and 24.8 us with 2, 3 and 4 to write (28.9 with 1 of each; whole
+// groups a thread, one token of each: 24.8), 24.4 with 2 to read; 700000 rows read 210 and
+// 198 with 2 and 4, 250 with 8 (with what goes before).  The quotients two at a time: 24.6
+// -> 23.7.
 constexpr int kAppendTokens = 2, kReadTokens = 4;
 
 template <int D, int kRowTokens>

@@ -13,19 +13,21 @@
 //   P = exp2(S - max), BF16, written over S's own columns
 //   O += P V     P from TMEM, V as TMA left it (N-major), O in TMEM
 // The two row tiles alternate: while the tensor cores work for one, the other's
-// four warps (a thread a row) compute its P.  TMEM is full: 2 x (128 S + 128 O).
+// four warps (a thread a row) compute its P.  TMEM holds 2 x (128 S + 128 O) columns,
+// which is all of it (with heads up to 64, whose O has 64, 128 stay idle).
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its last
 // reference (p <= 2^8 until then; the row's sum is held to the same reference).
 // P is rounded to BF16 (half a step, 2^-8 of a p): kind::f16 takes both operands in
 // one type, and V is BF16.
 //
-// Measured: 16384 tokens, 32 heads over 4 of 128: 1.27 ms, 1.73 PFLOP/s of what the
-// causal triangle needs, 0.88 of cuBLAS's BF16 rate (in a stream of such calls 1.34 ms,
-// at the power cap, where cuBLAS has 1.74 PFLOP/s).  A pair of steps takes 2630 cycles,
-// of which the tensor cores' 2150: a tile's chain is 1200 for its softmax, 150 until its
-// products begin and 1280 until the next scores are there.  A unit's end costs some 4000
-// more: nine ragged prompts of 4099 tokens together, 64 heads over 8, take 74 us, 0.46 of
-// that rate.  CTA pairs sharing K and V (cta_group::2) gained 2 % and are left out.
+// Measured: 16384 tokens, 32 heads over 4 of 128: 1.22 to 1.35 ms, with the power cap (all
+// at the cap: 1.63 PFLOP/s of what the causal triangle needs, where cuBLAS has 1.74).  A
+// pair of steps takes 2630 cycles, of which the tensor cores' 2150: a tile's chain is 1200
+// for its softmax, 150 until its products begin and 1280 until the next scores are there.
+// A unit's end costs some 4000 more, and 12 to 19 % of the tensor work of short prompts goes
+// to pairs of a unit's last tiles that the mask hides: nine ragged prompts of 4099 tokens
+// together, 64 heads over 8, take 72.5 us, 0.48 of cuBLAS's rate.  CTA pairs sharing K and V
+// (cta_group::2) gained 2 % and are left out.
 #include "common.cuh"
 #include "ptx.cuh"
 

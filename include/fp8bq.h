@@ -561,7 +561,9 @@ FP8BQ_API size_t fp8bq_moe_workspace_bytes(int64_t M, int64_t E, int64_t H, int6
  * of heads are BF16, value d of head h of token t at [t * ts + h * hs + d], with
  * pointers 16-byte aligned and strides multiples of 8 (ERR_ALIGN).  scale (the
  * softmax's, 1/sqrt(D) as a rule), k_scale and v_scale are positive and finite
- * (ERR_SHAPE). */
+ * (ERR_SHAPE).  Prompts take heads of 16 to 128 (multiples of 16), the cache heads of 64,
+ * 128 and 256: both have 64 and 128.  A prompt's attention starts with its first row:
+ * none goes on behind a cached prefix. */
 
 /* Causal attention over whole prompts, S sequences packed one after the other:
  * rows offsets[s] .. offsets[s+1]-1 belong to sequence s, and for its token i
@@ -616,9 +618,9 @@ FP8BQ_API int fp8bq_kv4_append(const void *k, int64_t k_ts, int64_t k_hs, const 
                                float k_scale, float v_scale, int64_t T, int64_t HK, int64_t D,
                                void *stream);
 
-/* Reads slots back into rows [T, HK, D] (what a prompt behind a cached prefix starts
- * with), exact up to one BF16 rounding of the product with k_scale or v_scale (none
- * for powers of two); rows of slots outside the cache are left as they are. */
+/* Reads slots back into rows [T, HK, D], exact up to one BF16 rounding of the product
+ * with k_scale or v_scale (none for powers of two); rows of slots outside the cache are
+ * left as they are.  k and v do not overlap. */
 FP8BQ_API int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, const void *slots,
                              int slot_bits, float k_scale, float v_scale, void *k, int64_t k_ts,
                              int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, int64_t T,
@@ -640,7 +642,9 @@ FP8BQ_API int fp8bq_kv4_read(const void *cache, int64_t pages, int64_t page, con
  * blocks of 64 tokens <= 2^30 (ERR_SHAPE).
  * Workspace: fp8bq_kv4_workspace_bytes(B, Tq, HQ, HK, D, width * page, weights !=
  * NULL), zeroed once; one that is large enough serves calls of any sizes, of this
- * function alone.  One launch, two with weights. */
+ * function alone.  With weights it holds B * Tq * HQ * width * page scores in FP32, by
+ * the tables' width and not by the lengths: narrow tables save memory and time then.
+ * One launch, two with weights. */
 FP8BQ_API int fp8bq_kv4_attention(const void *q, int64_t q_ts, int64_t q_hs, const void *cache,
                                   int64_t pages, int64_t page, const int32_t *table, int64_t width,
                                   const int32_t *lens, float scale, float k_scale, float v_scale,
