@@ -559,6 +559,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap qm, const __grid_con
           *y = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
+      __syncwarp();  // (every lane is done with the marks)
       if (lane == 0) mbar_arrive(&sh.u_empty[k & 1]);
     }
   } else {

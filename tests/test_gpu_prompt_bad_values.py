@@ -79,3 +79,32 @@ def test_time_with_bad_values(T, HQ, HK, D):
     assert fb.fp8bq_poll_status(ws) == 0
     print(f"{plain * 1e3:.1f} us; one NaN {one * 1e3:.1f}, infinite {infinite * 1e3:.1f}, NaN {full * 1e3:.1f}")
     assert one < 4 * plain and full < 12 * plain and infinite < 60 * plain
+
+
+def test_marks_of_one_unit_and_the_next():
+    """Many units a CTA, a few of them with values that are not finite, far apart in time for
+    the rows of a warp (some have none to take up, some 256): nothing is lost or left behind."""
+    HQ, HK, D = 24, 24, 64
+    g = torch.Generator("cuda").manual_seed(4)
+    T = 1500
+    q, k, v = packed(g, T, HQ, HK, D)
+    bounds = [0, 700, 701, 1100, T]
+    bad = v.clone()
+    for i in range(60):
+        t, h = (i * 97 + 11) % T, i % HK
+        bad[t, h, (5 * i) % D:] = math.inf
+        bad[t, h, :(3 * i) % 9] = math.nan
+    off = torch.tensor(bounds, dtype=I32, device="cuda")
+    ws = fb.new_workspace(fb.OP_PROMPT_ATTENTION, T, HQ, D)
+    want, bound = reference(q, k, torch.where(bad.isfinite(), v, 0.0), bounds, D ** -0.5)
+
+    def seen(x):
+        return torch.cat([x[a:b].long().cummax(0).values for a, b in zip(bounds, bounds[1:])]).bool()
+
+    nan, inf = seen(bad.isnan()), seen(bad == math.inf)
+    for _ in range(20):
+        y = torch.empty_like(want, dtype=BF16)
+        fb.fp8bq_prompt_attention(q, k, bad, off, y, ws)
+        y = y.double()
+        assert bool(y[nan].isnan().all()) and bool((y[inf & ~nan] == math.inf).all())
+        check(y[~(nan | inf)], want[~(nan | inf)], bound[~(nan | inf)])
