@@ -209,9 +209,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // m = n - recent weights: their smallest key by a radix selection (11 + 11 + 10
 // bits), of the keys equal to it the first ones.  A warp then has a run of the
 // tokens of its own, so that one exchange between the warps numbers them all in
-// order.  (Every token has its page, as the interface asks; one without counts as a NaN
-// weight would, so that nothing is read out of range.)  Latency of one CTA: a gather of n weights, three counts, two walks (2203
-// tokens: 18 us with one warp looking for the bin, 64 bins a lane).
+// order.  (Every token has its page, as the interface asks; one without counts as a
+// NaN weight would, so that nothing is read out of range.)  Latency of one CTA: a
+// gather of n weights, three counts, two walks (2203 tokens: 18 us with one warp
+// looking for the bin, 64 bins a lane).
 __global__ void __launch_bounds__(kChooseThreads) kv4_choose_kernel(const Kv4EvictArgs a) {
   extern __shared__ uint32_t keys[];
   __shared__ uint32_t bins[kBinCopies][kBins];

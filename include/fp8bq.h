@@ -560,8 +560,8 @@ FP8BQ_API size_t fp8bq_moe_workspace_bytes(int64_t M, int64_t E, int64_t H, int6
  * belongs to key/value head h / (HQ / HK); HQ is a multiple of HK.  All tensors
  * of heads are BF16, value d of head h of token t at [t * ts + h * hs + d], with
  * pointers 16-byte aligned and strides multiples of 8 (ERR_ALIGN).  scale (the
- * softmax's, 1/sqrt(D) as a rule), k_scale and v_scale are positive and finite
- * (ERR_SHAPE).  Prompts take heads of 16 to 128 (multiples of 16), the cache heads of 64,
+ * softmax's, 1/sqrt(D) as a rule), k_scale and v_scale are positive and finite, and so
+ * is scale * k_scale * log2(e) (ERR_SHAPE).  Prompts take heads of 16 to 128 (multiples of 16), the cache heads of 64,
  * 128 and 256: both have 64 and 128.  A prompt's attention starts with its first row:
  * none goes on behind a cached prefix. */
 
